@@ -1,5 +1,5 @@
 /*
- * focus.h - C ABI of the Focus centroid-gated sparse attention forward pass
+ * focus.h - C ABI of the Focus centroid-gated sparse attention library
  *           (libfocus.so, sm_103a).
  *
  * The method: "Why Attend to Everything? Focus is the Key" (Yao, Chen et al.).
@@ -316,6 +316,157 @@ int focus_attn_bwd_ev(const focus_params* p, const uint16_t* q, const uint16_t* 
                       const uint16_t* v, const uint32_t* mask, const uint16_t* o, const float* lse,
                       const uint16_t* d_o, uint16_t* dq, uint16_t* dk, uint16_t* dv, void* ws,
                       size_t ws_bytes, void* stream, void* const* stage_events);
+
+/*
+ * Rotary positions.  Pair i of a head (i < dim / 2) is turned by the angle
+ * pos * f_i and multiplied by attn_factor:
+ *   a' = g (a cos(pos f_i) - b sin(pos f_i)),   b' = g (b cos(pos f_i) + a sin(pos f_i))
+ * where (a, b) are columns (i, i + dim / 2) (FOCUS_ROPE_HALF) or (2i, 2i + 1)
+ * (FOCUS_ROPE_INTERLEAVED); columns from dim on are copied unchanged.
+ * f_i = base^(-2i / dim), and for contexts longer than a model was trained on:
+ *   LINEAR    f_i / factor
+ *   NTK       base * factor^(dim / max(dim - 2, 1)) in place of base
+ *   BY_PARTS  f_i (1 - keep) / factor + f_i keep with keep = clamp((orig_len f_i / 2 pi -
+ *             beta_slow) / (beta_fast - beta_slow), 0, 1): pairs that turn often inside
+ *             the original context stay, slow ones are stretched
+ * The angle is exact for every 32-bit position: the plan holds f_i as a 64-bit
+ * fraction of a turn, and pos * f_i modulo one turn is a 64-bit integer product.
+ */
+enum focus_rope_layout { FOCUS_ROPE_HALF = 0, FOCUS_ROPE_INTERLEAVED = 1 };
+enum focus_rope_scaling {
+  FOCUS_ROPE_SCALING_NONE = 0,
+  FOCUS_ROPE_SCALING_LINEAR = 1,
+  FOCUS_ROPE_SCALING_NTK = 2,
+  FOCUS_ROPE_SCALING_BY_PARTS = 3
+};
+enum focus_dtype { FOCUS_DTYPE_BF16 = 0, FOCUS_DTYPE_F16 = 1, FOCUS_DTYPE_F32 = 2 };
+
+typedef struct focus_rope_params {
+  int32_t dim;        /* rotated columns of a head: even, 2 <= dim <= 128 */
+  int32_t layout;     /* enum focus_rope_layout */
+  int32_t scaling;    /* enum focus_rope_scaling */
+  int32_t orig_len;   /* BY_PARTS: tokens of the original context, >= 1 */
+  double base;        /* >= 1 (10000 typical) */
+  double factor;      /* >= 1; not used with NONE */
+  double beta_fast;   /* BY_PARTS: turns from which a pair is kept, > beta_slow */
+  double beta_slow;   /* BY_PARTS: turns up to which a pair is stretched, >= 0 */
+  double attn_factor; /* g; <= 0 selects 1, or 0.1 ln(factor) + 1 with BY_PARTS */
+} focus_rope_params;
+
+/* The plan a caller keeps (host memory, no device state): made once by
+ * focus_rope_init, passed to every call. */
+typedef struct focus_rope {
+  int32_t dim, layout;
+  float attn_factor;
+  int32_t reserved;
+  uint64_t turn[64]; /* f_i / 2 pi as a fraction of 2^64 */
+} focus_rope;
+int focus_rope_init(const focus_rope_params* params, focus_rope* rope);
+
+/* Element strides of a [batch, token, head, column] tensor whose columns are
+ * consecutive.  A NULL pointer in a call means the dense layout. */
+typedef struct focus_strides {
+  int64_t b, n, h;
+} focus_strides;
+
+/*
+ * Rotate queries and keys (one launch).
+ *   q   [B, N, H, d_head], k [B, N, H_kv, d_head] of `dtype`; k may be NULL (then
+ *       H_kv, ks, k_out, kos are ignored); d_head 64 or 128, dim <= d_head
+ *   positions  [B, N] int32 (any value, negative ones too) or NULL: token n stands at
+ *       offset + n (offset is not used when positions are given)
+ *   inverse    0: forward.  1: the backward pass: q and k hold the gradients with
+ *       respect to the rotated tensors, and the outputs are those with respect to the
+ *       inputs (the rotation by -pos f_i, times attn_factor)
+ *   q_out, k_out  outputs; each may be its own input (same pointer, same strides) and
+ *       overlaps nothing else
+ * Pointers are aligned to the element size; 16-byte aligned pointers and strides that
+ * are multiples of 16 bytes take the vector path.  Computed in fp32, rounded once.
+ */
+int focus_rope_apply(const focus_rope* rope, int32_t dtype, int32_t B, int32_t N, int32_t H,
+                     int32_t H_kv, int32_t d_head, const void* q, const focus_strides* qs,
+                     const void* k, const focus_strides* ks, const int32_t* positions,
+                     int64_t offset, int32_t inverse, void* q_out, const focus_strides* qos,
+                     void* k_out, const focus_strides* kos, void* stream);
+
+/*
+ * Key/value cache of sequences that grow: B sequences of `cap` token slots.
+ *   k_cache, v_cache  [B, cap, H_kv, d_head] in the format
+ *   k_scale, v_scale  [B, H_kv, cap] fp32, the 8-bit formats only (NULL for BF16)
+ *   mask_cache        [B, R, cap] uint32 group bitmasks (e.g. from focus_route)
+ * 8-bit formats: a row (one token, one head, d_head values) is held as codes c_i with
+ * one scale: x_i ~ c_i * scale, scale = max|x| / M, c_i = round(x_i * (M / max|x|)),
+ * M = 448 (E4M3: 4 exponent and 3 mantissa bits, ties to even) or 127 (INT8).  A row
+ * with max|x| < 2^-100 is held as zeros with scale 0; a row with a NaN or an infinity
+ * as zeros with a NaN scale (it reads back as NaN).
+ */
+enum focus_cache_format { FOCUS_CACHE_BF16 = 0, FOCUS_CACHE_E4M3 = 1, FOCUS_CACHE_INT8 = 2 };
+#define FOCUS_MAX_DRAFT 64 /* tokens of one focus_decode_tree call */
+
+typedef struct focus_cache_params {
+  int32_t B, cap;                /* sequences; token slots of each (B * cap * H_kv < 2^40, cap <= 2^30) */
+  int32_t T;                     /* tokens per sequence of this call */
+  int32_t H, H_kv, d_head, R;    /* as in focus_params; d_head in {64, 128} */
+  int32_t K, top_k, w;           /* groups per token (balances the work of decode_tree) and window */
+  int32_t format;                /* enum focus_cache_format */
+  float softmax_scale;           /* <= 0 selects 1 / sqrt(d_head) */
+} focus_cache_params;
+
+/*
+ * Append tokens: token t < count[b] of sequence b goes to slot start[b] + t, its key
+ * rotated on the way when a rope is given.
+ *   k, v       [B, T, H_kv, d_head] bf16 with strides ks, vs (16-byte aligned rows)
+ *   mask       [B, R, T] uint32 or NULL (then mask_cache is not written)
+ *   start      [B] int32;  count [B] int32 or NULL (all T tokens)
+ *   rope       NULL or a plan with dim <= d_head; positions [B, T] int32 or NULL: the
+ *              key stands at its slot, start[b] + t
+ *   status     NULL or a device int32 that the caller zeroed: set to FOCUS_ERR_BOUNDS
+ *              when a token's slot lies outside [0, cap) or a count outside [0, T]
+ *              (focus_get_status reads it); such tokens are not written
+ * Every other slot keeps its contents.  Rotation, maximum and quotient in fp32.
+ */
+int focus_cache_write(const focus_cache_params* p, const uint16_t* k, const focus_strides* ks,
+                      const uint16_t* v, const focus_strides* vs, const uint32_t* mask,
+                      const int32_t* start, const int32_t* count, const focus_rope* rope,
+                      const int32_t* positions, void* k_cache, void* v_cache, float* k_scale,
+                      float* v_scale, uint32_t* mask_cache, int32_t* status, void* stream);
+
+/*
+ * Read tokens back as bf16 (e.g. the prefix of a further prompt for focus_attn_fwd):
+ * k, v [B, T, H_kv, d_head] out, token t from slot start[b] + t (start NULL: 0); tokens
+ * from count[b] on (count NULL: none) are zeros, and so are tokens outside the cache,
+ * which set `status` as in focus_cache_write.
+ */
+int focus_cache_read(const focus_cache_params* p, const void* k_cache, const void* v_cache,
+                     const float* k_scale, const float* v_scale, const int32_t* start,
+                     const int32_t* count, uint16_t* k, uint16_t* v, int32_t* status, void* stream);
+
+/*
+ * Decode step for T <= FOCUS_MAX_DRAFT drafted tokens per sequence over a cache in any
+ * format (T = 1: the next token of sequences of different lengths).  Sequence b holds
+ * lens[b] tokens in slots 0 .. lens[b] - 1; its drafted tokens' keys, values and masks
+ * stand in slots lens[b] + u (focus_cache_write puts them there, with
+ * positions lens[b] + depth when they form a tree).
+ *   q     [B, T, H, d_head] bf16;  lens [B] int32
+ *   tree  [B, T] uint64 or NULL: bit u of tree[b][t] is set when drafted token u is an
+ *         ancestor of t or t itself (bits from T on are ignored); NULL: a chain (u <= t).
+ *         The token's depth is the number of its set bits less one, its position
+ *         i = lens[b] + depth.  A word without bits marks a row that is no token.
+ * Token t attends to the cached j < lens[b] and the drafted u of its word (at position
+ * j = lens[b] + depth of u) with i - j < w or mask_t & mask_j != 0, in one softmax.
+ *   o     [B, T, H, d_head] bf16 out;  lse [B, H, T] fp32 out or NULL.  A row that sees
+ *         nothing gets zeros and -inf.
+ * A NaN or an infinity in a row's own keys and values shows in that row's result, in
+ * keys it does not see in no result.  A sequence with lens[b] outside [0, cap - T]
+ * raises FOCUS_ERR_BOUNDS in the workspace's status word (focus_get_status); its rows
+ * get zeros and -inf, and nothing of it is read.
+ *   ws    focus_decode_tree_workspace_size(p) bytes, 256-byte aligned
+ */
+size_t focus_decode_tree_workspace_size(const focus_cache_params* p);
+int focus_decode_tree(const focus_cache_params* p, const uint16_t* q, const void* k_cache,
+                      const void* v_cache, const float* k_scale, const float* v_scale,
+                      const uint32_t* mask_cache, const int32_t* lens, const uint64_t* tree,
+                      uint16_t* o, float* lse, void* ws, size_t ws_bytes, void* stream);
 
 /*
  * Diagnostic of the device-side failure path (no counterpart in the paper): runs

@@ -1,6 +1,7 @@
 """Focus centroid-gated sparse attention for GB300 (sm_103a): routing, the forward
 pass (exact-set segments or group lists), decode, and the backward pass with the
-group masks held fixed.
+group masks held fixed; rotary positions, and a key/value cache in bf16 or 8 bits with
+the decode step of one or many drafted tokens over it.
 
 Thin ctypes binding over the C ABI in ``include/focus.h`` (``libfocus.so``, built
 in-tree by ``learned_centroid_gated_gb300.build``). This module only marshals
@@ -15,6 +16,7 @@ from __future__ import annotations
 
 import ctypes
 import dataclasses
+import functools
 import math
 import os
 import re
@@ -425,6 +427,329 @@ def attn_bwd(p: Params, q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, mask:
         evs = (ctypes.c_void_p * N_BWD_STAGE_EVENTS)(*[e.cuda_event for e in stage_events])
         _check(_lib.focus_attn_bwd_ev(*args, evs), "focus_attn_bwd_ev")
     return dq, dk, dv
+
+
+# ---------------------------------------------------------------- rotary positions ----
+class _RopeParams(ctypes.Structure):
+    _fields_ = [("dim", ctypes.c_int32), ("layout", ctypes.c_int32), ("scaling", ctypes.c_int32),
+                ("orig_len", ctypes.c_int32), ("base", ctypes.c_double), ("factor", ctypes.c_double),
+                ("beta_fast", ctypes.c_double), ("beta_slow", ctypes.c_double),
+                ("attn_factor", ctypes.c_double)]
+
+
+class _RopePlan(ctypes.Structure):
+    _fields_ = [("dim", ctypes.c_int32), ("layout", ctypes.c_int32), ("attn_factor", ctypes.c_float),
+                ("reserved", ctypes.c_int32), ("turn", ctypes.c_uint64 * 64)]
+
+
+class _Strides(ctypes.Structure):
+    _fields_ = [("b", ctypes.c_int64), ("n", ctypes.c_int64), ("h", ctypes.c_int64)]
+
+
+class _CacheParams(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int32) for n in ("B", "cap", "T", "H", "H_kv", "d_head", "R", "K", "top_k", "w",
+                                              "format")] + [("softmax_scale", ctypes.c_float)]
+
+
+_I32, _I64 = ctypes.c_int32, ctypes.c_int64
+_lib.focus_rope_init.argtypes = [_P, _P]
+_lib.focus_rope_init.restype = ctypes.c_int
+_lib.focus_rope_apply.argtypes = [_P, _I32, _I32, _I32, _I32, _I32, _I32, _P, _P, _P, _P, _P, _I64, _I32,
+                                  _P, _P, _P, _P, _P]
+_lib.focus_rope_apply.restype = ctypes.c_int
+_lib.focus_cache_write.argtypes = [_P] * 17
+_lib.focus_cache_write.restype = ctypes.c_int
+_lib.focus_cache_read.argtypes = [_P] * 11
+_lib.focus_cache_read.restype = ctypes.c_int
+_lib.focus_decode_tree_workspace_size.argtypes = [_P]
+_lib.focus_decode_tree_workspace_size.restype = ctypes.c_size_t
+_lib.focus_decode_tree.argtypes = [_P] * 12 + [ctypes.c_size_t, _P]
+_lib.focus_decode_tree.restype = ctypes.c_int
+
+ROPE_LAYOUTS = {"half": 0, "interleaved": 1}
+ROPE_SCALINGS = {"none": 0, "linear": 1, "ntk": 2, "by_parts": 3}
+_ROPE_DTYPES = {torch.bfloat16: 0, torch.float16: 1, torch.float32: 2}
+CACHE_FORMATS = {"bf16": 0, "e4m3": 1, "int8": 2}
+_CACHE_DTYPES = {"bf16": torch.bfloat16, "e4m3": torch.float8_e4m3fn, "int8": torch.int8}
+MAX_DRAFT = 64
+
+
+def _require(ok, what: str):
+    """An argument that the C ABI cannot see to be wrong (a tensor's shape, type or device)."""
+    if not ok:
+        raise FocusError(-1, what)
+
+
+@dataclasses.dataclass(frozen=True)
+class Rope:
+    """Rotary positions (focus_rope_params): dim rotated columns of each head, pairs
+    (i, i + dim / 2) ("half") or (2i, 2i + 1) ("interleaved"); scaling "none", "linear",
+    "ntk" or "by_parts" stretches the positions by `factor` (by_parts: beyond orig_len
+    tokens; attn_factor 0 selects 0.1 ln(factor) + 1 there, else 1).  Made once and kept:
+    it holds the plan (focus_rope) that every call passes."""
+    dim: int
+    layout: str = "half"
+    base: float = 10000.0
+    scaling: str = "none"
+    factor: float = 1.0
+    orig_len: int = 4096
+    beta_fast: float = 32.0
+    beta_slow: float = 1.0
+    attn_factor: float = 0.0
+
+    def __post_init__(self):
+        _require(self.layout in ROPE_LAYOUTS and self.scaling in ROPE_SCALINGS, "focus_rope_init")
+        plan = _RopePlan()
+        params = _RopeParams(self.dim, ROPE_LAYOUTS[self.layout], ROPE_SCALINGS[self.scaling], self.orig_len,
+                             self.base, self.factor, self.beta_fast, self.beta_slow, self.attn_factor)
+        _check(_lib.focus_rope_init(ctypes.byref(params), ctypes.byref(plan)), "focus_rope_init")
+        object.__setattr__(self, "_plan", plan)
+        object.__setattr__(self, "_addr", ctypes.addressof(plan))
+
+
+def _strides_of(t: torch.Tensor):
+    """focus_strides of a [B, N, H, d] tensor, None where it is dense."""
+    if t.is_contiguous():
+        return None
+    return ctypes.byref(_Strides(t.stride(0), t.stride(1), t.stride(2)))
+
+
+def _on(t: torch.Tensor, stream):
+    """The raw stream to launch on for tensor t: `stream`, or the current one of t's device."""
+    if stream is None:
+        return torch.cuda.current_stream(t.device).cuda_stream
+    return stream.cuda_stream
+
+
+class _Launch:
+    """Makes the device of a call's tensors current, and the stream that it runs on, so
+    that what is allocated meanwhile belongs to that stream."""
+
+    def __init__(self, t: torch.Tensor, stream):
+        here = torch.cuda.current_device() == t.device.index
+        self.device = None if here else torch.cuda.device(t.device)
+        self.stream = None if stream is None else torch.cuda.stream(stream)
+
+    def __enter__(self):
+        if self.device is not None:
+            self.device.__enter__()
+        if self.stream is not None:
+            self.stream.__enter__()
+
+    def __exit__(self, *exc):
+        if self.stream is not None:
+            self.stream.__exit__(*exc)
+        if self.device is not None:
+            self.device.__exit__(*exc)
+
+
+def _rope_call(what, rope_plan, q, k, positions, offset, out, out_k, inverse, stream):
+    _require(q.is_cuda and q.dim() == 4 and q.dtype in _ROPE_DTYPES and q.stride(3) == 1, what)
+    B, N, H, d = q.shape
+    H_kv = 0
+    if k is not None:
+        _require(k.device == q.device and k.dtype == q.dtype and k.dim() == 4 and k.stride(3) == 1 and
+                 k.shape[0] == B and k.shape[1] == N and k.shape[3] == d, what)
+        H_kv = k.shape[2]
+    if positions is not None:
+        _require(positions.device == q.device and positions.dtype == torch.int32 and
+                 positions.shape == (B, N) and positions.is_contiguous(), what)
+    with _Launch(q, stream):
+        if out is None:
+            out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+        if k is not None and out_k is None:
+            out_k = torch.empty(k.shape, dtype=k.dtype, device=k.device)
+        for x, y in ((q, out), (k, out_k)):
+            _require(x is None or (y.shape == x.shape and y.dtype == x.dtype and y.device == x.device and
+                                   y.stride(3) == 1), what)
+        if q.numel() and (k is None or k.numel()):
+            _check(_lib.focus_rope_apply(
+                rope_plan._addr, _ROPE_DTYPES[q.dtype], B, N, H, H_kv, d, q.data_ptr(), _strides_of(q),
+                None if k is None else k.data_ptr(), None if k is None else _strides_of(k),
+                None if positions is None else positions.data_ptr(), offset, inverse,
+                out.data_ptr(), _strides_of(out), None if k is None else out_k.data_ptr(),
+                None if k is None else _strides_of(out_k), _on(q, stream)), what)
+    return out if k is None else (out, out_k)
+
+
+def rope(plan: Rope, q: torch.Tensor, k: torch.Tensor | None = None, *, positions=None, offset: int = 0,
+         out=None, out_k=None, stream=None):
+    """Rotary positions of q [B, N, H, d] and, in the same launch, k [B, N, H_kv, d] (bf16,
+    fp16 or fp32; strided views with consecutive columns are fine).  Token n stands at
+    offset + n, or at positions[b, n] (int32).  out / out_k may be q / k themselves.
+    Returns the rotated q, or (q, k)."""
+    return _rope_call("focus_rope_apply", plan, q, k, positions, offset, out, out_k, 0, stream)
+
+
+def rope_bwd(plan: Rope, dq: torch.Tensor, dk: torch.Tensor | None = None, *, positions=None, offset: int = 0,
+             out=None, out_k=None, stream=None):
+    """Backward of rope(): gradients of its inputs from those of its outputs (e.g. from
+    attn_bwd), with the forward's plan and positions."""
+    return _rope_call("focus_rope_apply", plan, dq, dk, positions, offset, out, out_k, 1, stream)
+
+
+# ------------------------------------------------------------------ key/value cache ----
+@dataclasses.dataclass(frozen=True)
+class CacheParams:
+    """A key/value cache and the attention over it (focus_cache_params): B sequences of
+    `cap` token slots, format "bf16", "e4m3" or "int8".  K, top_k: groups and groups per
+    token, as routed (they balance the work of decode_tree)."""
+    B: int
+    cap: int
+    H: int
+    H_kv: int
+    d_head: int
+    R: int
+    K: int
+    top_k: int
+    w: int
+    format: str = "bf16"
+    softmax_scale: float = 0.0
+
+    def c(self, T: int) -> _CacheParams:
+        return _cache_params(self, T)
+
+    @property
+    def scale(self) -> float:
+        return self.softmax_scale if self.softmax_scale > 0 else 1.0 / math.sqrt(self.d_head)
+
+
+@functools.lru_cache(maxsize=1024)
+def _cache_params(p: CacheParams, T: int) -> _CacheParams:
+    _require(p.format in CACHE_FORMATS, "focus_cache_params")
+    return _CacheParams(p.B, p.cap, T, p.H, p.H_kv, p.d_head, p.R, p.K, p.top_k, p.w, CACHE_FORMATS[p.format],
+                        p.softmax_scale)
+
+
+@dataclasses.dataclass
+class KVCache:
+    """The tensors of a cache: k, v [B, cap, H_kv, d] (bfloat16, float8_e4m3fn or int8),
+    k_scale, v_scale [B, H_kv, cap] fp32 (None for bf16), mask [B, R, cap] int32."""
+    k: torch.Tensor
+    v: torch.Tensor
+    k_scale: torch.Tensor | None
+    v_scale: torch.Tensor | None
+    mask: torch.Tensor
+
+    @classmethod
+    def empty(cls, p: CacheParams, device="cuda") -> "KVCache":
+        """A cache of zeros."""
+        _require(p.format in CACHE_FORMATS, "focus_cache_params")
+        kv = [torch.zeros(p.B, p.cap, p.H_kv, p.d_head, dtype=torch.uint8 if p.format != "bf16" else torch.bfloat16,
+                          device=device).view(_CACHE_DTYPES[p.format]) for _ in range(2)]
+        sc = [None if p.format == "bf16" else torch.zeros(p.B, p.H_kv, p.cap, device=device) for _ in range(2)]
+        return cls(*kv, *sc, torch.zeros(p.B, p.R, p.cap, dtype=torch.int32, device=device))
+
+    def _args(self, p: CacheParams, what: str):
+        k = self.k
+        shape, dtype, dev = (p.B, p.cap, p.H_kv, p.d_head), _CACHE_DTYPES.get(p.format), k.device
+        _require(k.is_cuda and self.mask.device == dev and self.mask.dtype == torch.int32 and
+                 self.mask.shape == (p.B, p.R, p.cap) and self.mask.is_contiguous(), what)
+        for x in (k, self.v):
+            _require(x.device == dev and x.dtype == dtype and x.shape == shape and x.is_contiguous(), what)
+        if p.format == "bf16":
+            _require(self.k_scale is None and self.v_scale is None, what)
+            return k.data_ptr(), self.v.data_ptr(), None, None
+        for x in (self.k_scale, self.v_scale):
+            _require(x is not None and x.device == dev and x.dtype == torch.float32 and
+                     x.shape == (p.B, p.H_kv, p.cap) and x.is_contiguous(), what)
+        return k.data_ptr(), self.v.data_ptr(), self.k_scale.data_ptr(), self.v_scale.data_ptr()
+
+
+def _vector(t, shape, like: torch.Tensor, what: str, dtype=torch.int32):
+    """The address of an optional dense device tensor of the given shape and type."""
+    if t is None:
+        return None
+    _require(t.device == like.device and t.dtype == dtype and t.shape == shape and t.is_contiguous(), what)
+    return t.data_ptr()
+
+
+def cache_write(p: CacheParams, cache: KVCache, k: torch.Tensor, v: torch.Tensor, mask, start: torch.Tensor,
+                count=None, *, rope: Rope | None = None, positions=None, status=None, stream=None) -> KVCache:
+    """Append tokens to the cache: k, v [B, T, H_kv, d] bf16 (token strides free, 16-byte
+    aligned rows), mask [B, R, T] int32 (e.g. from route) or None to leave the cache's masks;
+    token t < count[b] goes to slot start[b] + t (int32 device tensors; count None: all T),
+    its key rotated by `rope` at positions[b, t], or at its slot.  status: an int32 device
+    word that get_status reads (FOCUS_ERR_BOUNDS when a token had no slot).  A tree's accepted
+    path is committed by writing its tokens again from start on, in order."""
+    what = "focus_cache_write"
+    args = cache._args(p, what)
+    T = k.shape[1] if k.dim() == 4 else 0
+    for x in (k, v):
+        _require(x.device == cache.k.device and x.dtype == torch.bfloat16 and
+                 x.shape == (p.B, T, p.H_kv, p.d_head) and x.stride(3) == 1, what)
+    _require(start is not None, what)
+    if T == 0:
+        return cache
+    with _Launch(k, stream):
+        _check(_lib.focus_cache_write(
+            ctypes.byref(p.c(T)), k.data_ptr(), _strides_of(k), v.data_ptr(), _strides_of(v),
+            _vector(mask, (p.B, p.R, T), k, what), _vector(start, (p.B,), k, what), _vector(count, (p.B,), k, what),
+            None if rope is None else rope._addr, _vector(positions, (p.B, T), k, what), *args,
+            cache.mask.data_ptr(), _vector(status, (1,), k, what), _on(k, stream)), what)
+    return cache
+
+
+def cache_read(p: CacheParams, cache: KVCache, T: int, start=None, count=None, *, out=None, status=None,
+               stream=None):
+    """k, v [B, T, H_kv, d] bf16 of the tokens in slots start[b] + t (start None: 0), zeros
+    for t >= count[b]; e.g. the prefix of a further prompt for attn_fwd.  out: (k, v) to fill."""
+    what = "focus_cache_read"
+    args = cache._args(p, what)
+    shape, dev = (p.B, T, p.H_kv, p.d_head), cache.k.device
+    with _Launch(cache.k, stream):
+        if out is None:
+            out = tuple(torch.empty(shape, dtype=torch.bfloat16, device=dev) for _ in range(2))
+        k, v = out
+        for x in (k, v):
+            _require(x.device == dev and x.dtype == torch.bfloat16 and x.shape == shape and x.is_contiguous(), what)
+        if T:
+            _check(_lib.focus_cache_read(
+                ctypes.byref(p.c(T)), *args, _vector(start, (p.B,), k, what), _vector(count, (p.B,), k, what),
+                k.data_ptr(), v.data_ptr(), _vector(status, (1,), k, what), _on(cache.k, stream)), what)
+    return k, v
+
+
+def decode_tree_workspace_size(p: CacheParams, T: int) -> int:
+    return _tree_workspace(p, T)
+
+
+@functools.lru_cache(maxsize=1024)
+def _tree_workspace(p: CacheParams, T: int) -> int:
+    return int(_lib.focus_decode_tree_workspace_size(ctypes.byref(p.c(T))))
+
+
+def decode_tree(p: CacheParams, q: torch.Tensor, cache: KVCache, lens: torch.Tensor, tree=None, *, out=None,
+                lse=None, want_lse: bool = True, ws=None, stream=None):
+    """Decode step for T <= MAX_DRAFT drafted tokens per sequence: q [B, T, H, d] bf16, lens [B]
+    int32 tokens in the cache before them; the drafted tokens' own keys, values and masks stand
+    in slots lens[b] + u.  tree [B, T] int64: bit u of word t set when drafted token u is an
+    ancestor of t or t itself (None: a chain; a word of 0 marks a row that is no token).
+    T = 1 is the plain next token of sequences of different lengths.
+    Returns (o [B, T, H, d] bf16, lse [B, H, T] fp32)."""
+    what = "focus_decode_tree"
+    args = cache._args(p, what)
+    _require(q.device == cache.k.device and q.dtype == torch.bfloat16 and q.dim() == 4 and q.is_contiguous(), what)
+    T = q.shape[1]
+    _require(q.shape == (p.B, T, p.H, p.d_head) and lens is not None, what)
+    with _Launch(q, stream):
+        need = _tree_workspace(p, T)
+        if need == 0:
+            raise FocusError(-2 if T > MAX_DRAFT else -1, "focus_decode_tree_workspace_size")
+        if out is None:
+            out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+        if lse is None and want_lse:
+            lse = torch.empty((p.B, p.H, T), dtype=torch.float32, device=q.device)
+        if ws is None:
+            ws = torch.empty(need, dtype=torch.uint8, device=q.device)
+        _require(out.device == q.device and out.dtype == q.dtype and out.shape == q.shape and out.is_contiguous() and
+                 ws.device == q.device and ws.is_contiguous(), what)
+        _check(_lib.focus_decode_tree(
+            ctypes.byref(p.c(T)), q.data_ptr(), *args, cache.mask.data_ptr(), _vector(lens, (p.B,), q, what),
+            _vector(tree, (p.B, T), q, what, torch.int64), out.data_ptr(),
+            _vector(lse, (p.B, p.H, T), q, what, torch.float32), ws.data_ptr(), ws.numel() * ws.element_size(),
+            _on(q, stream)), what)
+    return out, lse
 
 
 def selftest_timeout(device="cuda", stream=None) -> int:

@@ -1,0 +1,344 @@
+// Key/value cache: tokens written (rotated, quantised, scattered to their slots with
+// their group masks) and read back as bf16.
+//
+// A row is one token's key or value of one head.  8-bit formats hold it as codes with one
+// scale, max|x| / M: c = round(x M / max|x|), x ~ c max|x| / M with M = 448 (e4m3) or 127
+// (int8).  Memory-bound: each bf16 row is read once, its codes written once.  A warp takes
+// one token: a key's cosines and sines are computed once and serve all KV heads, the row
+// maximum is a shuffle over the row's D / 16 lanes, and the codes leave from registers.
+#include <cuda_fp8.h>
+#include <math.h>
+
+#include "rope.cuh"
+
+namespace focus {
+namespace {
+
+constexpr float kTinyRow = 7.888609052210118e-31f;  // 2^-100: below it M / max|x| nears fp32's end
+
+enum RopeMode { kNoRope = 0, kHalf = 1, kInterleaved = 2, kHalfAny = 3 };
+
+struct CacheArgs {
+  focus_rope rope;
+  const uint16_t *k, *v;
+  focus_strides ks, vs;
+  const uint32_t* mask;
+  const int32_t *start, *count, *positions;
+  void *kc, *vc;
+  float *kscale, *vscale;
+  uint32_t* mc;
+  uint16_t *ko, *vo;  // cache_read's outputs
+  int32_t* status;
+  int64_t tokens;     // B * T
+  int T, cap, H_kv, R, splits, per;
+};
+
+// Slot of token t of sequence b; -1 when it is not to be moved.  A slot outside the cache
+// or a count outside [0, T] raises FOCUS_ERR_BOUNDS.
+__device__ __forceinline__ int slot_of(const CacheArgs& a, int b, int t, bool report) {
+  const int64_t first = a.start ? (int64_t)__ldg(a.start + b) : 0;
+  const int n = a.count ? __ldg(a.count + b) : a.T;
+  bool bad = n < 0 || n > a.T;
+  int64_t slot = -1;
+  if (t < n) {
+    slot = first + t;
+    if (slot < 0 || slot >= a.cap) {
+      bad = true;
+      slot = -1;
+    }
+  }
+  if (bad && report && a.status) raise_status(a.status, FOCUS_ERR_BOUNDS);
+  return (int)slot;
+}
+
+template <int FMT>
+__device__ __forceinline__ uint2 encode(const float (&f)[8], float inv) {
+  uint32_t w[2];
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    if constexpr (FMT == FOCUS_CACHE_E4M3) {
+      const float* x = f + 4 * i;
+      const uint32_t lo = __nv_cvt_float2_to_fp8x2(make_float2(x[0] * inv, x[1] * inv), __NV_SATFINITE, __NV_E4M3);
+      const uint32_t hi = __nv_cvt_float2_to_fp8x2(make_float2(x[2] * inv, x[3] * inv), __NV_SATFINITE, __NV_E4M3);
+      w[i] = lo | hi << 16;
+    } else {
+      w[i] = 0;
+#pragma unroll
+      for (int e = 0; e < 4; ++e)
+        w[i] |= ((uint32_t)__float2int_rn(f[4 * i + e] * inv) & 0xffu) << (8 * e);
+    }
+  }
+  return make_uint2(w[0], w[1]);
+}
+
+template <int FMT>
+__device__ __forceinline__ void decode8(const uint2& x, float scale, float (&f)[8]) {
+  const uint32_t w[2] = {x.x, x.y};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const uint32_t h = (w[i >> 1] >> (16 * (i & 1))) & 0xffffu;
+    if constexpr (FMT == FOCUS_CACHE_E4M3) {
+      const __half2_raw r = __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)h, __NV_E4M3);
+      const float2 t = __half22float2(*reinterpret_cast<const __half2*>(&r));
+      f[2 * i] = t.x * scale;
+      f[2 * i + 1] = t.y * scale;
+    } else {
+      f[2 * i] = (float)(int)(int8_t)(h & 0xffu) * scale;
+      f[2 * i + 1] = (float)(int)(int8_t)(h >> 8) * scale;
+    }
+  }
+}
+
+// Lane c of a row's D / 16 lanes holds two 8-element chunks (ca, cb).  With kHalf
+// (dim a multiple of 16) they are the two halves of eight pairs, with kInterleaved each
+// holds four pairs, and with kHalfAny (any other even dim) the partner of each element is
+// read from the row (a cached read: the row's other lanes load it too).
+template <int D, int FMT, int MODE>
+__global__ void __launch_bounds__(256) cache_write(const __grid_constant__ CacheArgs a) {
+  using C = RowChunk<bf16>;
+  constexpr int LPR = D / 16, RPW = 32 / LPR;
+  const int64_t warp = (int64_t)blockIdx.x * (blockDim.x >> 5) + (threadIdx.x >> 5);
+  const int64_t tk = warp / a.splits;
+  if (tk >= a.tokens) return;
+  const int sp = (int)(warp - tk * a.splits);
+  const int lane = threadIdx.x & 31, c = lane % LPR, sub = lane / LPR;
+  const int b = (int)(tk / a.T), t = (int)(tk - (int64_t)b * a.T);
+  const int slot = slot_of(a, b, t, lane == 0);
+  if (slot < 0) return;
+  if (sp == 0 && a.mask)
+    for (int r = lane; r < a.R; r += 32)
+      a.mc[((int64_t)b * a.R + r) * a.cap + slot] = a.mask[((int64_t)b * a.R + r) * a.T + t];
+  const int np = a.rope.dim / 2, P = np / 8;
+  const bool pair = MODE == kHalf && c < P;
+  const int ca = MODE == kHalf && !pair ? 2 * P + 2 * (c - P) : c;
+  const int cb = MODE == kHalf ? (pair ? c + P : ca + 1) : c + LPR;
+  const int i0 = sp * a.per, i1 = min(2 * a.H_kv, i0 + a.per);  // rows: keys, then values
+  constexpr int NA = MODE == kHalfAny ? 16 : 8;
+  float cs[NA], sn[NA];
+  if constexpr (MODE != kNoRope) {
+    if (i0 < a.H_kv) {
+      const int64_t pos = a.positions ? (int64_t)__ldg(a.positions + tk) : (int64_t)slot;
+#pragma unroll
+      for (int e = 0; e < NA; ++e) {
+        int i;
+        if constexpr (MODE == kHalf) i = c * 8 + e;
+        else if constexpr (MODE == kInterleaved) i = (e < 4 ? ca : cb) * 4 + (e & 3);
+        else {
+          const int x = (e < 8 ? ca : cb) * 8 + (e & 7);
+          i = x < np ? x : x < 2 * np ? x - np : np;
+        }
+        cs[e] = 1.0f, sn[e] = 0.0f;
+        if (i < np) rope_angle(pos, a.rope.turn[i], a.rope.attn_factor, cs[e], sn[e]);
+      }
+    }
+  }
+  // Every lane takes part in every pass (the row maximum is a shuffle); rows past the end
+  // are not loaded or stored.
+  for (int p0 = i0; p0 < i1; p0 += RPW) {
+    const int row = p0 + sub;
+    const bool on = row < i1, key = row < a.H_kv;
+    const int h = key ? row : row - a.H_kv;
+    const bf16* x = reinterpret_cast<const bf16*>(key ? a.k : a.v);
+    {
+      const focus_strides& st = key ? a.ks : a.vs;
+      x += b * st.b + t * st.n + h * st.h;
+    }
+    float fa[8], fb[8];
+    uint4 xa = make_uint4(0u, 0u, 0u, 0u), xb = xa;
+    if (on) {
+      xa = __ldg(reinterpret_cast<const uint4*>(x + 8 * ca));
+      xb = __ldg(reinterpret_cast<const uint4*>(x + 8 * cb));
+    }
+    C::unpack(xa, fa);
+    C::unpack(xb, fb);
+    if (MODE != kNoRope && on && key) {
+      if constexpr (MODE == kHalf) {
+        if (pair) {
+#pragma unroll
+          for (int e = 0; e < 8; ++e) rope_turn(fa[e], fb[e], cs[e], sn[e]);
+        }
+      } else if constexpr (MODE == kInterleaved) {
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          if (ca * 4 + e < np) rope_turn(fa[2 * e], fa[2 * e + 1], cs[e], sn[e]);
+          if (cb * 4 + e < np) rope_turn(fb[2 * e], fb[2 * e + 1], cs[4 + e], sn[4 + e]);
+        }
+      } else if constexpr (MODE == kHalfAny) {
+#pragma unroll
+        for (int e = 0; e < 16; ++e) {
+          const int i = (e < 8 ? ca : cb) * 8 + (e & 7);
+          if (i < 2 * np) {
+            float& f = e < 8 ? fa[e & 7] : fb[e & 7];
+            float o = __bfloat162float(x[i < np ? i + np : i - np]);
+            if (i < np) rope_turn(f, o, cs[e], sn[e]);
+            else rope_turn(o, f, cs[e], sn[e]);
+          }
+        }
+      }
+    }
+    char* dst = reinterpret_cast<char*>(key ? a.kc : a.vc);
+    const int64_t at = (((int64_t)b * a.cap + slot) * a.H_kv + h) * D;
+    if constexpr (FMT == FOCUS_CACHE_BF16) {
+      if (on) {
+        *reinterpret_cast<uint4*>(dst + 2 * (at + 8 * ca)) = C::pack(fa);
+        *reinterpret_cast<uint4*>(dst + 2 * (at + 8 * cb)) = C::pack(fb);
+      }
+    } else {
+      constexpr float M = FMT == FOCUS_CACHE_E4M3 ? 448.0f : 127.0f;
+      // the maximum of the magnitudes as bit patterns: a NaN or an infinity wins
+      uint32_t top = 0;
+#pragma unroll
+      for (int e = 0; e < 8; ++e)
+        top = max(top, max(__float_as_uint(fa[e]) & 0x7fffffffu, __float_as_uint(fb[e]) & 0x7fffffffu));
+#pragma unroll
+      for (int o = 1; o < LPR; o <<= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
+      const float mx = __uint_as_float(top);
+      const bool finite = top < 0x7f800000u, some = finite && mx >= kTinyRow;
+      if (on) {
+        const float inv = some ? M / mx : 0.0f;
+        const uint2 zero = make_uint2(0u, 0u);
+        *reinterpret_cast<uint2*>(dst + at + 8 * ca) = some ? encode<FMT>(fa, inv) : zero;
+        *reinterpret_cast<uint2*>(dst + at + 8 * cb) = some ? encode<FMT>(fb, inv) : zero;
+        if (c == 0)
+          (key ? a.kscale : a.vscale)[((int64_t)b * a.H_kv + h) * a.cap + slot] =
+              some ? mx / M : finite ? 0.0f : __uint_as_float(0x7fc00000u);
+      }
+    }
+  }
+}
+
+template <int D, int FMT>
+__global__ void __launch_bounds__(256) cache_read(const __grid_constant__ CacheArgs a) {
+  using C = RowChunk<bf16>;
+  constexpr int LPR = D / 8, RPW = 32 / LPR, U = 4;
+  const int64_t warp = (int64_t)blockIdx.x * (blockDim.x >> 5) + (threadIdx.x >> 5);
+  const int64_t tk = warp / a.splits;
+  if (tk >= a.tokens) return;
+  const int sp = (int)(warp - tk * a.splits);
+  const int lane = threadIdx.x & 31, c = lane % LPR, sub = lane / LPR;
+  const int b = (int)(tk / a.T), t = (int)(tk - (int64_t)b * a.T);
+  const int slot = slot_of(a, b, t, lane == 0);
+  const int i0 = sp * a.per, i1 = min(2 * a.H_kv, i0 + a.per);
+  for (int p0 = i0 + sub; p0 < i1; p0 += U * RPW) {
+    uint4 x[U];
+    float sc[U];
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int row = p0 + u * RPW;
+      x[u] = make_uint4(0u, 0u, 0u, 0u);
+      sc[u] = 0.0f;
+      if (row < i1 && slot >= 0) {
+        const bool key = row < a.H_kv;
+        const int h = key ? row : row - a.H_kv;
+        const char* src = reinterpret_cast<const char*>(key ? a.kc : a.vc);
+        const int64_t at = (((int64_t)b * a.cap + slot) * a.H_kv + h) * D + 8 * c;
+        if constexpr (FMT == FOCUS_CACHE_BF16) {
+          x[u] = __ldg(reinterpret_cast<const uint4*>(src + 2 * at));
+        } else {
+          const uint2 w = __ldg(reinterpret_cast<const uint2*>(src + at));
+          x[u].x = w.x, x[u].y = w.y;
+          sc[u] = __ldg((key ? a.kscale : a.vscale) + ((int64_t)b * a.H_kv + h) * a.cap + slot);
+        }
+      }
+    }
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int row = p0 + u * RPW;
+      if (row >= i1) continue;
+      const bool key = row < a.H_kv;
+      const int h = key ? row : row - a.H_kv;
+      if constexpr (FMT != FOCUS_CACHE_BF16) {
+        float f[8];
+        decode8<FMT>(make_uint2(x[u].x, x[u].y), sc[u], f);
+        x[u] = slot >= 0 ? C::pack(f) : make_uint4(0u, 0u, 0u, 0u);
+      }
+      uint16_t* y = key ? a.ko : a.vo;
+      *reinterpret_cast<uint4*>(y + (tk * a.H_kv + h) * D + 8 * c) = x[u];
+    }
+  }
+}
+
+constexpr int kCacheWarps = 2432;  // warps that fill the GPU: 16 per SM on 152 SMs
+
+// Warps per token and rows (of the 2 H_kv) of each: one warp, or for few tokens several.
+unsigned split_rows(CacheArgs& a, int step) {
+  const int rows = 2 * a.H_kv, most = (rows + step - 1) / step;
+  const int64_t want = (kCacheWarps + a.tokens - 1) / a.tokens;
+  a.splits = (int)(want < most ? want : most);
+  a.per = ((rows + a.splits - 1) / a.splits + step - 1) / step * step;
+  a.splits = (rows + a.per - 1) / a.per;
+  const int64_t blocks = (a.tokens * a.splits + 7) / 8;
+  return blocks > INT32_MAX ? 0u : (unsigned)blocks;
+}
+
+template <int D, int FMT>
+cudaError_t write_d(CacheArgs& a, int mode, cudaStream_t s) {
+  const unsigned g = split_rows(a, 512 / D);
+  if (!g) return cudaErrorInvalidConfiguration;
+  switch (mode) {
+    case kNoRope: cache_write<D, FMT, kNoRope><<<g, 256, 0, s>>>(a); break;
+    case kHalf: cache_write<D, FMT, kHalf><<<g, 256, 0, s>>>(a); break;
+    case kInterleaved: cache_write<D, FMT, kInterleaved><<<g, 256, 0, s>>>(a); break;
+    default: cache_write<D, FMT, kHalfAny><<<g, 256, 0, s>>>(a);
+  }
+  return cudaGetLastError();
+}
+
+template <int D, int FMT>
+cudaError_t read_d(CacheArgs& a, cudaStream_t s) {
+  const unsigned g = split_rows(a, 256 / D);
+  if (!g) return cudaErrorInvalidConfiguration;
+  cache_read<D, FMT><<<g, 256, 0, s>>>(a);
+  return cudaGetLastError();
+}
+
+CacheArgs args_of(const focus_cache_params& p, const int32_t* start, const int32_t* count, int32_t* status) {
+  CacheArgs a{};
+  a.start = start, a.count = count, a.status = status;
+  a.tokens = (int64_t)p.B * p.T;
+  a.T = p.T, a.cap = p.cap, a.H_kv = p.H_kv, a.R = p.R;
+  return a;
+}
+
+}  // namespace
+
+cudaError_t launch_cache_write(const focus_cache_params& p, const uint16_t* k, const focus_strides& ks,
+                               const uint16_t* v, const focus_strides& vs, const uint32_t* mask,
+                               const int32_t* start, const int32_t* count, const focus_rope* rope,
+                               const int32_t* positions, void* kc, void* vc, float* kscale,
+                               float* vscale, uint32_t* mc, int32_t* status, cudaStream_t s) {
+  CacheArgs a = args_of(p, start, count, status);
+  a.k = k, a.v = v, a.ks = ks, a.vs = vs, a.mask = mask, a.positions = positions;
+  a.kc = kc, a.vc = vc, a.kscale = kscale, a.vscale = vscale, a.mc = mc;
+  int mode = kNoRope;
+  if (rope) {
+    a.rope = *rope;
+    mode = rope->layout == FOCUS_ROPE_INTERLEAVED ? kInterleaved : rope->dim % 16 == 0 ? kHalf : kHalfAny;
+  }
+  if (p.d_head == 64)
+    return p.format == FOCUS_CACHE_BF16   ? write_d<64, FOCUS_CACHE_BF16>(a, mode, s)
+           : p.format == FOCUS_CACHE_E4M3 ? write_d<64, FOCUS_CACHE_E4M3>(a, mode, s)
+                                          : write_d<64, FOCUS_CACHE_INT8>(a, mode, s);
+  return p.format == FOCUS_CACHE_BF16   ? write_d<128, FOCUS_CACHE_BF16>(a, mode, s)
+         : p.format == FOCUS_CACHE_E4M3 ? write_d<128, FOCUS_CACHE_E4M3>(a, mode, s)
+                                        : write_d<128, FOCUS_CACHE_INT8>(a, mode, s);
+}
+
+cudaError_t launch_cache_read(const focus_cache_params& p, const void* kc, const void* vc,
+                              const float* kscale, const float* vscale, const int32_t* start,
+                              const int32_t* count, uint16_t* k, uint16_t* v, int32_t* status,
+                              cudaStream_t s) {
+  CacheArgs a = args_of(p, start, count, status);
+  a.kc = const_cast<void*>(kc), a.vc = const_cast<void*>(vc);
+  a.kscale = const_cast<float*>(kscale), a.vscale = const_cast<float*>(vscale);
+  a.ko = k, a.vo = v;
+  if (p.d_head == 64)
+    return p.format == FOCUS_CACHE_BF16   ? read_d<64, FOCUS_CACHE_BF16>(a, s)
+           : p.format == FOCUS_CACHE_E4M3 ? read_d<64, FOCUS_CACHE_E4M3>(a, s)
+                                          : read_d<64, FOCUS_CACHE_INT8>(a, s);
+  return p.format == FOCUS_CACHE_BF16   ? read_d<128, FOCUS_CACHE_BF16>(a, s)
+         : p.format == FOCUS_CACHE_E4M3 ? read_d<128, FOCUS_CACHE_E4M3>(a, s)
+                                        : read_d<128, FOCUS_CACHE_INT8>(a, s);
+}
+
+}  // namespace focus

@@ -134,6 +134,29 @@ size_t decode_workspace_bytes(const focus_params& p);
 cudaError_t launch_decode(const focus_params& p, const bf16* q, const bf16* k, const bf16* v,
                           const uint32_t* mask, bf16* o, float* lse, char* ws, float scale,
                           cudaStream_t s);
+// rope.cu
+int rope_plan(const focus_rope_params& p, focus_rope* out);
+int rope_check(const focus_rope* r, int d_head);
+cudaError_t launch_rope(const focus_rope& rope, int dtype, int B, int N, int H, int H_kv, int d,
+                        const void* q, const focus_strides& qs, const void* k, const focus_strides& ks,
+                        const int32_t* positions, int64_t offset, bool inverse, void* qo,
+                        const focus_strides& qos, void* ko, const focus_strides& kos, cudaStream_t s);
+// cache.cu
+cudaError_t launch_cache_write(const focus_cache_params& p, const uint16_t* k, const focus_strides& ks,
+                               const uint16_t* v, const focus_strides& vs, const uint32_t* mask,
+                               const int32_t* start, const int32_t* count, const focus_rope* rope,
+                               const int32_t* positions, void* kc, void* vc, float* kscale,
+                               float* vscale, uint32_t* mc, int32_t* status, cudaStream_t s);
+cudaError_t launch_cache_read(const focus_cache_params& p, const void* kc, const void* vc,
+                              const float* kscale, const float* vscale, const int32_t* start,
+                              const int32_t* count, uint16_t* k, uint16_t* v, int32_t* status,
+                              cudaStream_t s);
+// tree.cu
+size_t tree_workspace_bytes(const focus_cache_params& p);
+cudaError_t launch_decode_tree(const focus_cache_params& p, const bf16* q, const void* kc, const void* vc,
+                               const float* ks, const float* vs, const uint32_t* mask,
+                               const int32_t* lens, const uint64_t* tree, bf16* o, float* lse, char* ws,
+                               float scale, cudaStream_t s);
 // attn_tc.cu (tcgen05 engine)
 int tc_block_rows();
 cudaError_t launch_timeout_selftest(char* ws, size_t ws_bytes, cudaStream_t s);

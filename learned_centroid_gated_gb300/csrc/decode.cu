@@ -34,11 +34,13 @@
 
 #include "common.cuh"
 #include "tc_ptx.cuh"
+#include "warp_mma.cuh"
 
 namespace focus {
 namespace {
 
 using namespace ptx;
+using namespace wmma16;
 
 constexpr int kDecTile = 16;           // keys per pipeline tile (one MMA reduction step)
 constexpr int kDecStages = 3;          // tiles in the shared-memory ring
@@ -61,48 +63,6 @@ struct DecLayout {
   static constexpr int BYTES = (OFF_CNT + kDecStages * 4 + 15) / 16 * 16;
   static_assert(ROW % 16 == 0 && STAGE % 16 == 0, "16-byte aligned rows");
 };
-
-__device__ __forceinline__ unsigned lanemask_lt_dec() {
-  unsigned r;
-  asm("mov.u32 %0, %%lanemask_lt;" : "=r"(r));
-  return r;
-}
-
-// Four 8x8 bf16 matrices from shared memory (lane L gives the row address of
-// matrix L / 8); .trans delivers them transposed.
-__device__ __forceinline__ void ldsm_x4(uint32_t addr, uint32_t& r0, uint32_t& r1, uint32_t& r2,
-                                        uint32_t& r3) {
-  asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
-               : "=r"(r0), "=r"(r1), "=r"(r2), "=r"(r3)
-               : "r"(addr));
-}
-__device__ __forceinline__ void ldsm_x4_t(uint32_t addr, uint32_t& r0, uint32_t& r1, uint32_t& r2,
-                                          uint32_t& r3) {
-  asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
-               : "=r"(r0), "=r"(r1), "=r"(r2), "=r"(r3)
-               : "r"(addr));
-}
-// D (16x8 fp32) += A (16x16 bf16, row) * B (16x8 bf16, col), one warp.
-__device__ __forceinline__ void mma_bf16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2,
-                                         uint32_t a3, uint32_t b0, uint32_t b1) {
-  asm volatile(
-      "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
-      "{%0,%1,%2,%3};"
-      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
-      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
-}
-__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src) {
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
-}
-__device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
-template <int P>
-__device__ __forceinline__ void cp_async_wait() {
-  asm volatile("cp.async.wait_group %0;" ::"n"(P) : "memory");
-}
-__device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
-  const __nv_bfloat162 t = __floats2bfloat162_rn(lo, hi);
-  return *reinterpret_cast<const uint32_t*>(&t);
-}
 
 // Lane (g, t) = (lane / 4, lane % 4) of the MMA fragments.  Scores S^T = q K^T: rows =
 // query heads (g < nh; rows g + 8 are zero), columns = the tile's keys (two 8-key
@@ -183,7 +143,7 @@ decode_split(int N, int H, int H_kv, int R, int w, int B, int nsl, int nsl1, int
         const int j = jb + 32 * t + lane;
         const bool ok = j < je && (i - j < w || (mw[t] & mq) != 0u);
         const unsigned bal = __ballot_sync(0xffffffffu, ok);
-        if (ok) idx[ncomp + __popc(bal & lanemask_lt_dec())] = j;
+        if (ok) idx[ncomp + __popc(bal & lanemask_lt())] = j;
         ncomp += __popc(bal);
       }
       jb += kDecBlock;

@@ -624,6 +624,142 @@ int focus_decode(const focus_params* p, const uint16_t* q, const uint16_t* k_cac
                                (cudaStream_t)stream));
 }
 
+// ------------------------------------------------- rotary positions and cache --
+namespace {
+
+focus_strides dense(int N, int H, int d) {
+  return focus_strides{(int64_t)N * H * d, (int64_t)H * d, (int64_t)d};
+}
+
+// Shape checks shared by the cache's entry points (host only).
+int check_cache_params(const focus_cache_params* p) {
+  if (!p) return FOCUS_ERR_INVALID_ARG;
+  if (p->B < 1 || p->cap < 1 || p->T < 1 || p->H < 1 || p->H_kv < 1 || p->R < 1 || p->K < 1 ||
+      p->top_k < 1 || p->w < 1)
+    return FOCUS_ERR_INVALID_ARG;
+  if (p->H % p->H_kv != 0 || p->H_kv % p->R != 0) return FOCUS_ERR_INVALID_ARG;
+  if (p->K > FOCUS_MAX_K || p->top_k > p->K) return FOCUS_ERR_INVALID_ARG;
+  if (p->format < FOCUS_CACHE_BF16 || p->format > FOCUS_CACHE_INT8) return FOCUS_ERR_INVALID_ARG;
+  if (p->d_head != 64 && p->d_head != 128) return FOCUS_ERR_UNSUPPORTED;
+  // slots fit int32 with room for a draft; byte offsets stay far inside int64
+  if (p->cap > (1 << 30) || p->H > (1 << 16) || p->B > (1 << 20)) return FOCUS_ERR_UNSUPPORTED;
+  if ((double)p->B * p->cap * p->H_kv >= (double)(1ll << 40)) return FOCUS_ERR_UNSUPPORTED;
+  if ((double)p->B * p->T * p->H >= (double)(1ll << 40)) return FOCUS_ERR_UNSUPPORTED;
+  return FOCUS_OK;
+}
+
+// The cache's own pointers: a format's scales are there, and those of no other.
+int check_cache_ptrs(const focus_cache_params* p, const void* kc, const void* vc, const float* ks,
+                     const float* vs) {
+  if (!kc || !vc) return FOCUS_ERR_INVALID_ARG;
+  const bool scales = p->format != FOCUS_CACHE_BF16;
+  if (scales != (ks != nullptr) || scales != (vs != nullptr)) return FOCUS_ERR_INVALID_ARG;
+  if (!aligned(kc, 16) || !aligned(vc, 16) || !aligned(ks, 4) || !aligned(vs, 4))
+    return FOCUS_ERR_ALIGNMENT;
+  return FOCUS_OK;
+}
+
+int check_draft_params(const focus_cache_params* p) {
+  const int rc = check_cache_params(p);
+  if (rc) return rc;
+  if (p->T > FOCUS_MAX_DRAFT) return FOCUS_ERR_UNSUPPORTED;
+  if (p->T > p->cap) return FOCUS_ERR_INVALID_ARG;
+  if (p->B > 65535 || p->H > 4096) return FOCUS_ERR_UNSUPPORTED;  // grid dimensions
+  return FOCUS_OK;
+}
+
+}  // namespace
+
+int focus_rope_init(const focus_rope_params* params, focus_rope* rope) {
+  if (!params || !rope) return FOCUS_ERR_INVALID_ARG;
+  return rope_plan(*params, rope);
+}
+
+int focus_rope_apply(const focus_rope* rope, int32_t dtype, int32_t B, int32_t N, int32_t H,
+                     int32_t H_kv, int32_t d_head, const void* q, const focus_strides* qs,
+                     const void* k, const focus_strides* ks, const int32_t* positions,
+                     int64_t offset, int32_t inverse, void* q_out, const focus_strides* qos,
+                     void* k_out, const focus_strides* kos, void* stream) {
+  if (!rope || !q || !q_out || (k && !k_out)) return FOCUS_ERR_INVALID_ARG;
+  if (B < 1 || N < 1 || H < 1 || (k && H_kv < 1)) return FOCUS_ERR_INVALID_ARG;
+  if (dtype < FOCUS_DTYPE_BF16 || dtype > FOCUS_DTYPE_F32) return FOCUS_ERR_INVALID_ARG;
+  if (d_head != 64 && d_head != 128) return FOCUS_ERR_UNSUPPORTED;
+  if (H > (1 << 16) || (k && H_kv > (1 << 16))) return FOCUS_ERR_UNSUPPORTED;
+  const int rc = rope_check(rope, d_head);
+  if (rc) return rc;
+  const size_t size = dtype == FOCUS_DTYPE_F32 ? 4 : 2;
+  if (!aligned(q, size) || !aligned(k, size) || !aligned(q_out, size) || !aligned(k_out, size) ||
+      !aligned(positions, 4))
+    return FOCUS_ERR_ALIGNMENT;
+  const int hk = k ? H_kv : 0;
+  // a grid of one warp per token and part of its heads
+  if ((double)B * N >= 8.0 * INT32_MAX) return FOCUS_ERR_UNSUPPORTED;
+  const focus_strides dq = dense(N, H, d_head), dk = dense(N, hk, d_head);
+  return cuda_rc(launch_rope(*rope, dtype, B, N, H, hk, d_head, q, qs ? *qs : dq, k, ks ? *ks : dk,
+                             positions, offset, inverse != 0, q_out, qos ? *qos : dq, k_out,
+                             kos ? *kos : dk, (cudaStream_t)stream));
+}
+
+int focus_cache_write(const focus_cache_params* p, const uint16_t* k, const focus_strides* ks,
+                      const uint16_t* v, const focus_strides* vs, const uint32_t* mask,
+                      const int32_t* start, const int32_t* count, const focus_rope* rope,
+                      const int32_t* positions, void* k_cache, void* v_cache, float* k_scale,
+                      float* v_scale, uint32_t* mask_cache, int32_t* status, void* stream) {
+  int rc = check_cache_params(p);
+  if (rc) return rc;
+  if (!k || !v || !start || (mask && !mask_cache)) return FOCUS_ERR_INVALID_ARG;
+  if ((rc = check_cache_ptrs(p, k_cache, v_cache, k_scale, v_scale))) return rc;
+  if (rope && (rc = rope_check(rope, p->d_head))) return rc;
+  const focus_strides d = dense(p->T, p->H_kv, p->d_head);
+  const focus_strides sk = ks ? *ks : d, sv = vs ? *vs : d;
+  if (!aligned(k, 16) || !aligned(v, 16) || (sk.b | sk.n | sk.h | sv.b | sv.n | sv.h) % 8 != 0 ||
+      !aligned(mask, 4) || !aligned(mask_cache, 4) || !aligned(start, 4) || !aligned(count, 4) ||
+      !aligned(positions, 4) || !aligned(status, 4))
+    return FOCUS_ERR_ALIGNMENT;
+  return cuda_rc(launch_cache_write(*p, k, sk, v, sv, mask, start, count, rope, positions, k_cache,
+                                    v_cache, k_scale, v_scale, mask_cache, status,
+                                    (cudaStream_t)stream));
+}
+
+int focus_cache_read(const focus_cache_params* p, const void* k_cache, const void* v_cache,
+                     const float* k_scale, const float* v_scale, const int32_t* start,
+                     const int32_t* count, uint16_t* k, uint16_t* v, int32_t* status, void* stream) {
+  int rc = check_cache_params(p);
+  if (rc) return rc;
+  if (!k || !v) return FOCUS_ERR_INVALID_ARG;
+  if ((rc = check_cache_ptrs(p, k_cache, v_cache, k_scale, v_scale))) return rc;
+  if (!aligned(k, 16) || !aligned(v, 16) || !aligned(start, 4) || !aligned(count, 4) ||
+      !aligned(status, 4))
+    return FOCUS_ERR_ALIGNMENT;
+  return cuda_rc(launch_cache_read(*p, k_cache, v_cache, k_scale, v_scale, start, count, k, v, status,
+                                   (cudaStream_t)stream));
+}
+
+size_t focus_decode_tree_workspace_size(const focus_cache_params* p) {
+  if (check_draft_params(p) != FOCUS_OK) return 0;
+  return tree_workspace_bytes(*p);
+}
+
+int focus_decode_tree(const focus_cache_params* p, const uint16_t* q, const void* k_cache,
+                      const void* v_cache, const float* k_scale, const float* v_scale,
+                      const uint32_t* mask_cache, const int32_t* lens, const uint64_t* tree,
+                      uint16_t* o, float* lse, void* ws, size_t ws_bytes, void* stream) {
+  int rc = check_draft_params(p);
+  if (rc) return rc;
+  if (!q || !mask_cache || !lens || !o) return FOCUS_ERR_INVALID_ARG;
+  if ((rc = check_cache_ptrs(p, k_cache, v_cache, k_scale, v_scale))) return rc;
+  if (!aligned(q, 16) || !aligned(o, 16) || !aligned(mask_cache, 4) || !aligned(lens, 4) ||
+      !aligned(tree, 8) || !aligned(lse, 4))
+    return FOCUS_ERR_ALIGNMENT;
+  if (!ws) return FOCUS_ERR_INVALID_ARG;
+  if (!aligned(ws, 256)) return FOCUS_ERR_ALIGNMENT;
+  if (ws_bytes < tree_workspace_bytes(*p)) return FOCUS_ERR_WORKSPACE;
+  const float scale = p->softmax_scale > 0.0f ? p->softmax_scale : 1.0f / sqrtf((float)p->d_head);
+  return cuda_rc(launch_decode_tree(*p, reinterpret_cast<const bf16*>(q), k_cache, v_cache, k_scale,
+                                    v_scale, mask_cache, lens, tree, reinterpret_cast<bf16*>(o), lse,
+                                    (char*)ws, scale, (cudaStream_t)stream));
+}
+
 int focus_selftest_timeout(void* ws, size_t ws_bytes, void* stream) {
   if (!ws) return FOCUS_ERR_INVALID_ARG;
   if (!aligned(ws, 256)) return FOCUS_ERR_ALIGNMENT;
@@ -661,7 +797,7 @@ const char* focus_strerror(int code) {
   }
 }
 
-int focus_version(void) { return (1 << 16) | 0; }
+int focus_version(void) { return (1 << 16) | 1; }
 
 const char* focus_cuda_error_string(void) {
   return g_last_cuda_error == cudaSuccess ? "no CUDA error" : cudaGetErrorString(g_last_cuda_error);

@@ -1,0 +1,97 @@
+// Rotary positions: the angle of one pair, and the 16-byte row chunks the kernels move.
+// Shared by rope.cu (queries and keys) and cache.cu (keys on their way into the cache).
+#pragma once
+
+#include <cuda_fp16.h>
+
+#include "common.cuh"
+
+namespace focus {
+
+// cos and sin of pos * f_i, times g.  turn = f_i / 2 pi as a fraction of 2^64, so the
+// 64-bit product's wrap-around is the reduction modulo one turn, exactly, for every
+// position (in fp32 the product alone would be off by 0.06 rad at a million tokens).
+// Its upper half read as a signed number is the angle in units of 2^-32 turns within
+// half a turn of zero; sincospi takes it in units of half a turn.
+__device__ __forceinline__ void rope_angle(int64_t pos, uint64_t turn, float g, float& c, float& s) {
+  const int t = (int)(uint32_t)(((uint64_t)pos * turn) >> 32);
+  sincospif((float)t * 4.656612873077393e-10f, &s, &c);  // 2^-31
+  c *= g;
+  s *= g;
+}
+
+// (a, b) turned: one product and one fused multiply-add each, the same on every path.
+__device__ __forceinline__ void rope_turn(float& a, float& b, float c, float s) {
+  const float x = a, y = b;
+  a = __fmaf_rn(x, c, -__fmul_rn(y, s));
+  b = __fmaf_rn(y, c, __fmul_rn(x, s));
+}
+
+template <typename T>
+struct RowChunk;  // 16 bytes of a row as V floats
+
+template <>
+struct RowChunk<bf16> {
+  static constexpr int V = 8;
+  static __device__ __forceinline__ void unpack(const uint4& x, float (&f)[8]) {
+    const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      f[2 * i] = __uint_as_float(w[i] << 16);
+      f[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+    }
+  }
+  static __device__ __forceinline__ uint4 pack(const float (&f)[8]) {
+    uint32_t w[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const __nv_bfloat162 t = __floats2bfloat162_rn(f[2 * i], f[2 * i + 1]);
+      w[i] = *reinterpret_cast<const uint32_t*>(&t);
+    }
+    return make_uint4(w[0], w[1], w[2], w[3]);
+  }
+  static __device__ __forceinline__ float to_float(bf16 x) { return __bfloat162float(x); }
+  static __device__ __forceinline__ bf16 from_float(float x) { return __float2bfloat16_rn(x); }
+};
+
+template <>
+struct RowChunk<__half> {
+  static constexpr int V = 8;
+  static __device__ __forceinline__ void unpack(const uint4& x, float (&f)[8]) {
+    const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const float2 t = __half22float2(*reinterpret_cast<const __half2*>(&w[i]));
+      f[2 * i] = t.x;
+      f[2 * i + 1] = t.y;
+    }
+  }
+  static __device__ __forceinline__ uint4 pack(const float (&f)[8]) {
+    uint32_t w[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const __half2 t = __floats2half2_rn(f[2 * i], f[2 * i + 1]);
+      w[i] = *reinterpret_cast<const uint32_t*>(&t);
+    }
+    return make_uint4(w[0], w[1], w[2], w[3]);
+  }
+  static __device__ __forceinline__ float to_float(__half x) { return __half2float(x); }
+  static __device__ __forceinline__ __half from_float(float x) { return __float2half_rn(x); }
+};
+
+template <>
+struct RowChunk<float> {
+  static constexpr int V = 4;
+  static __device__ __forceinline__ void unpack(const uint4& x, float (&f)[4]) {
+    f[0] = __uint_as_float(x.x), f[1] = __uint_as_float(x.y);
+    f[2] = __uint_as_float(x.z), f[3] = __uint_as_float(x.w);
+  }
+  static __device__ __forceinline__ uint4 pack(const float (&f)[4]) {
+    return make_uint4(__float_as_uint(f[0]), __float_as_uint(f[1]), __float_as_uint(f[2]),
+                      __float_as_uint(f[3]));
+  }
+  static __device__ __forceinline__ float to_float(float x) { return x; }
+  static __device__ __forceinline__ float from_float(float x) { return x; }
+};
+
+}  // namespace focus
