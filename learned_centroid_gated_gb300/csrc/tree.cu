@@ -12,20 +12,12 @@
 //                 shared-memory ring with 16-byte asynchronous copies, and keeps an online
 //                 softmax per row; both products are m16n8k16 register-fragment MMAs.
 //   tree_combine  merges a row's slices by their maxima: O, LSE.
-//
-// The slices: host and device agree only on the cache's capacity, the lengths are known to
-// the device alone.  Keys come in units of 32 with an integer weight each (dense ones near
-// the window, the expected share of matching masks far from it).  All sequences' units
-// stand in one row, cut into equal weights, so that a batch of one long and many short
-// sequences keeps every warp busy.  Slice g of sequence b writes partial g + b: going along
-// the row either g or b grows by one, so the numbers are distinct.
-#include <cuda_fp8.h>
 #include <math.h>
 
 #include <algorithm>
 
-#include "common.cuh"
 #include "tc_ptx.cuh"
+#include "tree.cuh"
 #include "warp_mma.cuh"
 
 namespace focus {
@@ -37,94 +29,11 @@ using namespace wmma16;
 constexpr int kTreeTile = 16;     // keys per pipeline tile (one MMA reduction step)
 constexpr int kTreeRows = 16;     // rows per warp (the MMA's M)
 constexpr int kTreeBlock = 256;   // raw keys per listing step
-constexpr int kTreeUnit = 32;     // keys per unit of work
-constexpr int kTreeNear = 64;     // weight of a unit near the window
 constexpr int kTreeMinUnits = 4;  // fewest dense units per slice
 constexpr int kTreeWarps = 1216;  // warps per launch: one wave of 8 per SM on 152 SMs
 constexpr float kLn2 = 0.6931471805599453f;
 constexpr float kLog2e = 1.4426950408889634f;
-constexpr float kPBias = 32768.0f;  // 8-bit formats: P in fp16 reaches from 2^15 to 2^-24
-
-struct TreeArgs {
-  const bf16* q;
-  const void *kc, *vc;
-  const float *ks, *vs;
-  const uint32_t* mask;
-  const int32_t* lens;
-  const uint64_t* tree;
-  float2* part_ml;   // [KV head][row group][slot][16] (max, sum)
-  float* part_acc;   // [KV head][row group][slot][16][D]
-  bf16* o;
-  float* lse;
-  int32_t* status;
-  int B, cap, T, H, H_kv, R, w, gq, rows, nrg, G, wfar;
-  float sl2;         // softmax scale * log2(e)
-};
-
-// ------------------------------------------------------------- the row of units --
-// Sequence b's part: far units of weight wfar (no key of them is near any drafted token's
-// window), then near units of weight kTreeNear up to the last drafted token.
-struct Stretch {
-  int units, far;
-  int64_t weight;
-};
-__device__ __forceinline__ bool len_ok(const TreeArgs& a, int len) { return len >= 0 && len <= a.cap - a.T; }
-__device__ __forceinline__ Stretch stretch_of(const TreeArgs& a, int len) {
-  Stretch s{0, 0, 0};
-  if (!len_ok(a, len)) return s;
-  s.units = (len + a.T + kTreeUnit - 1) / kTreeUnit;
-  s.far = max(0, len - a.w + 1) / kTreeUnit;
-  s.weight = (int64_t)s.far * a.wfar + (int64_t)(s.units - s.far) * kTreeNear;
-  return s;
-}
-// Units of a stretch that begin before weight x.
-__device__ __forceinline__ int units_before(const TreeArgs& a, const Stretch& s, int64_t x) {
-  if (x <= 0) return 0;
-  const int64_t wf = (int64_t)s.far * a.wfar;
-  const int64_t u = x <= wf ? (x + a.wfar - 1) / a.wfar : s.far + (x - wf + kTreeNear - 1) / kTreeNear;
-  return (int)min((int64_t)s.units, u);
-}
-__device__ __forceinline__ int slices_of(const TreeArgs& a, int64_t total) {
-  return (int)max((int64_t)1, min((int64_t)a.G, total / (kTreeMinUnits * kTreeNear)));
-}
-__device__ __forceinline__ int64_t warp_sum(int64_t x) {
-#pragma unroll
-  for (int o = 16; o; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
-  return x;
-}
-__device__ __forceinline__ int64_t warp_scan(int64_t x, int lane) {  // inclusive
-#pragma unroll
-  for (int o = 1; o < 32; o <<= 1) {
-    const int64_t y = __shfl_up_sync(0xffffffffu, x, o);
-    if (lane >= o) x += y;
-  }
-  return x;
-}
-__device__ __forceinline__ int64_t total_weight(const TreeArgs& a, int lane) {
-  int64_t t = 0;
-  for (int b = lane; b < a.B; b += 32) t += stretch_of(a, __ldg(a.lens + b)).weight;
-  return warp_sum(t);
-}
-
-// Ancestors of drafted token t (itself among them), bits from T on cleared.
-__device__ __forceinline__ uint64_t tree_word(const TreeArgs& a, int b, int t) {
-  const uint64_t all = a.T == 64 ? ~0ull : (1ull << a.T) - 1;
-  return (a.tree ? a.tree[(int64_t)b * a.T + t] : (2ull << t) - 1) & all;
-}
-
-// ------------------------------------------------------------------ code formats --
-template <int FMT>
-__device__ __forceinline__ uint32_t codes_f16(uint32_t two) {  // two codes (low half) as fp16
-  if constexpr (FMT == FOCUS_CACHE_E4M3) {
-    const __half2_raw r = __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)(two & 0xffffu), __NV_E4M3);
-    return *reinterpret_cast<const uint32_t*>(&r);
-  } else {
-    // 0x6400 | (c + 128) is 1024 + c + 128 in fp16
-    const uint32_t h = __byte_perm(two ^ 0x8080u, 0x64646464u, 0x4140);
-    const __half2 r = __hsub2(*reinterpret_cast<const __half2*>(&h), __float2half2_rn(1152.0f));
-    return *reinterpret_cast<const uint32_t*>(&r);
-  }
-}
+constexpr float kPTop = 14.0f;  // 8-bit formats: log2 of the largest P times V scale (in fp16)
 
 // Per-warp shared memory: a ring of tiles, each kTreeTile K rows, as many V rows and, in
 // the 8-bit formats, their scales; per stage its keys' slots and masks; the listing.
@@ -167,20 +76,12 @@ __global__ void __launch_bounds__(32) tree_split(const __grid_constant__ TreeArg
   constexpr int DB = D / 8;  // 8-bit formats: consecutive columns of a lane's V pieces
   extern __shared__ __align__(128) char smem[];
   const int lane = threadIdx.x, g = lane >> 2, t4 = lane & 3;
-  const int slice = blockIdx.x;
-  const int rg = blockIdx.y % a.nrg, kvh = blockIdx.y / a.nrg;
-  const int rho = kvh / (a.H_kv / a.R);
   int* idx = reinterpret_cast<int*>(smem + L::OFF_IDX);
   uint32_t* msk = reinterpret_cast<uint32_t*>(smem + L::OFF_MSK);
   int* cnt = reinterpret_cast<int*>(smem + L::OFF_CNT);
   const uint32_t ring = smem_u32(smem);
 
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-  const int64_t total = total_weight(a, lane);
-  const int ns = slices_of(a, total);
-  if (slice >= ns) return;
-  const int64_t lo = total * slice / ns, hi = total * (slice + 1) / ns;
-
   // Rows of a partial tile beyond its keys keep older rows; zero them once so that they
   // are finite (their probabilities are exactly zero).
   for (int o = 16 * lane; o < L::STAGES * L::STAGE; o += 512)
@@ -189,373 +90,338 @@ __global__ void __launch_bounds__(32) tree_split(const __grid_constant__ TreeArg
   const int64_t kvrow = (int64_t)a.H_kv * D;  // elements per slot
   constexpr int ES = B16 ? 2 : 1;
 
-  // The rows: row x of the group is query head x % gq of drafted token x / gq.  With all
-  // rows of one token its list of keys is exact and needs no test per element.
-  const int r_end = min(a.rows - rg * kTreeRows, kTreeRows);
-  const bool one_token = (rg * kTreeRows) / a.gq == (rg * kTreeRows + r_end - 1) / a.gq;
+  for_segments(a, blockIdx.x, lane, [&](int64_t partial, int kvh, int rg, int b, int len, int js, int je) {
+    // The rows: row x of the group is query head x % gq of drafted token x / gq.  With all
+    // rows of one token its list of keys is exact and needs no test per element.
+    const int r_end = min(a.rows - rg * kTreeRows, kTreeRows);
+    const bool one_token = (rg * kTreeRows) / a.gq == (rg * kTreeRows + r_end - 1) / a.gq;
+    const int rho = kvh / (a.H_kv / a.R);
+    const uint32_t* M = a.mask + ((int64_t)b * a.R + rho) * a.cap;
 
-  int64_t before = 0;
-  for (int bc = 0; bc < a.B && before < hi; bc += 32) {
-    const int lb = bc + lane < a.B ? __ldg(a.lens + bc + lane) : -1;
-    const Stretch mine = stretch_of(a, lb);
-    const int64_t upto = warp_scan(mine.weight, lane);
-    const int64_t from = before + upto - mine.weight;
-    const int my0 = units_before(a, mine, lo - from), my1 = units_before(a, mine, hi - from);
-    before += __shfl_sync(0xffffffffu, upto, 31);
-    unsigned todo = __ballot_sync(0xffffffffu, my0 < my1);
-    while (todo) {
-      const int src = __ffs(todo) - 1;
-      todo &= todo - 1;
-      const int b = bc + src;
-      const int len = __shfl_sync(0xffffffffu, lb, src);
-      const int js = __shfl_sync(0xffffffffu, my0, src) * kTreeUnit;
-      const int je = min(len + a.T, __shfl_sync(0xffffffffu, my1, src) * kTreeUnit);
-      const uint32_t* M = a.mask + ((int64_t)b * a.R + rho) * a.cap;
-
-      // ---- this lane's two rows, g and g + 8
-      uint64_t word[2];
-      uint32_t mrow[2];
-      int near[2], pos[2];  // first position inside the window, own position
-      float fac[2];         // logit (log2) = MMA result * fac (* K scale)
-      uint32_t qa[D / 16][4];
+    // ---- this lane's two rows, g and g + 8
+    uint64_t word[2];
+    uint32_t mrow[2];
+    int near[2], pos[2];  // first position inside the window, own position
+    float fac[2];         // logit (log2) = MMA result * fac (* K scale)
+    uint32_t qa[D / 16][4];
 #pragma unroll
-      for (int e = 0; e < 2; ++e) {
-        const int r = g + 8 * e;
-        const bool on = r < r_end;
-        const int x = rg * kTreeRows + (on ? r : 0), t = x / a.gq, h = kvh * a.gq + x % a.gq;
-        word[e] = on ? tree_word(a, b, t) : 0ull;
-        pos[e] = len + __popcll(word[e]) - 1;
-        near[e] = word[e] ? pos[e] - a.w + 1 : INT_MAX;
-        mrow[e] = word[e] ? __ldg(M + len + t) : 0u;
-        fac[e] = a.sl2;
-        const bf16* qr = a.q + (((int64_t)b * a.T + t) * a.H + h) * D;
-        if constexpr (B16) {
-          const uint32_t* qw = reinterpret_cast<const uint32_t*>(qr);
+    for (int e = 0; e < 2; ++e) {
+      const int r = g + 8 * e;
+      const bool on = r < r_end;
+      const int x = rg * kTreeRows + (on ? r : 0), t = x / a.gq, h = kvh * a.gq + x % a.gq;
+      word[e] = on ? tree_word(a, b, t) : 0ull;
+      pos[e] = len + __popcll(word[e]) - 1;
+      near[e] = word[e] ? pos[e] - a.w + 1 : INT_MAX;
+      mrow[e] = word[e] ? __ldg(M + len + t) : 0u;
+      fac[e] = a.sl2;
+      const bf16* qr = a.q + (((int64_t)b * a.T + t) * a.H + h) * D;
+      if constexpr (B16) {
+        const uint32_t* qw = reinterpret_cast<const uint32_t*>(qr);
 #pragma unroll
-          for (int c = 0; c < D / 16; ++c) {
-            qa[c][e] = on ? __ldg(qw + 8 * c + t4) : 0u;
-            qa[c][2 + e] = on ? __ldg(qw + 8 * c + 4 + t4) : 0u;
-          }
-        } else {
-          // fp16 operands: the row is scaled by the power of two that brings its maximum
-          // into [1, 2), which keeps every bf16 digit down to 2^-24 of that maximum.
-          // Step (c, i) multiplies columns 64 c + 16 t4 + 4 i .. + 3: the order of a
-          // product's columns is free, and this one reads K in 16-byte pieces.
-          float f[D / 4];
-          float mx = 0.0f;
-#pragma unroll
-          for (int c = 0; c < D / 64; ++c)
-#pragma unroll
-            for (int i = 0; i < 8; ++i) {
-              const uint32_t w = on ? __ldg(reinterpret_cast<const uint32_t*>(qr) + 32 * c + 8 * t4 + i) : 0u;
-              f[16 * c + 2 * i] = __uint_as_float(w << 16);
-              f[16 * c + 2 * i + 1] = __uint_as_float(w & 0xffff0000u);
-              mx = fmaxf(mx, fmaxf(fabsf(f[16 * c + 2 * i]), fabsf(f[16 * c + 2 * i + 1])));
-            }
-          mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
-          mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
-          uint32_t ex = __float_as_uint(mx) >> 23;
-          ex = ex == 0u || ex >= 254u ? 127u : ex;
-          const float up = __uint_as_float((254u - ex) << 23);
-          fac[e] *= __uint_as_float(ex << 23);
-#pragma unroll
-          for (int c = 0; c < D / 16; ++c) {
-            qa[c][e] = pack_f16(f[4 * c] * up, f[4 * c + 1] * up);
-            qa[c][2 + e] = pack_f16(f[4 * c + 2] * up, f[4 * c + 3] * up);
-          }
+        for (int c = 0; c < D / 16; ++c) {
+          qa[c][e] = on ? __ldg(qw + 8 * c + t4) : 0u;
+          qa[c][2 + e] = on ? __ldg(qw + 8 * c + 4 + t4) : 0u;
         }
-      }
-      // ---- what any row of the group sees
-      const uint32_t many = __reduce_or_sync(0xffffffffu, mrow[0] | mrow[1]);
-      const int nearest = __reduce_min_sync(0xffffffffu, min(near[0], near[1]));
-      const uint32_t wlo = __reduce_or_sync(0xffffffffu, (uint32_t)(word[0] | word[1]));
-      const uint32_t whi = __reduce_or_sync(0xffffffffu, (uint32_t)((word[0] | word[1]) >> 32));
-      const uint64_t any_word = (uint64_t)whi << 32 | wlo;
-
-      // ---- listing: keys of [js, je) in blocks, tiles issued from a block's list
-      int jb = js, ncomp = 0, at = 0;
-      constexpr int MW = kTreeBlock / 32;
-      uint32_t mw[MW];
+      } else {
+        // Step (c, i) multiplies columns 64 c + 16 t4 + 4 i .. + 3: the order of a
+        // product's columns is free, and this one reads K in 16-byte pieces.
+        float f[D / 4];
+        float mx = 0.0f;
 #pragma unroll
-      for (int t = 0; t < MW; ++t) {
-        const int j = jb + 32 * t + lane;
-        mw[t] = j < je ? __ldg(M + j) : 0u;
-      }
-      const char* kb = reinterpret_cast<const char*>(a.kc) + ((int64_t)b * a.cap * kvrow + (int64_t)kvh * D) * ES;
-      const char* vb = reinterpret_cast<const char*>(a.vc) + ((int64_t)b * a.cap * kvrow + (int64_t)kvh * D) * ES;
-      const float* ksc = B16 ? nullptr : a.ks + ((int64_t)b * a.H_kv + kvh) * a.cap;
-      const float* vsc = B16 ? nullptr : a.vs + ((int64_t)b * a.H_kv + kvh) * a.cap;
-
-      auto issue = [&](int s) -> bool {
-        while (at >= ncomp) {
-          if (jb >= je) return false;
-          ncomp = 0;
+        for (int c = 0; c < D / 64; ++c)
 #pragma unroll
-          for (int t = 0; t < MW; ++t) {
-            const int j = jb + 32 * t + lane;
-            bool ok = j < je;
-            if (ok) {
-              if (j < len) {
-                ok = j >= nearest || (mw[t] & many) != 0u;
-              } else {
-                const int u = j - len;
-                ok = (any_word >> u & 1ull) != 0ull;
-                if (ok && one_token)  // the window among drafted tokens: by their depths
-                  ok = len + __popcll(tree_word(a, b, u)) - 1 >= nearest || (mw[t] & many) != 0u;
-              }
-            }
-            const unsigned bal = __ballot_sync(0xffffffffu, ok);
-            if (ok) {
-              const int x = ncomp + __popc(bal & lanemask_lt());
-              idx[x] = j;
-              msk[x] = mw[t];
-            }
-            ncomp += __popc(bal);
+          for (int i = 0; i < 8; ++i) {
+            const uint32_t w = on ? __ldg(reinterpret_cast<const uint32_t*>(qr) + 32 * c + 8 * t4 + i) : 0u;
+            f[16 * c + 2 * i] = __uint_as_float(w << 16);
+            f[16 * c + 2 * i + 1] = __uint_as_float(w & 0xffff0000u);
+            mx = fmaxf(mx, fmaxf(fabsf(f[16 * c + 2 * i]), fabsf(f[16 * c + 2 * i + 1])));
           }
-          jb += kTreeBlock;
+        mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
+        mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
+        float up, down;
+        row_unit(mx, up, down);
+        fac[e] *= down;
 #pragma unroll
-          for (int t = 0; t < MW; ++t) {  // the next block's words, in flight meanwhile
-            const int j = jb + 32 * t + lane;
-            mw[t] = j < je ? __ldg(M + j) : 0u;
-          }
-          at = 0;
-          __syncwarp();
-        }
-        const int n = min(kTreeTile, ncomp - at);
-        const uint32_t st = ring + s * L::STAGE;
-        if (lane == 0) cnt[s] = n;
-        if (lane < n) {
-          int* key = reinterpret_cast<int*>(smem + s * L::STAGE + L::OFF_KEY);
-          key[lane] = idx[at + lane];
-          key[kTreeTile + lane] = (int)msk[at + lane];
-        }
-        constexpr int CH = D * ES / 16, RPI = 32 / CH;  // 16-byte pieces per row, rows per instruction
-        const int ch = lane % CH;
-        for (int rr = lane / CH; rr < n; rr += RPI) {
-          const int64_t off = (int64_t)idx[at + rr] * kvrow * ES + 16 * ch;
-          if constexpr (B16) {
-            cp_async16(st + rr * L::ROW + 16 * ch, kb + off);
-            cp_async16(st + (kTreeTile + rr) * L::ROW + 16 * ch, vb + off);
-          } else {
-            cp_async16(st + k_piece<D>(rr, ch), kb + off);
-            cp_async16(st + kTreeTile * D + v_piece<D>(rr, ch), vb + off);
-          }
-        }
-        if constexpr (!B16) {
-          const int rr = lane & 15;
-          if (rr < n) cp_async4(st + L::OFF_SCALE + 4 * lane, (lane < 16 ? ksc : vsc) + idx[at + rr]);
-        }
-        cp_async_commit();
-        at += n;
-        return true;
-      };
-
-      float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.0f, 0.0f};
-      float sv = 8.0e-31f;  // 8-bit formats: largest V scale so far; acc holds O 2^15 / sv
-      float acc[DB][4];
-#pragma unroll
-      for (int i = 0; i < DB; ++i)
-#pragma unroll
-        for (int e = 0; e < 4; ++e) acc[i][e] = 0.0f;
-      __syncwarp();  // zeroed stages (and the last stretch's reads) before the first copy
-      int issued = 0;  // one copy group per stage and per refill, empty or not
-      for (int s = 0; s < L::STAGES; ++s) {
-        if (issue(s)) ++issued;
-        else cp_async_commit();
-      }
-      for (int t = 0; t < issued; ++t) {
-        const int s = t % L::STAGES;
-        cp_async_wait<L::STAGES - 1>();  // tile t's group has landed (this lane's copies)
-        __syncwarp();                    // ... and every lane's
-        const int n = cnt[s];
-        const uint32_t st = ring + s * L::STAGE;
-        float c0[4] = {0.0f, 0.0f, 0.0f, 0.0f}, c1[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-        if constexpr (B16) {
-          const uint32_t ka = st + ((lane & 7) + ((lane >> 4) << 3)) * L::ROW + ((lane >> 3) & 1) * 16;
-#pragma unroll
-          for (int c = 0; c < D / 16; ++c) {
-            uint32_t r0, r1, r2, r3;
-            ldsm_x4(ka + 32 * c, r0, r1, r2, r3);
-            mma_bf16(c0, qa[c][0], qa[c][1], qa[c][2], qa[c][3], r0, r1);
-            mma_bf16(c1, qa[c][0], qa[c][1], qa[c][2], qa[c][3], r2, r3);
-          }
-        } else {
-#pragma unroll
-          for (int c = 0; c < D / 64; ++c) {
-            const uint4 x = lds128(st + k_piece<D>(g, 4 * c + t4));
-            const uint4 y = lds128(st + k_piece<D>(g + 8, 4 * c + t4));
-            const uint32_t xw[4] = {x.x, x.y, x.z, x.w}, yw[4] = {y.x, y.y, y.z, y.w};
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              const uint32_t* A = qa[4 * c + i];
-              mma_f16(c0, A[0], A[1], A[2], A[3], codes_f16<FMT>(xw[i]), codes_f16<FMT>(xw[i] >> 16));
-              mma_f16(c1, A[0], A[1], A[2], A[3], codes_f16<FMT>(yw[i]), codes_f16<FMT>(yw[i] >> 16));
-            }
-          }
-        }
-        // ---- logits of rows g, g + 8 and keys 2 t4, 2 t4 + 1, 8 + 2 t4, 9 + 2 t4
-        const int kk[4] = {2 * t4, 2 * t4 + 1, 2 * t4 + 8, 2 * t4 + 9};
-        float sx[2][4] = {{c0[0], c0[1], c1[0], c1[1]}, {c0[2], c0[3], c1[2], c1[3]}};
-        float kf[4] = {1.0f, 1.0f, 1.0f, 1.0f}, vf[4];
-        if constexpr (!B16) {
-          const float* sc = reinterpret_cast<const float*>(smem + s * L::STAGE + L::OFF_SCALE);
-#pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            kf[e] = sc[kk[e]];
-            vf[e] = kk[e] < n ? sc[kTreeTile + kk[e]] : 0.0f;
-          }
-        }
-        bool see[2][4];
-#pragma unroll
-        for (int e = 0; e < 4; ++e) see[0][e] = see[1][e] = kk[e] < n;
-        if (!one_token) {
-          const int* key = reinterpret_cast<const int*>(smem + s * L::STAGE + L::OFF_KEY);
-          const bool drafts = key[n - 1] >= len;  // slots ascend in a list
-#pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            if (kk[e] >= n) continue;
-            const int j = key[kk[e]];
-            const uint32_t mk = (uint32_t)key[kTreeTile + kk[e]];
-            int p = j;
-            uint64_t bit = ~0ull;
-            if (drafts && j >= len) {
-              p = len + __popcll(tree_word(a, b, j - len)) - 1;
-              bit = 1ull << (j - len);
-            }
-#pragma unroll
-            for (int r = 0; r < 2; ++r)
-              see[r][e] = (word[r] & bit) != 0ull && (p >= near[r] || (mk & mrow[r]) != 0u);
-          }
-        }
-        float corr[2];
-        float p[2][4];
-#pragma unroll
-        for (int r = 0; r < 2; ++r) {
-#pragma unroll
-          for (int e = 0; e < 4; ++e) sx[r][e] = see[r][e] ? sx[r][e] * kf[e] * fac[r] : -INFINITY;
-          float mt = fmaxf(fmaxf(sx[r][0], sx[r][1]), fmaxf(sx[r][2], sx[r][3]));
-          mt = fmaxf(mt, __shfl_xor_sync(0xffffffffu, mt, 1));
-          mt = fmaxf(mt, __shfl_xor_sync(0xffffffffu, mt, 2));
-          const float mn = fmaxf(m[r], mt);
-          const float mu = mn == -INFINITY ? 0.0f : mn;  // a row without a key so far
-          corr[r] = ex2(m[r] - mu);
-#pragma unroll
-          for (int e = 0; e < 4; ++e) p[r][e] = ex2(sx[r][e] - mu);
-          l[r] = l[r] * corr[r] + ((p[r][0] + p[r][1]) + (p[r][2] + p[r][3]));
-          m[r] = mn;
-        }
-        uint32_t pa[4];
-        if constexpr (B16) {
-          // P rounded to bf16 for the tensor core, as in the forward pass; l sums it unrounded
-          pa[0] = pack_bf16(p[0][0], p[0][1]);
-          pa[1] = pack_bf16(p[1][0], p[1][1]);
-          pa[2] = pack_bf16(p[0][2], p[0][3]);
-          pa[3] = pack_bf16(p[1][2], p[1][3]);
-        } else {
-          // V's scales join P: p vs / sv <= 1, times 2^15 so that what is smaller than the
-          // largest weight by up to 2^-39 still counts in fp16
-          float top = 0.0f;
-#pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            const float x = fabsf(vf[e]);
-            if (x < INFINITY) top = fmaxf(top, x);
-            else vf[e] = __uint_as_float(0x7fc00000u);
-          }
-          top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
-          top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
-          if (top > sv) {  // the same in every lane
-            corr[0] *= sv / top;
-            corr[1] *= sv / top;
-            sv = top;
-          }
-          const float inv = kPBias / sv;
-          float y[2][4];
-#pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            const float f = vf[e] * inv;
-            y[0][e] = see[0][e] ? p[0][e] * f : 0.0f;
-            y[1][e] = see[1][e] ? p[1][e] * f : 0.0f;
-          }
-          pa[0] = pack_f16(y[0][0], y[0][1]);
-          pa[1] = pack_f16(y[1][0], y[1][1]);
-          pa[2] = pack_f16(y[0][2], y[0][3]);
-          pa[3] = pack_f16(y[1][2], y[1][3]);
-        }
-        if (__any_sync(0xffffffffu, corr[0] != 1.0f || corr[1] != 1.0f)) {
-#pragma unroll
-          for (int i = 0; i < DB; ++i) {
-            acc[i][0] *= corr[0];
-            acc[i][1] *= corr[0];
-            acc[i][2] *= corr[1];
-            acc[i][3] *= corr[1];
-          }
-        }
-        if constexpr (B16) {
-          const uint32_t va = st + (kTreeTile + (lane & 15)) * L::ROW + (lane >> 4) * 16;
-#pragma unroll
-          for (int i = 0; i < D / 16; ++i) {
-            uint32_t r0, r1, r2, r3;
-            ldsm_x4_t(va + 32 * i, r0, r1, r2, r3);
-            mma_bf16(acc[2 * i], pa[0], pa[1], pa[2], pa[3], r0, r1);
-            mma_bf16(acc[2 * i + 1], pa[0], pa[1], pa[2], pa[3], r2, r3);
-          }
-        } else {
-          // rows 2 t4, 2 t4 + 1 and those + 8 of columns DB g .. DB g + DB - 1: byte i of a
-          // row pair is the B operand of block i, whose column g is column DB g + i of O
-          uint32_t vw[4][DB / 4];
-#pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            if constexpr (D == 128) {
-              const uint4 x = lds128(st + kTreeTile * D + v_piece<D>(kk[e], g));
-              vw[e][0] = x.x, vw[e][1] = x.y, vw[e][2] = x.z, vw[e][3] = x.w;
-            } else {
-              const uint2 x = lds64(st + kTreeTile * D + v_piece<D>(kk[e], g >> 1) + 8 * (g & 1));
-              vw[e][0] = x.x, vw[e][1] = x.y;
-            }
-          }
-#pragma unroll
-          for (int i = 0; i < DB / 4; ++i) {
-#pragma unroll
-            for (int hh = 0; hh < 2; ++hh) {
-              const uint32_t sel = hh ? 0x7362u : 0x5140u;
-              const uint32_t x = __byte_perm(vw[0][i], vw[1][i], sel), y = __byte_perm(vw[2][i], vw[3][i], sel);
-              const int blk = 4 * i + 2 * hh;
-              mma_f16(acc[blk], pa[0], pa[1], pa[2], pa[3], codes_f16<FMT>(x), codes_f16<FMT>(y));
-              mma_f16(acc[blk + 1], pa[0], pa[1], pa[2], pa[3], codes_f16<FMT>(x >> 16), codes_f16<FMT>(y >> 16));
-            }
-          }
-        }
-        __syncwarp();  // every lane is done with the stage
-        if (issue(s)) ++issued;
-        else cp_async_commit();
-      }
-      // ---- this slice's partial of sequence b
-      const int64_t slot = ((int64_t)(kvh * a.nrg + rg) * (a.G + a.B) + slice + b) * kTreeRows;
-#pragma unroll
-      for (int r = 0; r < 2; ++r) {
-        l[r] += __shfl_xor_sync(0xffffffffu, l[r], 1);
-        l[r] += __shfl_xor_sync(0xffffffffu, l[r], 2);
-        const int row = g + 8 * r;
-        if (row >= r_end) continue;
-        if (t4 == 0) a.part_ml[slot + row] = make_float2(m[r], l[r]);
-        float* dst = a.part_acc + (slot + row) * D;
-        if constexpr (B16) {
-#pragma unroll
-          for (int i = 0; i < DB; ++i)
-            *reinterpret_cast<float2*>(dst + 8 * i + 2 * t4) = make_float2(acc[i][2 * r], acc[i][2 * r + 1]);
-        } else {
-          const float f = sv * (1.0f / kPBias);
-#pragma unroll
-          for (int e = 0; e < 2; ++e)
-#pragma unroll
-            for (int i = 0; i < DB; i += 4)
-              *reinterpret_cast<float4*>(dst + DB * (2 * t4 + e) + i) =
-                  make_float4(acc[i][2 * r + e] * f, acc[i + 1][2 * r + e] * f, acc[i + 2][2 * r + e] * f,
-                              acc[i + 3][2 * r + e] * f);
+        for (int c = 0; c < D / 16; ++c) {
+          qa[c][e] = pack_f16(f[4 * c] * up, f[4 * c + 1] * up);
+          qa[c][2 + e] = pack_f16(f[4 * c + 2] * up, f[4 * c + 3] * up);
         }
       }
     }
-  }
+    // ---- what any row of the group sees
+    const uint32_t many = __reduce_or_sync(0xffffffffu, mrow[0] | mrow[1]);
+    const int nearest = __reduce_min_sync(0xffffffffu, min(near[0], near[1]));
+    const uint32_t wlo = __reduce_or_sync(0xffffffffu, (uint32_t)(word[0] | word[1]));
+    const uint32_t whi = __reduce_or_sync(0xffffffffu, (uint32_t)((word[0] | word[1]) >> 32));
+    const uint64_t any_word = (uint64_t)whi << 32 | wlo;
+
+    // ---- listing: keys of [js, je) in blocks, tiles issued from a block's list
+    int jb = js, ncomp = 0, at = 0;
+    constexpr int MW = kTreeBlock / 32;
+    uint32_t mw[MW];
+#pragma unroll
+    for (int t = 0; t < MW; ++t) {
+      const int j = jb + 32 * t + lane;
+      mw[t] = j < je ? __ldg(M + j) : 0u;
+    }
+    const char* kb = reinterpret_cast<const char*>(a.kc) + ((int64_t)b * a.cap * kvrow + (int64_t)kvh * D) * ES;
+    const char* vb = reinterpret_cast<const char*>(a.vc) + ((int64_t)b * a.cap * kvrow + (int64_t)kvh * D) * ES;
+    const float* ksc = B16 ? nullptr : a.ks + ((int64_t)b * a.H_kv + kvh) * a.cap;
+    const float* vsc = B16 ? nullptr : a.vs + ((int64_t)b * a.H_kv + kvh) * a.cap;
+
+    auto issue = [&](int s) -> bool {
+      while (at >= ncomp) {
+        if (jb >= je) return false;
+        ncomp = 0;
+#pragma unroll
+        for (int t = 0; t < MW; ++t) {
+          const int j = jb + 32 * t + lane;
+          bool ok = j < je;
+          if (ok) {
+            if (j < len) {
+              ok = j >= nearest || (mw[t] & many) != 0u;
+            } else {
+              const int u = j - len;
+              ok = (any_word >> u & 1ull) != 0ull;
+              if (ok && one_token)  // the window among drafted tokens: by their depths
+                ok = len + __popcll(tree_word(a, b, u)) - 1 >= nearest || (mw[t] & many) != 0u;
+            }
+          }
+          const unsigned bal = __ballot_sync(0xffffffffu, ok);
+          if (ok) {
+            const int x = ncomp + __popc(bal & lanemask_lt());
+            idx[x] = j;
+            msk[x] = mw[t];
+          }
+          ncomp += __popc(bal);
+        }
+        jb += kTreeBlock;
+#pragma unroll
+        for (int t = 0; t < MW; ++t) {  // the next block's words, in flight meanwhile
+          const int j = jb + 32 * t + lane;
+          mw[t] = j < je ? __ldg(M + j) : 0u;
+        }
+        at = 0;
+        __syncwarp();
+      }
+      const int n = min(kTreeTile, ncomp - at);
+      const uint32_t st = ring + s * L::STAGE;
+      if (lane == 0) cnt[s] = n;
+      if (lane < n) {
+        int* key = reinterpret_cast<int*>(smem + s * L::STAGE + L::OFF_KEY);
+        key[lane] = idx[at + lane];
+        key[kTreeTile + lane] = (int)msk[at + lane];
+      }
+      constexpr int CH = D * ES / 16, RPI = 32 / CH;  // 16-byte pieces per row, rows per instruction
+      const int ch = lane % CH;
+      for (int rr = lane / CH; rr < n; rr += RPI) {
+        const int64_t off = (int64_t)idx[at + rr] * kvrow * ES + 16 * ch;
+        if constexpr (B16) {
+          cp_async16(st + rr * L::ROW + 16 * ch, kb + off);
+          cp_async16(st + (kTreeTile + rr) * L::ROW + 16 * ch, vb + off);
+        } else {
+          cp_async16(st + k_piece<D>(rr, ch), kb + off);
+          cp_async16(st + kTreeTile * D + v_piece<D>(rr, ch), vb + off);
+        }
+      }
+      if constexpr (!B16) {
+        const int rr = lane & 15;
+        if (rr < n) cp_async4(st + L::OFF_SCALE + 4 * lane, (lane < 16 ? ksc : vsc) + idx[at + rr]);
+      }
+      cp_async_commit();
+      at += n;
+      return true;
+    };
+
+    float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.0f, 0.0f};
+    float acc[DB][4];
+#pragma unroll
+    for (int i = 0; i < DB; ++i)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) acc[i][e] = 0.0f;
+    __syncwarp();  // zeroed stages (and the last stretch's reads) before the first copy
+    int issued = 0;  // one copy group per stage and per refill, empty or not
+    for (int s = 0; s < L::STAGES; ++s) {
+      if (issue(s)) ++issued;
+      else cp_async_commit();
+    }
+    for (int t = 0; t < issued; ++t) {
+      const int s = t % L::STAGES;
+      cp_async_wait<L::STAGES - 1>();  // tile t's group has landed (this lane's copies)
+      __syncwarp();                    // ... and every lane's
+      const int n = cnt[s];
+      const uint32_t st = ring + s * L::STAGE;
+      float c0[4] = {0.0f, 0.0f, 0.0f, 0.0f}, c1[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+      if constexpr (B16) {
+        const uint32_t ka = st + ((lane & 7) + ((lane >> 4) << 3)) * L::ROW + ((lane >> 3) & 1) * 16;
+#pragma unroll
+        for (int c = 0; c < D / 16; ++c) {
+          uint32_t r0, r1, r2, r3;
+          ldsm_x4(ka + 32 * c, r0, r1, r2, r3);
+          mma_bf16(c0, qa[c][0], qa[c][1], qa[c][2], qa[c][3], r0, r1);
+          mma_bf16(c1, qa[c][0], qa[c][1], qa[c][2], qa[c][3], r2, r3);
+        }
+      } else {
+#pragma unroll
+        for (int c = 0; c < D / 64; ++c) {
+          const uint4 x = lds128(st + k_piece<D>(g, 4 * c + t4));
+          const uint4 y = lds128(st + k_piece<D>(g + 8, 4 * c + t4));
+          const uint32_t xw[4] = {x.x, x.y, x.z, x.w}, yw[4] = {y.x, y.y, y.z, y.w};
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const uint32_t* A = qa[4 * c + i];
+            mma_f16(c0, A[0], A[1], A[2], A[3], codes_f16<FMT>(xw[i]), codes_f16<FMT>(xw[i] >> 16));
+            mma_f16(c1, A[0], A[1], A[2], A[3], codes_f16<FMT>(yw[i]), codes_f16<FMT>(yw[i] >> 16));
+          }
+        }
+      }
+      // ---- logits of rows g, g + 8 and keys 2 t4, 2 t4 + 1, 8 + 2 t4, 9 + 2 t4
+      const int kk[4] = {2 * t4, 2 * t4 + 1, 2 * t4 + 8, 2 * t4 + 9};
+      float sx[2][4] = {{c0[0], c0[1], c1[0], c1[1]}, {c0[2], c0[3], c1[2], c1[3]}};
+      float kf[4] = {1.0f, 1.0f, 1.0f, 1.0f}, vf[4], lv[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+      if constexpr (!B16) {
+        const float* sc = reinterpret_cast<const float*>(smem + s * L::STAGE + L::OFF_SCALE);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          kf[e] = sc[kk[e]];
+          vf[e] = kk[e] < n ? sc[kTreeTile + kk[e]] : 0.0f;
+          if (!(fabsf(vf[e]) < INFINITY)) vf[e] = __uint_as_float(0x7fc00000u);
+          // 8-bit formats: V's scales join P before it is rounded to fp16.  The reference m of
+          // a row is that of the product: the largest P vs of the keys that it sees is 2^14,
+          // so that what is smaller by up to 2^-38 still counts.
+          lv[e] = __log2f(fmaxf(fabsf(vf[e]), kTinyScale)) - kPTop;
+        }
+      }
+      bool see[2][4];
+#pragma unroll
+      for (int e = 0; e < 4; ++e) see[0][e] = see[1][e] = kk[e] < n;
+      if (!one_token) {
+        const int* key = reinterpret_cast<const int*>(smem + s * L::STAGE + L::OFF_KEY);
+        const bool drafts = key[n - 1] >= len;  // slots ascend in a list
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          if (kk[e] >= n) continue;
+          const int j = key[kk[e]];
+          const uint32_t mk = (uint32_t)key[kTreeTile + kk[e]];
+          int p = j;
+          uint64_t bit = ~0ull;
+          if (drafts && j >= len) {
+            p = len + __popcll(tree_word(a, b, j - len)) - 1;
+            bit = 1ull << (j - len);
+          }
+#pragma unroll
+          for (int r = 0; r < 2; ++r)
+            see[r][e] = (word[r] & bit) != 0ull && (p >= near[r] || (mk & mrow[r]) != 0u);
+        }
+      }
+      float corr[2];
+      float p[2][4];
+#pragma unroll
+      for (int r = 0; r < 2; ++r) {
+#pragma unroll
+        for (int e = 0; e < 4; ++e) sx[r][e] = see[r][e] ? sx[r][e] * kf[e] * fac[r] : -INFINITY;
+        float mt = fmaxf(fmaxf(sx[r][0] + lv[0], sx[r][1] + lv[1]), fmaxf(sx[r][2] + lv[2], sx[r][3] + lv[3]));
+        mt = fmaxf(mt, __shfl_xor_sync(0xffffffffu, mt, 1));
+        mt = fmaxf(mt, __shfl_xor_sync(0xffffffffu, mt, 2));
+        const float mn = fmaxf(m[r], mt);
+        const float mu = mn == -INFINITY ? 0.0f : mn;  // a row without a key so far
+        corr[r] = ex2(m[r] - mu);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) p[r][e] = ex2(sx[r][e] - mu);
+        l[r] = l[r] * corr[r] + ((p[r][0] + p[r][1]) + (p[r][2] + p[r][3]));
+        m[r] = mn;
+      }
+      uint32_t pa[4];
+      if constexpr (B16) {
+        // P rounded to bf16 for the tensor core, as in the forward pass; l sums it unrounded
+        pa[0] = pack_bf16(p[0][0], p[0][1]);
+        pa[1] = pack_bf16(p[1][0], p[1][1]);
+        pa[2] = pack_bf16(p[0][2], p[0][3]);
+        pa[3] = pack_bf16(p[1][2], p[1][3]);
+      } else {
+        float y[2][4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          y[0][e] = see[0][e] ? p[0][e] * vf[e] : 0.0f;
+          y[1][e] = see[1][e] ? p[1][e] * vf[e] : 0.0f;
+        }
+        pa[0] = pack_f16(y[0][0], y[0][1]);
+        pa[1] = pack_f16(y[1][0], y[1][1]);
+        pa[2] = pack_f16(y[0][2], y[0][3]);
+        pa[3] = pack_f16(y[1][2], y[1][3]);
+      }
+      if (__any_sync(0xffffffffu, corr[0] != 1.0f || corr[1] != 1.0f)) {
+#pragma unroll
+        for (int i = 0; i < DB; ++i) {
+          acc[i][0] *= corr[0];
+          acc[i][1] *= corr[0];
+          acc[i][2] *= corr[1];
+          acc[i][3] *= corr[1];
+        }
+      }
+      if constexpr (B16) {
+        const uint32_t va = st + (kTreeTile + (lane & 15)) * L::ROW + (lane >> 4) * 16;
+#pragma unroll
+        for (int i = 0; i < D / 16; ++i) {
+          uint32_t r0, r1, r2, r3;
+          ldsm_x4_t(va + 32 * i, r0, r1, r2, r3);
+          mma_bf16(acc[2 * i], pa[0], pa[1], pa[2], pa[3], r0, r1);
+          mma_bf16(acc[2 * i + 1], pa[0], pa[1], pa[2], pa[3], r2, r3);
+        }
+      } else {
+        // rows 2 t4, 2 t4 + 1 and those + 8 of columns DB g .. DB g + DB - 1: byte i of a
+        // row pair is the B operand of block i, whose column g is column DB g + i of O
+        uint32_t vw[4][DB / 4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          if constexpr (D == 128) {
+            const uint4 x = lds128(st + kTreeTile * D + v_piece<D>(kk[e], g));
+            vw[e][0] = x.x, vw[e][1] = x.y, vw[e][2] = x.z, vw[e][3] = x.w;
+          } else {
+            const uint2 x = lds64(st + kTreeTile * D + v_piece<D>(kk[e], g >> 1) + 8 * (g & 1));
+            vw[e][0] = x.x, vw[e][1] = x.y;
+          }
+        }
+#pragma unroll
+        for (int i = 0; i < DB / 4; ++i) {
+#pragma unroll
+          for (int hh = 0; hh < 2; ++hh) {
+            const uint32_t sel = hh ? 0x7362u : 0x5140u;
+            const uint32_t x = __byte_perm(vw[0][i], vw[1][i], sel), y = __byte_perm(vw[2][i], vw[3][i], sel);
+            const int blk = 4 * i + 2 * hh;
+            mma_f16(acc[blk], pa[0], pa[1], pa[2], pa[3], codes_f16<FMT>(x), codes_f16<FMT>(y));
+            mma_f16(acc[blk + 1], pa[0], pa[1], pa[2], pa[3], codes_f16<FMT>(x >> 16), codes_f16<FMT>(y >> 16));
+          }
+        }
+      }
+      __syncwarp();  // every lane is done with the stage
+      if (issue(s)) ++issued;
+      else cp_async_commit();
+    }
+    // ---- this segment's partial
+    const int64_t slot = partial * kTreeRows;
+#pragma unroll
+    for (int r = 0; r < 2; ++r) {
+      l[r] += __shfl_xor_sync(0xffffffffu, l[r], 1);
+      l[r] += __shfl_xor_sync(0xffffffffu, l[r], 2);
+      const int row = g + 8 * r;
+      if (row >= r_end) continue;
+      if (t4 == 0) a.part_ml[slot + row] = make_float2(m[r], l[r]);
+      float* dst = a.part_acc + (slot + row) * D;
+      if constexpr (B16) {
+#pragma unroll
+        for (int i = 0; i < DB; ++i)
+          *reinterpret_cast<float2*>(dst + 8 * i + 2 * t4) = make_float2(acc[i][2 * r], acc[i][2 * r + 1]);
+      } else {
+#pragma unroll
+        for (int e = 0; e < 2; ++e)
+#pragma unroll
+          for (int i = 0; i < DB; i += 4)
+            *reinterpret_cast<float4*>(dst + DB * (2 * t4 + e) + i) =
+                make_float4(acc[i][2 * r + e], acc[i + 1][2 * r + e], acc[i + 2][2 * r + e], acc[i + 3][2 * r + e]);
+      }
+    }
+  });
 }
 
 // ------------------------------------------------------------------------ combine --
@@ -620,9 +486,9 @@ __device__ __noinline__ float row_by_hand(const TreeArgs& a, int b, int t, int h
   return out;
 }
 
-// Merge the slices of one row: grid (T * H, B).  Warp g folds slices g (mod the warps) into
-// a running (max, sum, acc), a lane D / 32 columns; then every thread folds the warps'
-// results in order.  A programmatic dependent of tree_split: it waits for its results.
+// Merge the partials of one row: grid (T * H, B).  Warp g folds partials g (mod the warps)
+// into a running (max, sum, acc), a lane D / 32 columns; then every thread folds the warps'
+// results in order.  A programmatic dependent of the kernel that writes the partials.
 template <int D, int FMT>
 __global__ void __launch_bounds__(32 * kTreeCombWarps) tree_combine(const __grid_constant__ TreeArgs a) {
   constexpr int CPL = D / 32, W = kTreeCombWarps;
@@ -631,7 +497,8 @@ __global__ void __launch_bounds__(32 * kTreeCombWarps) tree_combine(const __grid
   __shared__ float weight[33 * W];
   const int g = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int b = blockIdx.y, t = blockIdx.x / a.H, h = blockIdx.x % a.H;
-  const int kvh = h / a.gq, row = t * a.gq + h % a.gq, rg = row / kTreeRows;
+  const int kvh = h / a.gq, row = t * a.gq + h % a.gq, rg = row / a.grp;
+  const int64_t ln = (int64_t)kvh * a.nrg + rg;
   int64_t total = 0, from = 0;  // all sequences' weight, and that before sequence b
   bool bad = false;
   for (int x = lane; x < a.B; x += 32) {
@@ -642,23 +509,31 @@ __global__ void __launch_bounds__(32 * kTreeCombWarps) tree_combine(const __grid
     from += x < b ? wgt : 0;
   }
   total = warp_sum(total);
-  from = warp_sum(from);
+  from = warp_sum(from) + ln * total;
   bad = __any_sync(0xffffffffu, bad);
   const int len = __ldg(a.lens + b);
   const Stretch s = stretch_of(a, len);
-  const int ns = slices_of(a, total);
+  const int64_t whole = total * a.H_kv * a.nrg;
+  const int ns = slices_of(a, whole);
   asm volatile("griddepcontrol.wait;" ::: "memory");
-  if (blockIdx.x == 0 && b == 0 && threadIdx.x == 0) *a.status = bad ? FOCUS_ERR_BOUNDS : 0;
+  if (blockIdx.x == 0 && b == 0 && g == 0) {  // the call's status
+    int code = 0;
+    if (a.flags && total > 0)
+      for (int x = lane; x < ns; x += 32) code = min(code, a.flags[x]);
+    code = __reduce_min_sync(0xffffffffu, code);
+    if (lane == 0) *a.status = code ? code : bad ? FOCUS_ERR_BOUNDS : 0;
+  }
   float m = -INFINITY, l = 0.0f, acc[CPL];
 #pragma unroll
   for (int e = 0; e < CPL; ++e) acc[e] = 0.0f;
-  if (s.units > 0) {
-    const int64_t first = max((int64_t)0, from * ns / total - 1);
-    const int64_t last = min((int64_t)ns - 1, (from + s.weight) * ns / total + 1);
-    for (int64_t c = first + g; c <= last; c += W) {
-      const int64_t lo = total * c / ns, hi = total * (c + 1) / ns;
+  if (s.units > 0 && tree_word(a, b, t) != 0ull) {
+    const int64_t first = max((int64_t)0, from * ns / whole - 1);
+    const int64_t last = min((int64_t)ns - 1, (from + s.weight) * ns / whole + 1);
+    for (int64_t c = first * a.parts + g; c < (last + 1) * a.parts; c += W) {
+      const int64_t sl = c / a.parts;
+      const int64_t lo = whole * sl / ns, hi = whole * (sl + 1) / ns;
       if (units_before(a, s, lo - from) >= units_before(a, s, hi - from)) continue;  // no such partial
-      const int64_t slot = ((int64_t)(kvh * a.nrg + rg) * (a.G + a.B) + c + b) * kTreeRows + row % kTreeRows;
+      const int64_t slot = ((sl + ln * a.B + b) * a.parts + c % a.parts) * a.grp + row % a.grp;
       const float2 x = a.part_ml[slot];
       if (x.y == 0.0f) continue;  // no key of the slice is seen
       float v[CPL];
@@ -695,37 +570,53 @@ __global__ void __launch_bounds__(32 * kTreeCombWarps) tree_combine(const __grid
 }
 
 // ------------------------------------------------------------------------- launch --
+constexpr int kTreeTcRows = 128;  // rows per CTA of the tensor-core kernel (the MMA's M)
+constexpr int kTreeTcSlices = 152;
+constexpr int kTreeTcMinUnits = 16;
+
 struct TreePlan {
-  int gq, rows, nrg, G, wfar;
-  size_t ml, acc, total;  // offsets and size of the workspace
+  int gq, rows, grp, nrg, parts, G, min_weight, wfar;
+  bool tc;
+  size_t flags, ml, acc, total;  // offsets and size of the workspace
 };
 
 TreePlan tree_plan(const focus_cache_params& p) {
   TreePlan t;
   t.gq = p.H / p.H_kv;
   t.rows = p.T * t.gq;
-  t.nrg = (t.rows + kTreeRows - 1) / kTreeRows;
+  t.tc = t.rows > kTreeRows;
+  t.grp = t.tc ? kTreeTcRows : kTreeRows;
+  t.nrg = (t.rows + t.grp - 1) / t.grp;
+  t.parts = t.tc ? kTreeTcParts : 1;
+  t.G = t.tc ? kTreeTcSlices : kTreeWarps;
+  t.min_weight = (t.tc ? kTreeTcMinUnits : kTreeMinUnits) * kTreeNear;
   const int64_t lanes = (int64_t)p.H_kv * t.nrg;
-  const int64_t units = (int64_t)p.B * ((p.cap + kTreeUnit - 1) / kTreeUnit);
-  t.G = (int)std::max<int64_t>(1, std::min<int64_t>(kTreeWarps / lanes, (units + kTreeMinUnits - 1) / kTreeMinUnits));
+  const int64_t most = lanes * p.B * (((int64_t)p.cap + kTreeUnit - 1) / kTreeUnit) * kTreeNear;
+  t.G = (int)std::max<int64_t>(1, std::min<int64_t>(t.G, most / t.min_weight));
   // expected share of the far keys that some drafted token's mask meets (balance only)
   double miss = 1.0;
   for (int i = 0; i < p.top_k; ++i) miss *= std::max(0.0, (double)(p.K - p.top_k - i)) / (p.K - i);
   t.wfar = std::max(1, (int)std::lround(kTreeNear * (1.0 - pow(miss, p.T))));
-  const size_t slots = (size_t)lanes * (t.G + p.B) * kTreeRows;
-  t.ml = 256;
+  const size_t slots = (size_t)(t.G + lanes * p.B) * t.parts * t.grp;
+  t.flags = 256;
+  t.ml = t.flags + align_up(sizeof(int32_t) * t.G, 256);
   t.acc = t.ml + align_up(sizeof(float2) * slots, 256);
   t.total = t.acc + align_up(sizeof(float) * slots * p.d_head, 256);
   return t;
 }
 
 template <int D, int FMT>
-cudaError_t launch_tree(const TreeArgs& a, cudaStream_t s) {
+cudaError_t launch_tree(const TreeArgs& a, bool tc, cudaStream_t s) {
   using L = TreeLayout<D, FMT>;
-  cudaError_t e = cudaFuncSetAttribute(tree_split<D, FMT>, cudaFuncAttributePreferredSharedMemoryCarveout, 100);
-  if (e != cudaSuccess) return e;
-  tree_split<D, FMT><<<dim3((unsigned)a.G, (unsigned)(a.H_kv * a.nrg)), 32, L::BYTES, s>>>(a);
-  if ((e = cudaGetLastError()) != cudaSuccess) return e;
+  cudaError_t e;
+  if (tc) {
+    if ((e = launch_tree_tc(a, D, FMT, s)) != cudaSuccess) return e;
+  } else {
+    e = cudaFuncSetAttribute(tree_split<D, FMT>, cudaFuncAttributePreferredSharedMemoryCarveout, 100);
+    if (e != cudaSuccess) return e;
+    tree_split<D, FMT><<<(unsigned)a.G, 32, L::BYTES, s>>>(a);
+    if ((e = cudaGetLastError()) != cudaSuccess) return e;
+  }
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)(a.T * a.H), (unsigned)a.B);
   cfg.blockDim = dim3(32 * kTreeCombWarps);
@@ -752,17 +643,19 @@ cudaError_t launch_decode_tree(const focus_cache_params& p, const bf16* q, const
   a.q = q, a.kc = kc, a.vc = vc, a.ks = ks, a.vs = vs, a.mask = mask, a.lens = lens, a.tree = tree;
   a.part_ml = reinterpret_cast<float2*>(ws + t.ml);
   a.part_acc = reinterpret_cast<float*>(ws + t.acc);
+  a.flags = t.tc ? reinterpret_cast<int32_t*>(ws + t.flags) : nullptr;
   a.o = o, a.lse = lse, a.status = reinterpret_cast<int32_t*>(ws);
   a.B = p.B, a.cap = p.cap, a.T = p.T, a.H = p.H, a.H_kv = p.H_kv, a.R = p.R, a.w = p.w;
-  a.gq = t.gq, a.rows = t.rows, a.nrg = t.nrg, a.G = t.G, a.wfar = t.wfar;
+  a.gq = t.gq, a.rows = t.rows, a.grp = t.grp, a.nrg = t.nrg, a.parts = t.parts;
+  a.G = t.G, a.min_weight = t.min_weight, a.wfar = t.wfar;
   a.sl2 = scale * kLog2e;
   if (p.d_head == 64)
-    return p.format == FOCUS_CACHE_BF16   ? launch_tree<64, FOCUS_CACHE_BF16>(a, s)
-           : p.format == FOCUS_CACHE_E4M3 ? launch_tree<64, FOCUS_CACHE_E4M3>(a, s)
-                                          : launch_tree<64, FOCUS_CACHE_INT8>(a, s);
-  return p.format == FOCUS_CACHE_BF16   ? launch_tree<128, FOCUS_CACHE_BF16>(a, s)
-         : p.format == FOCUS_CACHE_E4M3 ? launch_tree<128, FOCUS_CACHE_E4M3>(a, s)
-                                        : launch_tree<128, FOCUS_CACHE_INT8>(a, s);
+    return p.format == FOCUS_CACHE_BF16   ? launch_tree<64, FOCUS_CACHE_BF16>(a, t.tc, s)
+           : p.format == FOCUS_CACHE_E4M3 ? launch_tree<64, FOCUS_CACHE_E4M3>(a, t.tc, s)
+                                          : launch_tree<64, FOCUS_CACHE_INT8>(a, t.tc, s);
+  return p.format == FOCUS_CACHE_BF16   ? launch_tree<128, FOCUS_CACHE_BF16>(a, t.tc, s)
+         : p.format == FOCUS_CACHE_E4M3 ? launch_tree<128, FOCUS_CACHE_E4M3>(a, t.tc, s)
+                                        : launch_tree<128, FOCUS_CACHE_INT8>(a, t.tc, s);
 }
 
 }  // namespace focus

@@ -1,0 +1,161 @@
+// Decode of drafted tokens over a cache: what its two kernels (tree.cu, tree_tc.cu) share.
+// Parameters, the row of work units that is cut into slices, the draft tree's words.
+#pragma once
+
+#include <cuda_fp8.h>
+#include <limits.h>
+
+#include "common.cuh"
+
+namespace focus {
+
+constexpr int kTreeUnit = 32;        // keys per unit of work
+constexpr int kTreeNear = 64;        // weight of a unit near the window
+constexpr int kTreeTcParts = 2;      // partials per segment of the tensor-core kernel
+// 8-bit formats: V scales count as at least 2^-80 where the reference of the exponentials is
+// chosen, so that a row of (next to) zeros cannot push the sum of exponentials out of fp32.
+constexpr float kTinyScale = 8.271806e-25f;
+
+struct TreeArgs {
+  const bf16* q;
+  const void *kc, *vc;
+  const float *ks, *vs;
+  const uint32_t* mask;
+  const int32_t* lens;
+  const uint64_t* tree;
+  float2* part_ml;   // [partial][group rows] (max, sum)
+  float* part_acc;   // [partial][group rows][D]
+  int32_t* flags;    // [slice] what went wrong in it (tensor-core kernel)
+  bf16* o;
+  float* lse;
+  int32_t* status;
+  int B, cap, T, H, H_kv, R, w, gq, rows;
+  int grp, nrg;      // rows per row group (16 or 128), row groups
+  int parts;         // partials per segment
+  int G, min_weight; // slices at most, least weight of one
+  int wfar;
+  float sl2;         // softmax scale * log2(e)
+};
+
+// ------------------------------------------------------------- the row of units --
+// Host and device agree only on the cache's capacity; the lengths are known to the device
+// alone.  Keys come in units of 32 with an integer weight each: far units (no key of them
+// is near any drafted token's window) of weight wfar, the expected share of matching masks,
+// then near units of weight kTreeNear up to the last drafted token.  All units of all
+// sequences, once per (KV head, row group), stand in one row that is cut into slices of
+// equal weight, so that a batch of one long and many short sequences keeps the GPU busy.
+// A segment is what a slice has of one (KV head, row group, sequence).  Going along the
+// row, each new segment begins a new slice or a new sequence: slice + sequence number is
+// different for each and numbers its partial results.
+struct Stretch {
+  int units, far;
+  int64_t weight;
+};
+__device__ __forceinline__ bool len_ok(const TreeArgs& a, int len) { return len >= 0 && len <= a.cap - a.T; }
+__device__ __forceinline__ Stretch stretch_of(const TreeArgs& a, int len) {
+  Stretch s{0, 0, 0};
+  if (!len_ok(a, len)) return s;
+  s.units = (len + a.T + kTreeUnit - 1) / kTreeUnit;
+  s.far = max(0, len - a.w + 1) / kTreeUnit;
+  s.weight = (int64_t)s.far * a.wfar + (int64_t)(s.units - s.far) * kTreeNear;
+  return s;
+}
+// Units of a stretch that begin before weight x.
+__device__ __forceinline__ int units_before(const TreeArgs& a, const Stretch& s, int64_t x) {
+  if (x <= 0) return 0;
+  const int64_t wf = (int64_t)s.far * a.wfar;
+  const int64_t u = x <= wf ? (x + a.wfar - 1) / a.wfar : s.far + (x - wf + kTreeNear - 1) / kTreeNear;
+  return (int)min((int64_t)s.units, u);
+}
+__device__ __forceinline__ int64_t warp_sum(int64_t x) {
+#pragma unroll
+  for (int o = 16; o; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
+  return x;
+}
+__device__ __forceinline__ int64_t warp_scan(int64_t x, int lane) {  // inclusive
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int64_t y = __shfl_up_sync(0xffffffffu, x, o);
+    if (lane >= o) x += y;
+  }
+  return x;
+}
+// All sequences' weight for one (KV head, row group), and the slices of the whole row.
+__device__ __forceinline__ int64_t total_weight(const TreeArgs& a, int lane) {
+  int64_t t = 0;
+  for (int b = lane; b < a.B; b += 32) t += stretch_of(a, __ldg(a.lens + b)).weight;
+  return warp_sum(t);
+}
+__device__ __forceinline__ int slices_of(const TreeArgs& a, int64_t row_weight) {
+  return (int)max((int64_t)1, min((int64_t)a.G, row_weight / a.min_weight));
+}
+
+// Calls f(number of the partial, KV head, row group, sequence, its length, first key, end)
+// for the segments of a slice, in order; a whole warp.
+template <typename F>
+__device__ __forceinline__ void for_segments(const TreeArgs& a, int slice, int lane, F&& f) {
+  const int64_t W = total_weight(a, lane), row = W * a.H_kv * a.nrg;
+  const int ns = slices_of(a, row);
+  if (W == 0 || slice >= ns) return;
+  const int64_t lo = row * slice / ns, hi = row * (slice + 1) / ns;
+  for (int64_t ln = lo / W; ln * W < hi; ++ln) {
+    int64_t before = ln * W;
+    const int rg = (int)(ln % a.nrg), kvh = (int)(ln / a.nrg);
+    for (int bc = 0; bc < a.B && before < hi; bc += 32) {
+      const int lb = bc + lane < a.B ? __ldg(a.lens + bc + lane) : -1;
+      const Stretch mine = stretch_of(a, lb);
+      const int64_t upto = warp_scan(mine.weight, lane);
+      const int64_t from = before + upto - mine.weight;
+      const int my0 = units_before(a, mine, lo - from), my1 = units_before(a, mine, hi - from);
+      before += __shfl_sync(0xffffffffu, upto, 31);
+      unsigned todo = __ballot_sync(0xffffffffu, my0 < my1);
+      while (todo) {
+        const int src = __ffs(todo) - 1;
+        todo &= todo - 1;
+        const int b = bc + src;
+        const int len = __shfl_sync(0xffffffffu, lb, src);
+        const int js = __shfl_sync(0xffffffffu, my0, src) * kTreeUnit;
+        const int je = min(len + a.T, __shfl_sync(0xffffffffu, my1, src) * kTreeUnit);
+        f(slice + ln * a.B + b, kvh, rg, b, len, js, je);
+      }
+    }
+  }
+}
+
+// Ancestors of drafted token t (itself among them), bits from T on cleared.
+__device__ __forceinline__ uint64_t tree_word(const TreeArgs& a, int b, int t) {
+  const uint64_t all = a.T == 64 ? ~0ull : (1ull << a.T) - 1;
+  return (a.tree ? __ldg(reinterpret_cast<const unsigned long long*>(a.tree) + (int64_t)b * a.T + t)
+                 : (2ull << t) - 1) &
+         all;
+}
+
+// Two 8-bit codes (low half of `two`) as a pair of fp16; exact.
+template <int FMT>
+__device__ __forceinline__ uint32_t codes_f16(uint32_t two) {
+  if constexpr (FMT == FOCUS_CACHE_E4M3) {
+    const __half2_raw r = __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)(two & 0xffffu), __NV_E4M3);
+    return *reinterpret_cast<const uint32_t*>(&r);
+  } else {
+    // 0x6400 | (c + 128) is 1024 + c + 128 in fp16
+    const uint32_t h = __byte_perm(two ^ 0x8080u, 0x64646464u, 0x4140);
+    const __half2 r = __hsub2(*reinterpret_cast<const __half2*>(&h), __float2half2_rn(1152.0f));
+    return *reinterpret_cast<const uint32_t*>(&r);
+  }
+}
+
+// fp16 operands of a bf16 query row (8-bit formats): the row is multiplied by the power of
+// two that brings its largest magnitude into [1, 2), which keeps every bf16 digit down to
+// 2^-24 of that maximum; the logits are multiplied back.  A row with a NaN or an infinity
+// stays as it is (its results are NaN either way).
+__device__ __forceinline__ void row_unit(float largest, float& up, float& down) {
+  uint32_t ex = __float_as_uint(largest) >> 23;
+  ex = ex == 0u || ex >= 254u ? 127u : ex;
+  up = __uint_as_float((254u - ex) << 23);
+  down = __uint_as_float(ex << 23);
+}
+
+// tree_tc.cu
+cudaError_t launch_tree_tc(const TreeArgs& a, int d_head, int format, cudaStream_t s);
+
+}  // namespace focus

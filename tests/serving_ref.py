@@ -49,16 +49,18 @@ def dequantise(codes, scale):
     return x if scale is None else x * scale.cpu().double().transpose(1, 2)[..., None]
 
 
-def decode_tree(q, k, v, mask, lens, words, *, w, R, scale=None):
+def decode_tree(q, k, v, mask, lens, words, *, w, R, scale=None, vs=None):
     """q [B, T, H, d]; k, v [B, cap, H_kv, d] float64; mask [B, R, cap]; lens, words: lists.
     Returns float64 o [B, T, H, d], lse [B, H, T], and per output the magnitudes
-    m = sum_j p_j |v_j| (as o) and s = max_j sum_c |q_c k_jc| scale (as lse)."""
+    m = sum_j p_j |v_j| (as o), s = max_j sum_c |q_c k_jc| scale (as lse) and, with the
+    scales vs [B, H_kv, cap] of an 8-bit cache, z = max_j (p_j vs_j) sum_j |code_j| (as o)."""
     B, T, H, d = q.shape
     H_kv = k.shape[2]
     scale = scale or 1 / math.sqrt(d)
     q = q.cpu().double()
     mask = mask.cpu().long() & 0xffffffff
     o, m = torch.zeros(B, T, H, d, dtype=torch.float64), torch.zeros(B, T, H, d, dtype=torch.float64)
+    zz = torch.zeros(B, T, H, d, dtype=torch.float64)
     lse, s = torch.full((B, H, T), -math.inf, dtype=torch.float64), torch.zeros(B, H, T, dtype=torch.float64)
     for b in range(B):
         n = int(lens[b])
@@ -85,8 +87,12 @@ def decode_tree(q, k, v, mask, lens, words, *, w, R, scale=None):
                 p = (z - lse[b, h, t]).exp()
                 o[b, t, h] = p @ vv
                 m[b, t, h] = p @ vv.abs()
+                if vs is not None:
+                    size = vs[b, kvh, keys].cpu().double()
+                    code = vv.abs() / size.clamp(min=1e-300)[:, None]
+                    zz[b, t, h] = (p * size).max() * code.sum(0)
                 s[b, h, t] = (kk.abs() @ q[b, t, h].abs()).max() * scale
-    return o, lse, m, s
+    return o, lse, m, s, zz
 
 
 def random_tree(rng, T, reach=8):

@@ -153,7 +153,7 @@ def test_reference_pins():
     mask = torch.ones(1, 1, 10, dtype=torch.int32)
     chain = [[1, 3, 7]]
     for w, m in ((1 << 30, 0 * mask), (1, mask)):
-        o, lse, _, _ = ref.decode_tree(q, k, v, m, [7], chain, w=w, R=1)
+        o, lse, _, _, _ = ref.decode_tree(q, k, v, m, [7], chain, w=w, R=1)
         bias = torch.full((3, 10), -math.inf, dtype=torch.float64).triu(8)
         want = torch.nn.functional.scaled_dot_product_attention(
             q.transpose(1, 2), k.transpose(1, 2), v.transpose(1, 2), attn_mask=bias).transpose(1, 2)
