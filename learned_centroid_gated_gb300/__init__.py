@@ -16,7 +16,6 @@ from __future__ import annotations
 
 import ctypes
 import dataclasses
-import functools
 import math
 import os
 import re
@@ -507,34 +506,28 @@ class Rope:
         object.__setattr__(self, "_addr", ctypes.addressof(plan))
 
 
-def _strides_of(t: torch.Tensor):
-    """focus_strides of a [B, N, H, d] tensor, None where it is dense."""
-    if t.is_contiguous():
-        return None
-    return ctypes.byref(_Strides(t.stride(0), t.stride(1), t.stride(2)))
-
-
-def _on(t: torch.Tensor, stream):
-    """The raw stream to launch on for tensor t: `stream`, or the current one of t's device."""
-    if stream is None:
-        return torch.cuda.current_stream(t.device).cuda_stream
-    return stream.cuda_stream
+# Device and stream look-ups of the serving calls, which a program makes for every token:
+# the raw forms where this torch has them.
+_current_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
+    lambda index: torch.cuda.current_stream(index).cuda_stream)
 
 
 class _Launch:
     """Makes the device of a call's tensors current, and the stream that it runs on, so
-    that what is allocated meanwhile belongs to that stream."""
+    that what is allocated meanwhile belongs to that stream; gives the raw stream."""
 
-    def __init__(self, t: torch.Tensor, stream):
-        here = torch.cuda.current_device() == t.device.index
-        self.device = None if here else torch.cuda.device(t.device)
+    def __init__(self, index: int, stream):
+        self.index = index
+        self.device = None if _current_device() == index else torch.cuda.device(index)
         self.stream = None if stream is None else torch.cuda.stream(stream)
 
-    def __enter__(self):
+    def __enter__(self) -> int:
         if self.device is not None:
             self.device.__enter__()
         if self.stream is not None:
             self.stream.__enter__()
+        return _raw_stream(self.index)
 
     def __exit__(self, *exc):
         if self.stream is not None:
@@ -543,32 +536,46 @@ class _Launch:
             self.device.__exit__(*exc)
 
 
+def _strides_of(t: torch.Tensor):
+    """focus_strides of a [B, N, H, d] tensor, None where it is dense."""
+    return None if t.is_contiguous() else ctypes.byref(_Strides(*t.stride()[:3]))
+
+
 def _rope_call(what, rope_plan, q, k, positions, offset, out, out_k, inverse, stream):
-    _require(q.is_cuda and q.dim() == 4 and q.dtype in _ROPE_DTYPES and q.stride(3) == 1, what)
+    dev, dtype = q.get_device(), q.dtype
+    code = _ROPE_DTYPES.get(dtype)
+    _require(dev >= 0 and code is not None and q.dim() == 4 and q.stride(3) == 1, what)
     B, N, H, d = q.shape
-    H_kv = 0
+    H_kv = kp = ks = pos = kop = kos = None
     if k is not None:
-        _require(k.device == q.device and k.dtype == q.dtype and k.dim() == 4 and k.stride(3) == 1 and
-                 k.shape[0] == B and k.shape[1] == N and k.shape[3] == d, what)
-        H_kv = k.shape[2]
+        _require(k.get_device() == dev and k.dtype is dtype and k.dim() == 4 and k.stride(3) == 1, what)
+        kB, kN, H_kv, kd = k.shape
+        _require(kB == B and kN == N and kd == d, what)
+        kp, ks = k.data_ptr(), _strides_of(k)
     if positions is not None:
-        _require(positions.device == q.device and positions.dtype == torch.int32 and
-                 positions.shape == (B, N) and positions.is_contiguous(), what)
-    with _Launch(q, stream):
+        pos = _vector(positions, (B, N), dev, what)
+    with _Launch(dev, stream) as s:
+        qs = qos = _strides_of(q)
         if out is None:
-            out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
-        if k is not None and out_k is None:
-            out_k = torch.empty(k.shape, dtype=k.dtype, device=k.device)
-        for x, y in ((q, out), (k, out_k)):
-            _require(x is None or (y.shape == x.shape and y.dtype == x.dtype and y.device == x.device and
-                                   y.stride(3) == 1), what)
-        if q.numel() and (k is None or k.numel()):
-            _check(_lib.focus_rope_apply(
-                rope_plan._addr, _ROPE_DTYPES[q.dtype], B, N, H, H_kv, d, q.data_ptr(), _strides_of(q),
-                None if k is None else k.data_ptr(), None if k is None else _strides_of(k),
-                None if positions is None else positions.data_ptr(), offset, inverse,
-                out.data_ptr(), _strides_of(out), None if k is None else out_k.data_ptr(),
-                None if k is None else _strides_of(out_k), _on(q, stream)), what)
+            out = torch.empty_like(q, memory_format=torch.contiguous_format)
+            qos = None
+        elif out is not q:
+            _require(out.shape == q.shape and out.dtype is dtype and out.get_device() == dev and
+                     out.stride(3) == 1, what)
+            qos = _strides_of(out)
+        if k is not None:
+            kos = ks
+            if out_k is None:
+                out_k = torch.empty_like(k, memory_format=torch.contiguous_format)
+                kos = None
+            elif out_k is not k:
+                _require(out_k.shape == k.shape and out_k.dtype is dtype and out_k.get_device() == dev and
+                         out_k.stride(3) == 1, what)
+                kos = _strides_of(out_k)
+            kop = out_k.data_ptr()
+        if B and N:
+            _check(_lib.focus_rope_apply(rope_plan._addr, code, B, N, H, H_kv or 0, d, q.data_ptr(), qs, kp, ks, pos,
+                                         offset, inverse, out.data_ptr(), qos, kop, kos, s), what)
     return out if k is None else (out, out_k)
 
 
@@ -606,19 +613,26 @@ class CacheParams:
     format: str = "bf16"
     softmax_scale: float = 0.0
 
+    def __post_init__(self):
+        _require(self.format in CACHE_FORMATS, "focus_cache_params")
+        object.__setattr__(self, "_by_tokens", {})
+
     def c(self, T: int) -> _CacheParams:
-        return _cache_params(self, T)
+        """focus_cache_params for T tokens, with its address and decode_tree's workspace size;
+        kept, since a program calls with few different T for every token that it makes."""
+        c = self._by_tokens.get(T)
+        if c is None:
+            c = _CacheParams(self.B, self.cap, T, self.H, self.H_kv, self.d_head, self.R, self.K, self.top_k, self.w,
+                             CACHE_FORMATS[self.format], self.softmax_scale)
+            c.addr = ctypes.addressof(c)
+            c.tree_ws = int(_lib.focus_decode_tree_workspace_size(c.addr))
+            if len(self._by_tokens) < 4096:
+                self._by_tokens[T] = c
+        return c
 
     @property
     def scale(self) -> float:
         return self.softmax_scale if self.softmax_scale > 0 else 1.0 / math.sqrt(self.d_head)
-
-
-@functools.lru_cache(maxsize=1024)
-def _cache_params(p: CacheParams, T: int) -> _CacheParams:
-    _require(p.format in CACHE_FORMATS, "focus_cache_params")
-    return _CacheParams(p.B, p.cap, T, p.H, p.H_kv, p.d_head, p.R, p.K, p.top_k, p.w, CACHE_FORMATS[p.format],
-                        p.softmax_scale)
 
 
 @dataclasses.dataclass
@@ -634,33 +648,31 @@ class KVCache:
     @classmethod
     def empty(cls, p: CacheParams, device="cuda") -> "KVCache":
         """A cache of zeros."""
-        _require(p.format in CACHE_FORMATS, "focus_cache_params")
         kv = [torch.zeros(p.B, p.cap, p.H_kv, p.d_head, dtype=torch.uint8 if p.format != "bf16" else torch.bfloat16,
                           device=device).view(_CACHE_DTYPES[p.format]) for _ in range(2)]
         sc = [None if p.format == "bf16" else torch.zeros(p.B, p.H_kv, p.cap, device=device) for _ in range(2)]
         return cls(*kv, *sc, torch.zeros(p.B, p.R, p.cap, dtype=torch.int32, device=device))
 
     def _args(self, p: CacheParams, what: str):
-        k = self.k
-        shape, dtype, dev = (p.B, p.cap, p.H_kv, p.d_head), _CACHE_DTYPES.get(p.format), k.device
-        _require(k.is_cuda and self.mask.device == dev and self.mask.dtype == torch.int32 and
-                 self.mask.shape == (p.B, p.R, p.cap) and self.mask.is_contiguous(), what)
-        for x in (k, self.v):
-            _require(x.device == dev and x.dtype == dtype and x.shape == shape and x.is_contiguous(), what)
+        """The device's index, and the addresses of k, v, their scales and the masks."""
+        k, v, mask, ks, vs = self.k, self.v, self.mask, self.k_scale, self.v_scale
+        dev, dtype, shape = k.get_device(), _CACHE_DTYPES.get(p.format), (p.B, p.cap, p.H_kv, p.d_head)
+        _require(dev >= 0 and k.dtype is dtype and k.shape == shape and k.is_contiguous() and
+                 v.get_device() == dev and v.dtype is dtype and v.shape == shape and v.is_contiguous(), what)
         if p.format == "bf16":
-            _require(self.k_scale is None and self.v_scale is None, what)
-            return k.data_ptr(), self.v.data_ptr(), None, None
-        for x in (self.k_scale, self.v_scale):
-            _require(x is not None and x.device == dev and x.dtype == torch.float32 and
-                     x.shape == (p.B, p.H_kv, p.cap) and x.is_contiguous(), what)
-        return k.data_ptr(), self.v.data_ptr(), self.k_scale.data_ptr(), self.v_scale.data_ptr()
+            _require(ks is None and vs is None, what)
+            return dev, k.data_ptr(), v.data_ptr(), None, None, _vector(mask, (p.B, p.R, p.cap), dev, what)
+        shape = (p.B, p.H_kv, p.cap)
+        _require(ks is not None and vs is not None, what)
+        return (dev, k.data_ptr(), v.data_ptr(), _vector(ks, shape, dev, what, torch.float32),
+                _vector(vs, shape, dev, what, torch.float32), _vector(mask, (p.B, p.R, p.cap), dev, what))
 
 
-def _vector(t, shape, like: torch.Tensor, what: str, dtype=torch.int32):
-    """The address of an optional dense device tensor of the given shape and type."""
+def _vector(t, shape, dev: int, what: str, dtype=torch.int32):
+    """The address of an optional dense tensor of the given device, shape and type."""
     if t is None:
         return None
-    _require(t.device == like.device and t.dtype == dtype and t.shape == shape and t.is_contiguous(), what)
+    _require(t.get_device() == dev and t.dtype is dtype and t.shape == shape and t.is_contiguous(), what)
     return t.data_ptr()
 
 
@@ -673,20 +685,21 @@ def cache_write(p: CacheParams, cache: KVCache, k: torch.Tensor, v: torch.Tensor
     word that get_status reads (FOCUS_ERR_BOUNDS when a token had no slot).  A tree's accepted
     path is committed by writing its tokens again from start on, in order."""
     what = "focus_cache_write"
-    args = cache._args(p, what)
-    T = k.shape[1] if k.dim() == 4 else 0
+    dev, kc, vc, ksc, vsc, mc = cache._args(p, what)
+    _require(k.dim() == 4 and start is not None, what)
+    T = k.shape[1]
     for x in (k, v):
-        _require(x.device == cache.k.device and x.dtype == torch.bfloat16 and
-                 x.shape == (p.B, T, p.H_kv, p.d_head) and x.stride(3) == 1, what)
-    _require(start is not None, what)
+        _require(x.get_device() == dev and x.dtype is torch.bfloat16 and x.shape == (p.B, T, p.H_kv, p.d_head) and
+                 x.stride(3) == 1, what)
     if T == 0:
         return cache
-    with _Launch(k, stream):
+    c = p.c(T)
+    with _Launch(dev, stream) as s:
         _check(_lib.focus_cache_write(
-            ctypes.byref(p.c(T)), k.data_ptr(), _strides_of(k), v.data_ptr(), _strides_of(v),
-            _vector(mask, (p.B, p.R, T), k, what), _vector(start, (p.B,), k, what), _vector(count, (p.B,), k, what),
-            None if rope is None else rope._addr, _vector(positions, (p.B, T), k, what), *args,
-            cache.mask.data_ptr(), _vector(status, (1,), k, what), _on(k, stream)), what)
+            c.addr, k.data_ptr(), _strides_of(k), v.data_ptr(), _strides_of(v),
+            _vector(mask, (p.B, p.R, T), dev, what), _vector(start, (p.B,), dev, what),
+            _vector(count, (p.B,), dev, what), None if rope is None else rope._addr,
+            _vector(positions, (p.B, T), dev, what), kc, vc, ksc, vsc, mc, _vector(status, (1,), dev, what), s), what)
     return cache
 
 
@@ -695,28 +708,25 @@ def cache_read(p: CacheParams, cache: KVCache, T: int, start=None, count=None, *
     """k, v [B, T, H_kv, d] bf16 of the tokens in slots start[b] + t (start None: 0), zeros
     for t >= count[b]; e.g. the prefix of a further prompt for attn_fwd.  out: (k, v) to fill."""
     what = "focus_cache_read"
-    args = cache._args(p, what)
-    shape, dev = (p.B, T, p.H_kv, p.d_head), cache.k.device
-    with _Launch(cache.k, stream):
+    dev, kc, vc, ksc, vsc, _ = cache._args(p, what)
+    shape = (p.B, T, p.H_kv, p.d_head)
+    with _Launch(dev, stream) as s:
         if out is None:
-            out = tuple(torch.empty(shape, dtype=torch.bfloat16, device=dev) for _ in range(2))
-        k, v = out
-        for x in (k, v):
-            _require(x.device == dev and x.dtype == torch.bfloat16 and x.shape == shape and x.is_contiguous(), what)
+            at = cache.k.device
+            k, v = torch.empty(shape, dtype=torch.bfloat16, device=at), torch.empty(shape, dtype=torch.bfloat16, device=at)
+        else:
+            k, v = out
+            _vector(k, shape, dev, what, torch.bfloat16), _vector(v, shape, dev, what, torch.bfloat16)
         if T:
+            c = p.c(T)
             _check(_lib.focus_cache_read(
-                ctypes.byref(p.c(T)), *args, _vector(start, (p.B,), k, what), _vector(count, (p.B,), k, what),
-                k.data_ptr(), v.data_ptr(), _vector(status, (1,), k, what), _on(cache.k, stream)), what)
+                c.addr, kc, vc, ksc, vsc, _vector(start, (p.B,), dev, what),
+                _vector(count, (p.B,), dev, what), k.data_ptr(), v.data_ptr(), _vector(status, (1,), dev, what), s), what)
     return k, v
 
 
 def decode_tree_workspace_size(p: CacheParams, T: int) -> int:
-    return _tree_workspace(p, T)
-
-
-@functools.lru_cache(maxsize=1024)
-def _tree_workspace(p: CacheParams, T: int) -> int:
-    return int(_lib.focus_decode_tree_workspace_size(ctypes.byref(p.c(T))))
+    return p.c(T).tree_ws
 
 
 def decode_tree(p: CacheParams, q: torch.Tensor, cache: KVCache, lens: torch.Tensor, tree=None, *, out=None,
@@ -728,27 +738,24 @@ def decode_tree(p: CacheParams, q: torch.Tensor, cache: KVCache, lens: torch.Ten
     T = 1 is the plain next token of sequences of different lengths.
     Returns (o [B, T, H, d] bf16, lse [B, H, T] fp32)."""
     what = "focus_decode_tree"
-    args = cache._args(p, what)
-    _require(q.device == cache.k.device and q.dtype == torch.bfloat16 and q.dim() == 4 and q.is_contiguous(), what)
+    dev, kc, vc, ksc, vsc, mc = cache._args(p, what)
+    _require(q.dim() == 4 and lens is not None, what)
     T = q.shape[1]
-    _require(q.shape == (p.B, T, p.H, p.d_head) and lens is not None, what)
-    with _Launch(q, stream):
-        need = _tree_workspace(p, T)
-        if need == 0:
-            raise FocusError(-2 if T > MAX_DRAFT else -1, "focus_decode_tree_workspace_size")
-        if out is None:
-            out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+    shape = (p.B, T, p.H, p.d_head)
+    qp = _vector(q, shape, dev, what, torch.bfloat16)
+    c = p.c(T)
+    if c.tree_ws == 0:
+        raise FocusError(-2 if T > MAX_DRAFT else -1, "focus_decode_tree_workspace_size")
+    with _Launch(dev, stream) as s:
+        out = torch.empty_like(q) if out is None else out
         if lse is None and want_lse:
             lse = torch.empty((p.B, p.H, T), dtype=torch.float32, device=q.device)
-        if ws is None:
-            ws = torch.empty(need, dtype=torch.uint8, device=q.device)
-        _require(out.device == q.device and out.dtype == q.dtype and out.shape == q.shape and out.is_contiguous() and
-                 ws.device == q.device and ws.is_contiguous(), what)
+        ws = q.new_empty((c.tree_ws + 1) // 2) if ws is None else ws  # (bytes, in the type at hand)
+        _require(ws.get_device() == dev and ws.is_contiguous(), what)
         _check(_lib.focus_decode_tree(
-            ctypes.byref(p.c(T)), q.data_ptr(), *args, cache.mask.data_ptr(), _vector(lens, (p.B,), q, what),
-            _vector(tree, (p.B, T), q, what, torch.int64), out.data_ptr(),
-            _vector(lse, (p.B, p.H, T), q, what, torch.float32), ws.data_ptr(), ws.numel() * ws.element_size(),
-            _on(q, stream)), what)
+            c.addr, qp, kc, vc, ksc, vsc, mc, _vector(lens, (p.B,), dev, what),
+            _vector(tree, (p.B, T), dev, what, torch.int64), _vector(out, shape, dev, what, torch.bfloat16),
+            _vector(lse, (p.B, p.H, T), dev, what, torch.float32), ws.data_ptr(), ws.nbytes, s), what)
     return out, lse
 
 

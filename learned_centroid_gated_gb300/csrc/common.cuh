@@ -5,6 +5,8 @@
 #include <cuda_runtime.h>
 #include <stdint.h>
 
+#include <atomic>
+
 #include "../../include/focus.h"
 
 namespace focus {
@@ -92,6 +94,20 @@ __device__ inline bool in_bounds(bool ok, int* status) {
 #else
 #define FOCUS_IN_BOUNDS(cond, status) true
 #endif
+
+// Runs f (which sets a kernel's attributes; they hold per device) once on each device:
+// `done` has a bit per device whose f succeeded.  Two host threads may both run it, which
+// is harmless, and neither goes on before it has.
+template <typename F>
+inline cudaError_t once_per_device(std::atomic<uint64_t>& done, F&& f) {
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  const uint64_t bit = dev < 64 ? 1ull << dev : 0ull;
+  if (done.load(std::memory_order_acquire) & bit) return cudaSuccess;
+  if ((e = f()) == cudaSuccess) done.fetch_or(bit, std::memory_order_release);
+  return e;
+}
 
 inline size_t align_up(size_t x, size_t a) { return (x + a - 1) / a * a; }
 

@@ -29,7 +29,6 @@ using namespace wmma16;
 constexpr int kTreeTile = 16;     // keys per pipeline tile (one MMA reduction step)
 constexpr int kTreeRows = 16;     // rows per warp (the MMA's M)
 constexpr int kTreeBlock = 256;   // raw keys per listing step
-constexpr int kTreeMinUnits = 4;  // fewest dense units per slice
 constexpr int kTreeWarps = 1216;  // warps per launch: one wave of 8 per SM on 152 SMs
 constexpr float kLn2 = 0.6931471805599453f;
 constexpr float kLog2e = 1.4426950408889634f;
@@ -570,12 +569,11 @@ __global__ void __launch_bounds__(32 * kTreeCombWarps) tree_combine(const __grid
 }
 
 // ------------------------------------------------------------------------- launch --
-constexpr int kTreeTcRows = 128;  // rows per CTA of the tensor-core kernel (the MMA's M)
+constexpr int kTreeTcRows = 128;  // rows of a product of the tensor-core kernel (the MMA's M)
 constexpr int kTreeTcSlices = 152;
-constexpr int kTreeTcMinUnits = 16;
 
 struct TreePlan {
-  int gq, rows, grp, nrg, parts, G, min_weight, wfar;
+  int gq, rows, grp, nrg, parts, G, wfar;
   bool tc;
   size_t flags, ml, acc, total;  // offsets and size of the workspace
 };
@@ -585,14 +583,13 @@ TreePlan tree_plan(const focus_cache_params& p) {
   t.gq = p.H / p.H_kv;
   t.rows = p.T * t.gq;
   t.tc = t.rows > kTreeRows;
-  t.grp = t.tc ? kTreeTcRows : kTreeRows;
+  t.grp = !t.tc ? kTreeRows : t.rows > kTreeTcRows ? 2 * kTreeTcRows : kTreeTcRows;
   t.nrg = (t.rows + t.grp - 1) / t.grp;
-  t.parts = t.tc ? kTreeTcParts : 1;
+  t.parts = t.grp == kTreeTcRows ? 2 : 1;
   t.G = t.tc ? kTreeTcSlices : kTreeWarps;
-  t.min_weight = (t.tc ? kTreeTcMinUnits : kTreeMinUnits) * kTreeNear;
   const int64_t lanes = (int64_t)p.H_kv * t.nrg;
   const int64_t most = lanes * p.B * (((int64_t)p.cap + kTreeUnit - 1) / kTreeUnit) * kTreeNear;
-  t.G = (int)std::max<int64_t>(1, std::min<int64_t>(t.G, most / t.min_weight));
+  t.G = (int)std::max<int64_t>(1, std::min<int64_t>(t.G, most / kTreeNear));
   // expected share of the far keys that some drafted token's mask meets (balance only)
   double miss = 1.0;
   for (int i = 0; i < p.top_k; ++i) miss *= std::max(0.0, (double)(p.K - p.top_k - i)) / (p.K - i);
@@ -612,7 +609,10 @@ cudaError_t launch_tree(const TreeArgs& a, bool tc, cudaStream_t s) {
   if (tc) {
     if ((e = launch_tree_tc(a, D, FMT, s)) != cudaSuccess) return e;
   } else {
-    e = cudaFuncSetAttribute(tree_split<D, FMT>, cudaFuncAttributePreferredSharedMemoryCarveout, 100);
+    static std::atomic<uint64_t> done{0};
+    e = once_per_device(done, [] {
+      return cudaFuncSetAttribute(tree_split<D, FMT>, cudaFuncAttributePreferredSharedMemoryCarveout, 100);
+    });
     if (e != cudaSuccess) return e;
     tree_split<D, FMT><<<(unsigned)a.G, 32, L::BYTES, s>>>(a);
     if ((e = cudaGetLastError()) != cudaSuccess) return e;
@@ -647,7 +647,7 @@ cudaError_t launch_decode_tree(const focus_cache_params& p, const bf16* q, const
   a.o = o, a.lse = lse, a.status = reinterpret_cast<int32_t*>(ws);
   a.B = p.B, a.cap = p.cap, a.T = p.T, a.H = p.H, a.H_kv = p.H_kv, a.R = p.R, a.w = p.w;
   a.gq = t.gq, a.rows = t.rows, a.grp = t.grp, a.nrg = t.nrg, a.parts = t.parts;
-  a.G = t.G, a.min_weight = t.min_weight, a.wfar = t.wfar;
+  a.G = t.G, a.wfar = t.wfar, a.tma = 0;
   a.sl2 = scale * kLog2e;
   if (p.d_head == 64)
     return p.format == FOCUS_CACHE_BF16   ? launch_tree<64, FOCUS_CACHE_BF16>(a, t.tc, s)

@@ -11,7 +11,6 @@ namespace focus {
 
 constexpr int kTreeUnit = 32;        // keys per unit of work
 constexpr int kTreeNear = 64;        // weight of a unit near the window
-constexpr int kTreeTcParts = 2;      // partials per segment of the tensor-core kernel
 // 8-bit formats: V scales count as at least 2^-80 where the reference of the exponentials is
 // chosen, so that a row of (next to) zeros cannot push the sum of exponentials out of fp32.
 constexpr float kTinyScale = 8.271806e-25f;
@@ -30,10 +29,11 @@ struct TreeArgs {
   float* lse;
   int32_t* status;
   int B, cap, T, H, H_kv, R, w, gq, rows;
-  int grp, nrg;      // rows per row group (16 or 128), row groups
+  int grp, nrg;      // rows per row group (16, or 128 or 256 on the tensor cores), row groups
   int parts;         // partials per segment
-  int G, min_weight; // slices at most, least weight of one
+  int G;             // slices at most
   int wfar;
+  int tma;           // tensor-core kernel: tensor maps are there
   float sl2;         // softmax scale * log2(e)
 };
 
@@ -80,14 +80,15 @@ __device__ __forceinline__ int64_t warp_scan(int64_t x, int lane) {  // inclusiv
   }
   return x;
 }
-// All sequences' weight for one (KV head, row group), and the slices of the whole row.
+// All sequences' weight for one (KV head, row group), and the slices of the whole row (a
+// unit at least each: short sequences are spread as far as they go).
 __device__ __forceinline__ int64_t total_weight(const TreeArgs& a, int lane) {
   int64_t t = 0;
   for (int b = lane; b < a.B; b += 32) t += stretch_of(a, __ldg(a.lens + b)).weight;
   return warp_sum(t);
 }
 __device__ __forceinline__ int slices_of(const TreeArgs& a, int64_t row_weight) {
-  return (int)max((int64_t)1, min((int64_t)a.G, row_weight / a.min_weight));
+  return (int)max((int64_t)1, min((int64_t)a.G, row_weight / kTreeNear));
 }
 
 // Calls f(number of the partial, KV head, row group, sequence, its length, first key, end)
@@ -141,6 +142,22 @@ __device__ __forceinline__ uint32_t codes_f16(uint32_t two) {
     const uint32_t h = __byte_perm(two ^ 0x8080u, 0x64646464u, 0x4140);
     const __half2 r = __hsub2(*reinterpret_cast<const __half2*>(&h), __float2half2_rn(1152.0f));
     return *reinterpret_cast<const uint32_t*>(&r);
+  }
+}
+
+// Four codes as two pairs of fp16.
+template <int FMT>
+__device__ __forceinline__ void codes_f16x2(uint32_t four, uint32_t& lo, uint32_t& hi) {
+  if constexpr (FMT == FOCUS_CACHE_E4M3) {
+    lo = codes_f16<FMT>(four);
+    hi = codes_f16<FMT>(four >> 16);
+  } else {
+    const uint32_t x = four ^ 0x80808080u;  // c + 128
+    const uint32_t a = __byte_perm(x, 0x64646464u, 0x4140), b = __byte_perm(x, 0x64646464u, 0x4342);
+    const __half2 k = __float2half2_rn(1152.0f);
+    const __half2 y = __hsub2(*reinterpret_cast<const __half2*>(&a), k), z = __hsub2(*reinterpret_cast<const __half2*>(&b), k);
+    lo = *reinterpret_cast<const uint32_t*>(&y);
+    hi = *reinterpret_cast<const uint32_t*>(&z);
   }
 }
 

@@ -16,6 +16,7 @@ Tolerances.  u(t) = eps(t) / 2 is the largest relative error of one rounding to 
   below 2^-14 a rounding is off by up to 2^-25 absolute, that is 2^-28 of the largest:
   another 2^-28 max(p vs) sum |c|, which matters where the large rows' codes are 0.
 """
+import dataclasses
 import math
 import random
 
@@ -269,7 +270,7 @@ def test_cache_rows_of_zeros_tiny_and_not_finite_values():
     x = x.to(torch.bfloat16).cuda()
     start = torch.zeros(1, dtype=torch.int32, device="cuda")
     for fmt in ("e4m3", "int8"):
-        p = focus.CacheParams(**{**p0.__dict__, "format": fmt})
+        p = dataclasses.replace(p0, format=fmt)
         c = focus.KVCache.empty(p)
         focus.cache_write(p, c, x, x, None, start)
         k, v = focus.cache_read(p, c, 6)
@@ -333,6 +334,10 @@ TREES = {
     "long_tree": dict(T=24, B=3, lens=[3000, 700, 0], cap=3100, w=100, tree=True, H=8, H_kv=2, K=8, top_k=1),
     "ragged_tree": dict(T=9, B=20, lens=[(b * 37) % 150 for b in range(20)], cap=160, w=9, tree=True, H=4, H_kv=1, d_head=64),
     "sparse_tree": dict(T=17, lens=[2500], B=1, cap=2600, w=1, tree=True, H=2, H_kv=1, K=32, top_k=1),
+    "wide_tree": dict(T=64, lens=[1500], B=1, cap=1600, w=30, tree=True, H=4, H_kv=1, K=4, top_k=1),
+    "wide_tree64": dict(T=40, lens=[1201, 700], cap=1300, w=30, tree=True, H=6, H_kv=1, d_head=64, K=4, top_k=2),
+    "sparse_wide": dict(T=17, lens=[1300], B=1, cap=1400, w=5, tree=True, H=8, H_kv=1, K=32, top_k=1),
+    "rows_300": dict(T=50, lens=[90, 600], cap=700, w=64, tree=True, H=6, H_kv=1, K=8, top_k=2),
     "scale": dict(T=4, lens=[100, 20], cap=120, softmax_scale=0.5, tree=True),
 }
 
