@@ -9,6 +9,8 @@
 #include <cuda_fp8.h>
 #include <math.h>
 
+#include <type_traits>
+
 #include "rope.cuh"
 
 namespace focus {
@@ -56,19 +58,31 @@ __device__ __forceinline__ uint2 encode(const float (&f)[8], float inv) {
   uint32_t w[2];
 #pragma unroll
   for (int i = 0; i < 2; ++i) {
+    const float* x = f + 4 * i;
     if constexpr (FMT == FOCUS_CACHE_E4M3) {
-      const float* x = f + 4 * i;
-      const uint32_t lo = __nv_cvt_float2_to_fp8x2(make_float2(x[0] * inv, x[1] * inv), __NV_SATFINITE, __NV_E4M3);
-      const uint32_t hi = __nv_cvt_float2_to_fp8x2(make_float2(x[2] * inv, x[3] * inv), __NV_SATFINITE, __NV_E4M3);
-      w[i] = lo | hi << 16;
+      float y[4];
+      ptx::fmul2(y[0], y[1], x[0], x[1], inv, inv);
+      ptx::fmul2(y[2], y[3], x[2], x[3], inv, inv);
+      const uint32_t lo = __nv_cvt_float2_to_fp8x2(make_float2(y[0], y[1]), __NV_SATFINITE, __NV_E4M3);
+      const uint32_t hi = __nv_cvt_float2_to_fp8x2(make_float2(y[2], y[3]), __NV_SATFINITE, __NV_E4M3);
+      w[i] = __byte_perm(lo, hi, 0x5410);
     } else {
-      w[i] = 0;
-#pragma unroll
-      for (int e = 0; e < 4; ++e)
-        w[i] |= ((uint32_t)__float2int_rn(f[4 * i + e] * inv) & 0xffu) << (8 * e);
+      // 1.5 * 2^23 + c has the integer c, rounded to nearest even, in its low bits
+      float y[4];
+      ptx::ffma2(y[0], y[1], x[0], x[1], inv, inv, 12582912.0f, 12582912.0f);
+      ptx::ffma2(y[2], y[3], x[2], x[3], inv, inv, 12582912.0f, 12582912.0f);
+      const uint32_t u[4] = {__float_as_uint(y[0]), __float_as_uint(y[1]), __float_as_uint(y[2]), __float_as_uint(y[3])};
+      w[i] = __byte_perm(__byte_perm(u[0], u[1], 0x0040), __byte_perm(u[2], u[3], 0x0040), 0x5410);
     }
   }
   return make_uint2(w[0], w[1]);
+}
+
+// The larger of three magnitudes, a NaN if there is one.
+__device__ __forceinline__ float abs_max3(float a, float b, float c) {
+  float d;
+  asm("max.NaN.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(fabsf(a)), "f"(fabsf(b)), "f"(fabsf(c)));
+  return d;
 }
 
 template <int FMT>
@@ -94,7 +108,7 @@ __device__ __forceinline__ void decode8(const uint2& x, float scale, float (&f)[
 // holds four pairs, and with kHalfAny (any other even dim) the partner of each element is
 // read from the row (a cached read: the row's other lanes load it too).
 template <int D, int FMT, int MODE>
-__global__ void __launch_bounds__(256) cache_write(const __grid_constant__ CacheArgs a) {
+__global__ void __launch_bounds__(256, MODE == kHalfAny ? 3 : 4) cache_write(const __grid_constant__ CacheArgs a) {
   using C = RowChunk<bf16>;
   constexpr int LPR = D / 16, RPW = 32 / LPR;
   const int64_t warp = (int64_t)blockIdx.x * (blockDim.x >> 5) + (threadIdx.x >> 5);
@@ -118,93 +132,110 @@ __global__ void __launch_bounds__(256) cache_write(const __grid_constant__ Cache
   if constexpr (MODE != kNoRope) {
     if (i0 < a.H_kv) {
       const int64_t pos = a.positions ? (int64_t)__ldg(a.positions + tk) : (int64_t)slot;
-#pragma unroll
-      for (int e = 0; e < NA; ++e) {
-        int i;
-        if constexpr (MODE == kHalf) i = c * 8 + e;
-        else if constexpr (MODE == kInterleaved) i = (e < 4 ? ca : cb) * 4 + (e & 3);
-        else {
-          const int x = (e < 8 ? ca : cb) * 8 + (e & 7);
-          i = x < np ? x : x < 2 * np ? x - np : np;
-        }
-        cs[e] = 1.0f, sn[e] = 0.0f;
-        if (i < np) rope_angle(pos, a.rope.turn[i], a.rope.attn_factor, cs[e], sn[e]);
-      }
+      rope_angles<NA, LPR>(
+          a.rope, pos, lane,
+          [&](int e) {
+            if (MODE == kHalf) return c * 8 + e;
+            if (MODE == kInterleaved) return (e < 4 ? ca : cb) * 4 + (e & 3);
+            const int x = (e < 8 ? ca : cb) * 8 + (e & 7);
+            return x < np ? x : x < 2 * np ? x - np : np;
+          },
+          cs, sn);
     }
   }
-  // Every lane takes part in every pass (the row maximum is a shuffle); rows past the end
-  // are not loaded or stored.
-  for (int p0 = i0; p0 < i1; p0 += RPW) {
-    const int row = p0 + sub;
-    const bool on = row < i1, key = row < a.H_kv;
-    const int h = key ? row : row - a.H_kv;
-    const bf16* x = reinterpret_cast<const bf16*>(key ? a.k : a.v);
-    {
-      const focus_strides& st = key ? a.ks : a.vs;
-      x += b * st.b + t * st.n + h * st.h;
-    }
-    float fa[8], fb[8];
-    uint4 xa = make_uint4(0u, 0u, 0u, 0u), xb = xa;
-    if (on) {
-      xa = __ldg(reinterpret_cast<const uint4*>(x + 8 * ca));
-      xb = __ldg(reinterpret_cast<const uint4*>(x + 8 * cb));
-    }
-    C::unpack(xa, fa);
-    C::unpack(xb, fb);
-    if (MODE != kNoRope && on && key) {
-      if constexpr (MODE == kHalf) {
-        if (pair) {
+  // Rows h0 .. h1 - 1 of the keys or of the values.  Every lane takes part in every pass (the
+  // row maximum is a shuffle); rows past the end are not loaded or stored.  The loads of two
+  // passes are in flight together.
+  auto rows = [&](auto is_key, const uint16_t* src, const focus_strides& st, void* cache, float* scale, int h0, int h1) {
+    constexpr bool KEY = decltype(is_key)::value;
+    constexpr int U = 2, ES = FMT == FOCUS_CACHE_BF16 ? 2 : 1;
+    const bf16* x = reinterpret_cast<const bf16*>(src) + b * st.b + t * st.n + (h0 + sub) * st.h;
+    const int64_t step = RPW * st.h;
+    char* dst = reinterpret_cast<char*>(cache) + (((int64_t)b * a.cap + slot) * a.H_kv + h0 + sub) * (D * ES);
+    for (int h = h0; h < h1; h += U * RPW) {
+      uint4 xa[U], xb[U];
 #pragma unroll
-          for (int e = 0; e < 8; ++e) rope_turn(fa[e], fb[e], cs[e], sn[e]);
+      for (int u = 0; u < U; ++u) {
+        xa[u] = xb[u] = make_uint4(0u, 0u, 0u, 0u);
+        if (h + u * RPW + sub < h1) {
+          xa[u] = __ldg(reinterpret_cast<const uint4*>(x + u * step + 8 * ca));
+          xb[u] = __ldg(reinterpret_cast<const uint4*>(x + u * step + 8 * cb));
         }
-      } else if constexpr (MODE == kInterleaved) {
+      }
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          if (ca * 4 + e < np) rope_turn(fa[2 * e], fa[2 * e + 1], cs[e], sn[e]);
-          if (cb * 4 + e < np) rope_turn(fb[2 * e], fb[2 * e + 1], cs[4 + e], sn[4 + e]);
+      for (int u = 0; u < U; ++u) {
+        if (h + u * RPW >= h1) break;
+        const bool on = h + u * RPW + sub < h1;
+        const bf16* xr = x + u * step;
+        char* y = dst + u * RPW * (D * ES);
+        float mx = 0.0f;
+        if constexpr (!KEY && FMT != FOCUS_CACHE_BF16) {
+          // magnitudes as 16-bit integers, two at a time; infinities and NaN are the largest
+          uint32_t m = 0u;
+          const uint32_t w[8] = {xa[u].x, xa[u].y, xa[u].z, xa[u].w, xb[u].x, xb[u].y, xb[u].z, xb[u].w};
+#pragma unroll
+          for (int e = 0; e < 8; ++e) m = __vmaxu2(m, w[e] & 0x7fff7fffu);
+          mx = __uint_as_float(max(m << 16, m & 0xffff0000u));
         }
-      } else if constexpr (MODE == kHalfAny) {
+        float fa[8], fb[8];
+        C::unpack(xa[u], fa);
+        C::unpack(xb[u], fb);
+        if constexpr (KEY && MODE == kHalf) {
+          if (pair) {
 #pragma unroll
-        for (int e = 0; e < 16; ++e) {
-          const int i = (e < 8 ? ca : cb) * 8 + (e & 7);
-          if (i < 2 * np) {
-            float& f = e < 8 ? fa[e & 7] : fb[e & 7];
-            float o = __bfloat162float(x[i < np ? i + np : i - np]);
-            if (i < np) rope_turn(f, o, cs[e], sn[e]);
-            else rope_turn(o, f, cs[e], sn[e]);
+            for (int e = 0; e < 8; e += 2)
+              rope_turn2(fa[e], fa[e + 1], fb[e], fb[e + 1], cs[e], cs[e + 1], sn[e], sn[e + 1]);
+          }
+        } else if constexpr (KEY && MODE == kInterleaved) {
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            if (ca * 4 + e < np) rope_turn(fa[2 * e], fa[2 * e + 1], cs[e], sn[e]);
+            if (cb * 4 + e < np) rope_turn(fb[2 * e], fb[2 * e + 1], cs[4 + e], sn[4 + e]);
+          }
+        } else if constexpr (KEY && MODE == kHalfAny) {
+#pragma unroll
+          for (int e = 0; e < 16; ++e) {
+            const int i = (e < 8 ? ca : cb) * 8 + (e & 7);
+            if (i < 2 * np && on) {
+              float& f = e < 8 ? fa[e & 7] : fb[e & 7];
+              float o = __bfloat162float(xr[i < np ? i + np : i - np]);
+              if (i < np) rope_turn(f, o, cs[e], sn[e]);
+              else rope_turn(o, f, cs[e], sn[e]);
+            }
+          }
+        }
+        if constexpr (FMT == FOCUS_CACHE_BF16) {
+          if (on) {
+            *reinterpret_cast<uint4*>(y + 16 * ca) = C::pack(fa);
+            *reinterpret_cast<uint4*>(y + 16 * cb) = C::pack(fb);
+          }
+        } else {
+          constexpr float M = FMT == FOCUS_CACHE_E4M3 ? 448.0f : 127.0f;
+          if constexpr (KEY) {
+#pragma unroll
+            for (int e = 0; e < 8; ++e) mx = abs_max3(mx, fa[e], fb[e]);
+          }
+#pragma unroll
+          for (int o = 1; o < LPR; o <<= 1) mx = abs_max3(mx, __shfl_xor_sync(0xffffffffu, mx, o), 0.0f);
+          const bool finite = mx < INFINITY, some = finite && mx >= kTinyRow;
+          // (the fast quotient, two units in the last place, holds up to 2^126)
+          const float inv = some ? (mx < 8e37f ? __fdividef(M, mx) : M / mx) : 0.0f;
+          if (on) {
+            const uint2 zero = make_uint2(0u, 0u);
+            *reinterpret_cast<uint2*>(y + 8 * ca) = some ? encode<FMT>(fa, inv) : zero;
+            *reinterpret_cast<uint2*>(y + 8 * cb) = some ? encode<FMT>(fb, inv) : zero;
+            if (c == 0)
+              scale[((int64_t)b * a.H_kv + h + u * RPW + sub) * a.cap + slot] =
+                  some ? mx * (1.0f / M) : finite ? 0.0f : __uint_as_float(0x7fc00000u);
           }
         }
       }
+      x += U * step;
+      dst += U * RPW * (D * ES);
     }
-    char* dst = reinterpret_cast<char*>(key ? a.kc : a.vc);
-    const int64_t at = (((int64_t)b * a.cap + slot) * a.H_kv + h) * D;
-    if constexpr (FMT == FOCUS_CACHE_BF16) {
-      if (on) {
-        *reinterpret_cast<uint4*>(dst + 2 * (at + 8 * ca)) = C::pack(fa);
-        *reinterpret_cast<uint4*>(dst + 2 * (at + 8 * cb)) = C::pack(fb);
-      }
-    } else {
-      constexpr float M = FMT == FOCUS_CACHE_E4M3 ? 448.0f : 127.0f;
-      // the maximum of the magnitudes as bit patterns: a NaN or an infinity wins
-      uint32_t top = 0;
-#pragma unroll
-      for (int e = 0; e < 8; ++e)
-        top = max(top, max(__float_as_uint(fa[e]) & 0x7fffffffu, __float_as_uint(fb[e]) & 0x7fffffffu));
-#pragma unroll
-      for (int o = 1; o < LPR; o <<= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
-      const float mx = __uint_as_float(top);
-      const bool finite = top < 0x7f800000u, some = finite && mx >= kTinyRow;
-      if (on) {
-        const float inv = some ? M / mx : 0.0f;
-        const uint2 zero = make_uint2(0u, 0u);
-        *reinterpret_cast<uint2*>(dst + at + 8 * ca) = some ? encode<FMT>(fa, inv) : zero;
-        *reinterpret_cast<uint2*>(dst + at + 8 * cb) = some ? encode<FMT>(fb, inv) : zero;
-        if (c == 0)
-          (key ? a.kscale : a.vscale)[((int64_t)b * a.H_kv + h) * a.cap + slot] =
-              some ? mx / M : finite ? 0.0f : __uint_as_float(0x7fc00000u);
-      }
-    }
-  }
+  };
+  if (i0 < a.H_kv) rows(std::true_type{}, a.k, a.ks, a.kc, a.kscale, i0, min(i1, a.H_kv));
+  if (i1 > a.H_kv) rows(std::false_type{}, a.v, a.vs, a.vc, a.vscale, max(i0, a.H_kv) - a.H_kv, i1 - a.H_kv);
 }
 
 template <int D, int FMT>

@@ -61,12 +61,11 @@ __global__ void __launch_bounds__(256) rope_rows(const __grid_constant__ RopeArg
   const int cb = HALF ? (turned ? c + P : ca + 1) : c + LPR;
   float cs[V], sn[V];
   bool rot[V];
+  auto pair = [&](int e) { return HALF ? c * V + e : (e < V / 2 ? ca * (V / 2) + e : cb * (V / 2) + e - V / 2); };
+  rope_angles<V, LPR>(a.rope, pos, lane, pair, cs, sn);
 #pragma unroll
   for (int e = 0; e < V; ++e) {
-    const int i = HALF ? c * V + e : (e < V / 2 ? ca * (V / 2) + e : cb * (V / 2) + e - V / 2);
-    rot[e] = i < np;
-    cs[e] = 1.0f, sn[e] = 0.0f;
-    if (rot[e]) rope_angle(pos, a.rope.turn[i], a.rope.attn_factor, cs[e], sn[e]);
+    rot[e] = pair(e) < np;
     sn[e] *= a.sign;
   }
   const int h1 = min(a.heads, (sp + 1) * a.per);

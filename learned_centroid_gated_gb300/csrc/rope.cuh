@@ -4,7 +4,7 @@
 
 #include <cuda_fp16.h>
 
-#include "common.cuh"
+#include "tc_ptx.cuh"
 
 namespace focus {
 
@@ -25,6 +25,43 @@ __device__ __forceinline__ void rope_turn(float& a, float& b, float c, float s) 
   const float x = a, y = b;
   a = __fmaf_rn(x, c, -__fmul_rn(y, s));
   b = __fmaf_rn(y, c, __fmul_rn(x, s));
+}
+
+// Two pairs at a time: packed fp32 arithmetic, the same roundings.
+__device__ __forceinline__ void rope_turn2(float& a0, float& a1, float& b0, float& b1, float c0, float c1, float s0,
+                                           float s1) {
+  float x0, x1, y0, y1, z0, z1, w0, w1;
+  ptx::fmul2(x0, x1, b0, b1, -s0, -s1);
+  ptx::fmul2(y0, y1, a0, a1, s0, s1);
+  ptx::ffma2(z0, z1, a0, a1, c0, c1, x0, x1);
+  ptx::ffma2(w0, w1, b0, b1, c0, c1, y0, y1);
+  a0 = z0, a1 = z1, b0 = w0, b1 = w1;
+}
+
+// The cosines and sines of a lane's NA pairs where SUBS lanes, LPR apart, need the same
+// ones (they hold the same columns of other heads): each works out NA / SUBS and the rest
+// comes by shuffles.  pair(e): the number of the lane's e-th pair.  A whole warp.
+template <int NA, int LPR, typename F>
+__device__ __forceinline__ void rope_angles(const focus_rope& r, int64_t pos, int lane, F&& pair, float (&cs)[NA],
+                                            float (&sn)[NA]) {
+  constexpr int SUBS = 32 / LPR, OWN = NA / SUBS > 0 ? NA / SUBS : 1;
+  static_assert(NA % OWN == 0 && NA / OWN <= SUBS, "each pair has one owner");
+  const int sub = lane / LPR, np = r.dim / 2;
+  float c[OWN], s[OWN];
+#pragma unroll
+  for (int k = 0; k < OWN; ++k) {
+    int i = np;
+#pragma unroll
+    for (int e = 0; e < NA; ++e)  // (pair() may index by its argument)
+      if (e == (sub * OWN + k) % NA) i = pair(e);
+    c[k] = 1.0f, s[k] = 0.0f;
+    if (i < np) rope_angle(pos, r.turn[i], r.attn_factor, c[k], s[k]);
+  }
+#pragma unroll
+  for (int e = 0; e < NA; ++e) {
+    cs[e] = __shfl_sync(0xffffffffu, c[e % OWN], (e / OWN) * LPR + lane % LPR);
+    sn[e] = __shfl_sync(0xffffffffu, s[e % OWN], (e / OWN) * LPR + lane % LPR);
+  }
 }
 
 template <typename T>

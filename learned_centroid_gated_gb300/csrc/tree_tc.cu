@@ -9,8 +9,8 @@
 //               keys a tile: 64 consecutive keys by TMA, others row by row with 16-byte
 //               asynchronous copies.  bf16 rows go straight into the 128-byte-swizzled
 //               operand tiles; 8-bit codes into a staging ring, whence the warps turn them
-//               into fp16 operands (exact).  For each tile they also work out which key each
-//               drafted token sees, as one 64-bit word per token.
+//               into fp16 operands (exact).  For each tile one of them, in turn, works out
+//               which key each drafted token sees, as one 64-bit word per token.
 //   warp 12     issues the products: S = Q K^T (128 x 64, both operands in shared memory)
 //               into one of four tensor-memory tiles, and O += P V with P read from tensor
 //               memory.  It takes whichever is ready, the next S or the next P V.
@@ -50,20 +50,25 @@ constexpr int kMeta = 8;        // entries of the tile-metadata ring
 constexpr int kThreads = 512;   // 16 warps; 13 work, the rest fill the last warpgroup
 constexpr int kMmaWarp = 12, kLoadWarp = 8;
 
-// What the softmax has to know of a tile.
+enum TileKind { kEnd = 1, kTma = 2 };  // no tile: the segment's end; its rows come by TMA
+
+// What the consumers have to know of a tile.
 template <bool B16>
 struct alignas(16) TileMeta;
 template <>
 struct alignas(16) TileMeta<true> {
   uint64_t see[FOCUS_MAX_DRAFT];  // [token of the row group]: its keys of the tile
-  int end;                        // no tile: the segment's end
+  int end;                        // no tile: the segment's end (for the softmax)
+  int what;                       // for the MMA warp: kEnd, kTma
 };
 template <>
 struct alignas(16) TileMeta<false> {
   uint64_t see[FOCUS_MAX_DRAFT];
-  int end;
+  int end, what;
+  int pad[1];
   int wide;                       // V scales differ by more than 2^4
   float lv, unit;                 // V scales are below 2^lv; 2^-lv
+  int pad2[2];
   float ks[kTile], vs[kTile];     // scales
   __half vn[kTile];               // vs 2^-lv (not of a wide tile)
 };
@@ -96,9 +101,10 @@ struct Tc {
   static constexpr int OFF_TOK = OFF_META + kMeta * (int)sizeof(Meta);
   static constexpr int OFF_LIST = OFF_TOK + FOCUS_MAX_DRAFT * (int)sizeof(Token);
   static constexpr int OFF_DOWN = OFF_LIST + LIST * 8;
-  static constexpr int OFF_CNT = OFF_DOWN + (B16 ? 0 : 2 * NT * kRows * 4);
+  static constexpr int OFF_SETS = OFF_DOWN + (B16 ? 0 : 2 * NT * kRows * 4);
+  static constexpr int OFF_CNT = OFF_SETS + 4 * 32 * 8;
   static constexpr int OFF_BAR = OFF_CNT + 2 * 4 * 4;
-  static constexpr int BARS = 2 * STAGES + 3 * kSBuf + 8 + 2 * SLOTS;
+  static constexpr int BARS = 2 * STAGES + 3 * kSBuf + 8 + 2 * SLOTS + kMeta;
   static constexpr int BYTES = OFF_BAR + 8 * (BARS + 2) + 1024;
   // A metadata entry is written anew kMeta tiles later, when its tile has long been through
   // the products: a tile is issued once the one AHEAD before it is.
@@ -133,7 +139,7 @@ tree_tc(const __grid_constant__ TreeArgs a, const __grid_constant__ CUtensorMap 
   constexpr int S = L::STAGES, ES = B16 ? 2 : 1;
   constexpr int MARKS = NT == 1 ? 2 : 1;  // end marks: one for each warpgroup that steps over tiles
   extern __shared__ uint8_t smem_raw[];
-  uint8_t* sm = reinterpret_cast<uint8_t*>(((uintptr_t)smem_raw + 1023) & ~(uintptr_t)1023);
+  uint8_t* sm = smem_raw + (-smem_u32(smem_raw) & 1023u);  // (stays a shared-memory pointer to the compiler)
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const uint32_t bar = smem_u32(sm + L::OFF_BAR);
   const uint32_t b_full = bar, b_empty = bar + 8 * S;                     // + 8 * stage
@@ -144,6 +150,7 @@ tree_tc(const __grid_constant__ TreeArgs a, const __grid_constant__ CUtensorMap 
   const uint32_t b_epi = b_qfree + 8;
   const uint32_t b_drain = b_epi + 32, b_load = b_drain + 8;              // the loader warps' meetings
   const uint32_t b_tma = b_load + 8, b_raw = b_tma + 8 * L::SLOTS;        // + 8 * slot: TMA there / codes read
+  const uint32_t b_meta = b_raw + 8 * L::SLOTS;                           // + 8 * entry (bf16): metadata there
   volatile uint32_t* tmem_slot = reinterpret_cast<volatile uint32_t*>(sm + L::OFF_BAR + 8 * L::BARS);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(sm + L::OFF_BAR + 8 * (L::BARS + 1));
   Meta* meta = reinterpret_cast<Meta*>(sm + L::OFF_META);
@@ -174,6 +181,7 @@ tree_tc(const __grid_constant__ TreeArgs a, const __grid_constant__ CUtensorMap 
       mbar_init(b_tma + 8 * i, 1);
       mbar_init(b_raw + 8 * i, 4);
     }
+    for (int i = 0; i < kMeta; ++i) mbar_init(b_meta + 8 * i, 1);
     *abort_flag = 0;
     *status = 0;
     fence_barrier_init();
@@ -200,8 +208,9 @@ tree_tc(const __grid_constant__ TreeArgs a, const __grid_constant__ CUtensorMap 
     Token* tok = reinterpret_cast<Token*>(sm + L::OFF_TOK);
     int t = 0;     // tiles, end marks among them
     int seg = 0, scans = 0, meets = 0;
-    uint32_t by_tma = 0u, tma_par = 0u;  // by slot: the tile in it came by TMA; its barrier's parity
-    uint32_t tma_out = 0u;               // by slot: a TMA copy that nobody has waited for
+    // by slot: the tile in it comes by TMA; TMA copies so far (their parity; whether any)
+    uint32_t by_tma = 0u, tma_odd = 0u, tma_any = 0u;
+    uint64_t* sets = reinterpret_cast<uint64_t*>(sm + L::OFF_SETS) + 32 * lw;  // [group]: keys of a tile
     bool ok = true;
     // The loader warps meet: a barrier with a bounded wait.
     auto meet = [&]() {
@@ -255,7 +264,7 @@ tree_tc(const __grid_constant__ TreeArgs a, const __grid_constant__ CUtensorMap 
       if (lane == 0) mbar_arrive(b_q);
       // ---- what the tokens see (each warp for itself; the first one also for the tiles)
       uint32_t many = 0u, wlo = 0u, whi = 0u;
-      int nearest = INT_MAX;
+      int nearest = INT_MAX, farthest = INT_MIN;
       for (int i = lane; i < ntok; i += 32) {
         Token k;
         k.word = tree_word(a, b, tok0 + i);
@@ -266,10 +275,12 @@ tree_tc(const __grid_constant__ TreeArgs a, const __grid_constant__ CUtensorMap 
         wlo |= (uint32_t)k.word;
         whi |= (uint32_t)(k.word >> 32);
         nearest = min(nearest, k.near);
+        if (k.word) farthest = max(farthest, k.near);
       }
       many = __reduce_or_sync(0xffffffffu, many);
       const uint64_t any_word = (uint64_t)__reduce_or_sync(0xffffffffu, whi) << 32 | __reduce_or_sync(0xffffffffu, wlo);
       nearest = __reduce_min_sync(0xffffffffu, nearest);
+      farthest = __reduce_max_sync(0xffffffffu, farthest);
 
       const int64_t kvrow = (int64_t)a.H_kv * D * ES;  // bytes per slot
       const int64_t base = ((int64_t)b * a.cap * a.H_kv + kvh) * D * ES;
@@ -338,6 +349,7 @@ tree_tc(const __grid_constant__ TreeArgs a, const __grid_constant__ CUtensorMap 
         const uint32_t st = smem_u32(sm + (B16 ? L::OFF_KV + sl * 2 * L::KV : L::OFF_RAW + sl * L::RAW_TILE));
         constexpr int VOFF = B16 ? L::KV : kTile * D;
         by_tma = (by_tma & ~(1u << sl)) | (uint32_t)run << sl;
+        if (lt == 0) me.what = run ? kTma : 0;
         if (run) {
           if (lt == 0) {
             if (!B16 && t >= L::SLOTS && !wait(b_raw + 8 * sl, t / L::SLOTS - 1)) ok = false;
@@ -355,11 +367,14 @@ tree_tc(const __grid_constant__ TreeArgs a, const __grid_constant__ CUtensorMap 
                 tma_load_3d(st, &map_k, 0, kvh, z, bt);
                 tma_load_3d(st + VOFF, &map_v, 0, kvh, z, bt);
               }
-              tma_out |= 1u << sl;
             }
           }
           ok = __shfl_sync(0xffffffffu, (int)ok, 0) != 0;
           if (!ok) return;
+          tma_odd ^= 1u << sl;
+          tma_any |= 1u << sl;
+          // bf16: the MMA warp waits for the copy itself
+          if (B16 && lane == 0) mbar_arrive(b_full + 8 * sl);
         } else {
           constexpr int CH = D * ES / 16, RPI = 128 / CH;  // pieces per row, rows per pass
           const int ch = lt % CH;
@@ -378,56 +393,85 @@ tree_tc(const __grid_constant__ TreeArgs a, const __grid_constant__ CUtensorMap 
             }
           }
         }
-        // ---- this lane's two keys: scales (warp 2 V's, warp 3 K's) and who sees them
-        int j[2];
-        uint32_t mk[2];
-        uint64_t bit[2];
-        bool drafts = last >= len;
+        // ---- scales of the 8-bit rows: a warp's lanes bring V's, another's K's
+        if constexpr (!B16) {
+          const int who = (lw - t) & 3;
+          if (who == 1 || who == 2) {
 #pragma unroll
-        for (int e = 0; e < 2; ++e) {
-          const int r = 32 * e + lane, x = (tail + r) & (L::LIST - 1);
-          const bool on = r < n;
-          j[e] = on ? lidx[x] : 0;
-          mk[e] = on ? lmsk[x] : 0u;
-          if constexpr (!B16) {
-            if (lw >= 2) {
-              float* dst = (lw == 2 ? me.vs : me.ks) + r;
-              if (on) cp_async4(smem_u32(dst), (lw == 2 ? vsc : ksc) + j[e]);
+            for (int e = 0; e < 2; ++e) {
+              const int r = 32 * e + lane;
+              float* dst = (who == 1 ? me.vs : me.ks) + r;
+              if (r < n) cp_async4(smem_u32(dst), (who == 1 ? vsc : ksc) + lidx[(tail + r) & (L::LIST - 1)]);
               else *dst = 0.0f;
             }
           }
-          bit[e] = on ? ~0ull : 0ull;
-          if (drafts && on && j[e] >= len) {  // a drafted key: its token's bit, its position
-            bit[e] = 1ull << (j[e] - len);
-            j[e] = len + __popcll(tree_word(a, b, j[e] - len)) - 1;
+        }
+        // ---- who sees its keys: one warp, the others go on; a lane has two keys, then two tokens
+        if (((lw - t) & 3) == 0) {
+          int j[2];
+          uint32_t mk[2], valid[2];
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            const int r = 32 * e + lane, x = (tail + r) & (L::LIST - 1);
+            j[e] = r < n ? lidx[x] : 0;
+            mk[e] = r < n ? lmsk[x] : 0u;
+            valid[e] = n >= 32 * e + 32 ? ~0u : n > 32 * e ? (1u << (n - 32 * e)) - 1u : 0u;
           }
+          if (last < min(nearest, len)) {
+            // before every window and the drafted tokens: for each group some token has, the
+            // tile's keys that have it; a token sees the union of its groups' keys
+            for (uint32_t g = many; g; g &= g - 1) {
+              const int at = __ffs(g) - 1;
+              const unsigned s0 = __ballot_sync(0xffffffffu, mk[0] >> at & 1u), s1 = __ballot_sync(0xffffffffu, mk[1] >> at & 1u);
+              if (lane == 0) sets[at] = (uint64_t)s1 << 32 | s0;
+            }
+            __syncwarp();
+            for (int i = lane; i < ntok; i += 32) {
+              uint64_t w = 0ull;
+              for (uint32_t g = tok[i].mask; g; g &= g - 1) w |= sets[__ffs(g) - 1];
+              me.see[i] = w;
+            }
+          } else if (first >= farthest && last < len) {  // inside every window
+            for (int i = lane; i < ntok; i += 32)
+              me.see[i] = tok[i].word ? (uint64_t)valid[1] << 32 | valid[0] : 0ull;
+          } else {
+            uint64_t bit[2];
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+              bit[e] = valid[e] >> lane & 1u ? ~0ull : 0ull;
+              if (bit[e] && j[e] >= len) {  // a drafted key: its token's bit, its position
+                bit[e] = 1ull << (j[e] - len);
+                j[e] = len + __popcll(tree_word(a, b, j[e] - len)) - 1;
+              }
+            }
+            for (int i = 0; i < ntok; ++i) {
+              const Token y = tok[i];
+              const unsigned s0 = __ballot_sync(0xffffffffu, (y.word & bit[0]) != 0ull && (j[0] >= y.near || (mk[0] & y.mask) != 0u));
+              const unsigned s1 = __ballot_sync(0xffffffffu, (y.word & bit[1]) != 0ull && (j[1] >= y.near || (mk[1] & y.mask) != 0u));
+              if (lane == 0) me.see[i] = (uint64_t)s1 << 32 | s0;
+            }
+          }
+          if (lane == 0) me.end = 0;
+          __syncwarp();
+          if (B16 && lane == 0) mbar_arrive(b_meta + 8 * (t & (kMeta - 1)));
         }
-#pragma unroll 4
-        for (int i = lw; i < ntok; i += 4) {
-          const Token k = tok[i];
-          const unsigned s0 = __ballot_sync(0xffffffffu, (k.word & bit[0]) != 0ull && (j[0] >= k.near || (mk[0] & k.mask) != 0u));
-          const unsigned s1 = __ballot_sync(0xffffffffu, (k.word & bit[1]) != 0ull && (j[1] >= k.near || (mk[1] & k.mask) != 0u));
-          if (lane == 0) me.see[i] = (uint64_t)s1 << 32 | s0;
-        }
-        if (lt == 0) me.end = 0;
         tail += n;
       };
       // Hands tile x over, its copies (the TMA's, or this thread's own) having landed.
       auto finish = [&](int x, bool end) {
         const int sl = x % L::SLOTS;
         const bool run = !end && (by_tma >> sl & 1u);
-        if (run) {
-          if (!(ok = wait_all(b_tma + 8 * sl, tma_par >> sl & 1u))) return;
-          tma_par ^= 1u << sl;
-          tma_out &= ~(1u << sl);
-        }
+        if (B16 && run) return;
+        if (run && !(ok = wait_all(b_tma + 8 * sl, (tma_odd >> sl & 1u) ^ 1u))) return;
         if constexpr (!B16) {
           if (x >= S && !(ok = wait_all(b_empty + 8 * (x % S), x / S - 1))) return;
           if (!end) {
             const uint32_t raw = smem_u32(sm + L::OFF_RAW + sl * L::RAW_TILE);
             const uint32_t st = smem_u32(sm + L::OFF_KV + (x % S) * 2 * L::KV);
             constexpr int CH = D / 16, RPI = 128 / CH;
-            const int ch = lt % CH, c = 2 * (ch & 3);
+            // (16 columns are two 16-byte chunks of the operand tile's row; lanes of the second
+            // box store theirs in the other order, so that eight lanes meet all banks)
+            const int ch = lt % CH, c = 2 * (ch & 3), second = (ch / 4) & 1;
 #pragma unroll 2
             for (int r = lt / CH; r < kTile; r += RPI) {
               const uint4 y0 = lds128(raw + r * D + 16 * ch), y1 = lds128(raw + kTile * D + r * D + 16 * ch);
@@ -437,13 +481,18 @@ tree_tc(const __grid_constant__ TreeArgs a, const __grid_constant__ CUtensorMap 
                 uint32_t h[8];
 #pragma unroll
                 for (int i = 0; i < 4; ++i) codes_f16x2<FMT>(w[i], h[2 * i], h[2 * i + 1]);
-                // 16 columns are two 16-byte chunks of the operand tile's row
                 const uint32_t dst = st + v * L::KV + (ch / 4) * L::KBOX + r * 128;
-                sts128(dst + ((c ^ (r & 7)) << 4), h[0], h[1], h[2], h[3]);
-                sts128(dst + (((c + 1) ^ (r & 7)) << 4), h[4], h[5], h[6], h[7]);
+                uint32_t u[4], y[4];
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                  u[i] = second ? h[4 + i] : h[i];
+                  y[i] = second ? h[i] : h[4 + i];
+                }
+                sts128(dst + (((c + second) ^ (r & 7)) << 4), u[0], u[1], u[2], u[3]);
+                sts128(dst + (((c + 1 - second) ^ (r & 7)) << 4), y[0], y[1], y[2], y[3]);
               }
             }
-            if (lw == 2) {  // V scales (an infinite one reads as NaN)
+            if (((lw - x) & 3) == 1) {  // V scales, by the warp that brought them (an infinite one reads as NaN)
               Meta& me = meta[x & (kMeta - 1)];
               float y[2] = {me.vs[lane], me.vs[32 + lane]};
               uint32_t top = 0u, low = 0x7f800000u;
@@ -504,16 +553,21 @@ tree_tc(const __grid_constant__ TreeArgs a, const __grid_constant__ CUtensorMap 
         if constexpr (B16) {
           if (t >= S && !(ok = wait_all(b_empty + 8 * (t % S), t / S - 1))) break;
         }
-        if (lt == 0) meta[t & (kMeta - 1)].end = 1;
+        Meta& me = meta[t & (kMeta - 1)];
+        if (lt == 0) me.what = kEnd;
+        if (((lw - t) & 3) == 0 && lane == 0) {
+          me.end = 1;
+          if (B16) mbar_arrive(b_meta + 8 * (t & (kMeta - 1)));
+        }
         finish(t++, true);
       }
       ++seg;
       if (ok) meet();  // the list and the tokens start anew
     });
     cp_async_wait<0>();
-    if (lt == 0 && tma_out)  // giving up: copies in flight land before the CTA exits
+    if (lt == 0 && *abort_flag)  // giving up: copies in flight land before the CTA exits
       for (int i = 0; i < L::SLOTS; ++i)
-        if (tma_out >> i & 1u) mbar_drain(b_tma + 8 * i, tma_par >> i & 1u);
+        if (tma_any >> i & 1u) mbar_drain(b_tma + 8 * i, (tma_odd >> i & 1u) ^ 1u);
     __syncwarp();
   } else if (warp >= kMmaWarp) {
     // ---------------------------------------------------------------- MMA issue --
@@ -522,6 +576,7 @@ tree_tc(const __grid_constant__ TreeArgs a, const __grid_constant__ CUtensorMap 
       constexpr uint32_t IS = B16 ? idesc_bf16(kRows, kTile, 0) : idesc_f16(kRows, kTile, 0);
       constexpr uint32_t IPV = B16 ? idesc_bf16(kRows, D, 1) : idesc_f16(kRows, D, 1);
       int t = 0, c = 0, seg = 0;  // tiles with end marks, products, segments
+      uint32_t tma_par = 0u;      // by stage: parity of its next TMA copy (bf16)
       bool ok = true;
       for_segments(a, blockIdx.x, lane, [&](int64_t, int, int, int, int, int, int) {
         if (lane == 0 && ok) {
@@ -529,28 +584,35 @@ tree_tc(const __grid_constant__ TreeArgs a, const __grid_constant__ CUtensorMap 
           tc_fence_after();
           int ts = t, cs = c, cp = c;
           bool ended = false, fresh[2] = {true, true};
+          int have = -1;  // the tile whose metadata and rows are there
           long long t0 = clock64();
           while (ok && !(ended && cp == cs)) {
             bool some = false;
             const bool begun = NT == 2 && ((cs - c) & 1);  // this tile's second product
-            if (!ended && cs < cp + kSBuf && (begun || mbar_try_wait(b_full + 8 * (ts % S), (ts / S) & 1))) {
-              some = true;
-              if (!begun && meta[ts & (kMeta - 1)].end) {
-                ended = true;
-              } else {
-                tc_fence_after();
-                const uint64_t da = sw128_desc(smem_u32(sm + (begun ? L::QT : 0)), 16, 1024);
-                const uint64_t db = sw128_desc(smem_u32(sm + L::OFF_KV + (ts % S) * 2 * L::KV), 16, 1024);
-#pragma unroll
-                for (int kk = 0; kk < D / 16; ++kk)
-                  umma_ss(tmem + (cs % kSBuf) * kTile, da + (((kk / 4) * L::QBOX + (kk % 4) * 32) >> 4),
-                          db + (((kk / 4) * L::KBOX + (kk % 4) * 32) >> 4), IS, kk > 0);
-                umma_commit(b_s + 8 * (cs % kSBuf));
-                ++cs;
-                if (NT == 1 || begun) ++ts;
+            if (!ended && cs < cp + kSBuf && have != ts && mbar_test_wait(b_full + 8 * (ts % S), (ts / S) & 1)) {
+              const int what = meta[ts & (kMeta - 1)].what;
+              if (!B16 || what != kTma) {
+                have = ts;
+              } else if (mbar_test_wait(b_tma + 8 * (ts % S), tma_par >> (ts % S) & 1u)) {
+                tma_par ^= 1u << (ts % S);
+                have = ts;
               }
+              if (what == kEnd) ended = some = true;
             }
-            if (cp < cs && mbar_try_wait(b_p + 8 * (cp % kSBuf), (cp / kSBuf) & 1)) {
+            if (!ended && cs < cp + kSBuf && have == ts) {
+              some = true;
+              tc_fence_after();
+              const uint64_t da = sw128_desc(smem_u32(sm + (begun ? L::QT : 0)), 16, 1024);
+              const uint64_t db = sw128_desc(smem_u32(sm + L::OFF_KV + (ts % S) * 2 * L::KV), 16, 1024);
+#pragma unroll
+              for (int kk = 0; kk < D / 16; ++kk)
+                umma_ss(tmem + (cs % kSBuf) * kTile, da + (((kk / 4) * L::QBOX + (kk % 4) * 32) >> 4),
+                        db + (((kk / 4) * L::KBOX + (kk % 4) * 32) >> 4), IS, kk > 0);
+              umma_commit(b_s + 8 * (cs % kSBuf));
+              ++cs;
+              if (NT == 1 || begun) ++ts;
+            }
+            if (cp < cs && mbar_test_wait(b_p + 8 * (cp % kSBuf), (cp / kSBuf) & 1)) {
               some = true;
               tc_fence_after();
               const int wg = cp & 1, st = (t + (cp - c) / NT) % S;
@@ -615,7 +677,7 @@ tree_tc(const __grid_constant__ TreeArgs a, const __grid_constant__ CUtensorMap 
       const int c0 = c;
       for (;; t += NT == 1 ? 2 : 1, c += 2) {
         const Meta& me = meta[t & (kMeta - 1)];
-        if (!(ok = wait_all(b_full + 8 * (t % S), t / S))) return;
+        if (!(ok = B16 ? wait_all(b_meta + 8 * (t & (kMeta - 1)), t / kMeta) : wait_all(b_full + 8 * (t % S), t / S))) return;
         if (me.end) break;
         if (!B16 && c == c0) fac = a.sl2 * down[((seg & 1) * NT + (NT == 2 ? wg : 0)) * kRows + r];
         const uint64_t see = alive ? me.see[ti] : 0ull;
