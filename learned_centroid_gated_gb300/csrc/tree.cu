@@ -27,9 +27,7 @@ using namespace ptx;
 using namespace wmma16;
 
 constexpr int kTreeTile = 16;     // keys per pipeline tile (one MMA reduction step)
-constexpr int kTreeRows = 16;     // rows per warp (the MMA's M)
-constexpr int kTreeBlock = 256;   // raw keys per listing step
-constexpr int kTreeWarps = 1216;  // warps per launch: one wave of 8 per SM on 152 SMs
+constexpr int kTreeSms = 152;
 constexpr float kLn2 = 0.6931471805599453f;
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kPTop = 14.0f;  // 8-bit formats: log2 of the largest P times V scale (in fp16)
@@ -38,19 +36,22 @@ constexpr float kPTop = 14.0f;  // 8-bit formats: log2 of the largest P times V 
 // the 8-bit formats, their scales; per stage its keys' slots and masks; the listing.
 // bf16 rows are padded by 16 bytes (the eight rows of an ldmatrix phase start in different
 // banks).  8-bit rows are read as 16-byte pieces (see below) and swizzled instead.
-template <int D, int FMT>
+template <int D, int FMT, int NR>
 struct TreeLayout {
   static constexpr bool B16 = FMT == FOCUS_CACHE_BF16;
-  static constexpr int STAGES = B16 ? (D == 128 ? 3 : 5) : (D == 128 ? 5 : 8);
+  static constexpr int STAGES = B16 ? (D == 128 ? 3 : 5) : (D == 128 ? 4 : 6);
+  static constexpr int WARPS = B16 ? 8 : NR == 8 ? 11 : 8;  // per SM
+  static constexpr int BLOCK = B16 && D == 128 ? 128 : 256;  // raw keys per listing step
   static constexpr int ROW = B16 ? 2 * D + 16 : D;
   static constexpr int OFF_SCALE = 2 * kTreeTile * ROW;
   static constexpr int OFF_KEY = OFF_SCALE + (B16 ? 0 : 2 * kTreeTile * 4);
   static constexpr int STAGE = OFF_KEY + 2 * kTreeTile * 4;
   static constexpr int OFF_IDX = STAGES * STAGE;
-  static constexpr int OFF_MSK = OFF_IDX + kTreeBlock * 4;
-  static constexpr int OFF_CNT = OFF_MSK + kTreeBlock * 4;
+  static constexpr int OFF_MSK = OFF_IDX + BLOCK * 4;
+  static constexpr int OFF_CNT = OFF_MSK + BLOCK * 4;
   static constexpr int BYTES = (OFF_CNT + STAGES * 4 + 15) / 16 * 16;
   static_assert(STAGE % 16 == 0 && ROW % 16 == 0, "16-byte aligned rows");
+  static_assert(WARPS * (BYTES + 1024) <= 228 * 1024, "shared memory of an SM");
 };
 
 // Byte offset of 16-byte piece c of row r of a tile, 8-bit formats.  K is read by quads:
@@ -68,10 +69,16 @@ __device__ __forceinline__ int v_piece(int r, int c) {
   return p * D + 16 * (c ^ (((p >> 1) & 1) << 1));
 }
 
-template <int D, int FMT>
-__global__ void __launch_bounds__(32) tree_split(const __grid_constant__ TreeArgs a) {
-  using L = TreeLayout<D, FMT>;
+// NR: rows per warp.  16 fill the MMA's M; O = P V has P as its row operand.  With up to 8
+// the scores' upper half is empty, and O^T = V^T P^T takes the lane's own scores as its
+// column operand: half the products and half the accumulators of NR = 16.
+template <int D, int FMT, int NR>
+__global__ void __launch_bounds__(32, (TreeLayout<D, FMT, NR>::WARPS))
+tree_split(const __grid_constant__ TreeArgs a) {
+  using L = TreeLayout<D, FMT, NR>;
   constexpr bool B16 = L::B16;
+  constexpr int RL = NR / 8;             // rows of a lane: g (and g + 8)
+  constexpr int NB = NR == 8 ? D / 16 : D / 8;  // accumulator blocks
   constexpr int DB = D / 8;  // 8-bit formats: consecutive columns of a lane's V pieces
   extern __shared__ __align__(128) char smem[];
   const int lane = threadIdx.x, g = lane >> 2, t4 = lane & 3;
@@ -92,25 +99,24 @@ __global__ void __launch_bounds__(32) tree_split(const __grid_constant__ TreeArg
   for_segments(a, blockIdx.x, lane, [&](int64_t partial, int kvh, int rg, int b, int len, int js, int je) {
     // The rows: row x of the group is query head x % gq of drafted token x / gq.  With all
     // rows of one token its list of keys is exact and needs no test per element.
-    const int r_end = min(a.rows - rg * kTreeRows, kTreeRows);
-    const bool one_token = (rg * kTreeRows) / a.gq == (rg * kTreeRows + r_end - 1) / a.gq;
+    const int r_end = min(a.rows - rg * NR, NR);
+    const bool one_token = (rg * NR) / a.gq == (rg * NR + r_end - 1) / a.gq;
     const int rho = kvh / (a.H_kv / a.R);
     const uint32_t* M = a.mask + ((int64_t)b * a.R + rho) * a.cap;
 
-    // ---- this lane's two rows, g and g + 8
-    uint64_t word[2];
-    uint32_t mrow[2];
-    int near[2], pos[2];  // first position inside the window, own position
-    float fac[2];         // logit (log2) = MMA result * fac (* K scale)
-    uint32_t qa[D / 16][4];
+    // ---- this lane's rows, g and g + 8
+    uint64_t word[RL];
+    uint32_t mrow[RL];
+    int near[RL];         // first position inside the window
+    float fac[RL];        // logit (log2) = MMA result * fac (* K scale)
+    uint32_t qa[D / 16][2 * RL];
 #pragma unroll
-    for (int e = 0; e < 2; ++e) {
+    for (int e = 0; e < RL; ++e) {
       const int r = g + 8 * e;
       const bool on = r < r_end;
-      const int x = rg * kTreeRows + (on ? r : 0), t = x / a.gq, h = kvh * a.gq + x % a.gq;
+      const int x = rg * NR + (on ? r : 0), t = x / a.gq, h = kvh * a.gq + x % a.gq;
       word[e] = on ? tree_word(a, b, t) : 0ull;
-      pos[e] = len + __popcll(word[e]) - 1;
-      near[e] = word[e] ? pos[e] - a.w + 1 : INT_MAX;
+      near[e] = word[e] ? len + __popcll(word[e]) - a.w : INT_MAX;
       mrow[e] = word[e] ? __ldg(M + len + t) : 0u;
       fac[e] = a.sl2;
       const bf16* qr = a.q + (((int64_t)b * a.T + t) * a.H + h) * D;
@@ -119,7 +125,7 @@ __global__ void __launch_bounds__(32) tree_split(const __grid_constant__ TreeArg
 #pragma unroll
         for (int c = 0; c < D / 16; ++c) {
           qa[c][e] = on ? __ldg(qw + 8 * c + t4) : 0u;
-          qa[c][2 + e] = on ? __ldg(qw + 8 * c + 4 + t4) : 0u;
+          qa[c][RL + e] = on ? __ldg(qw + 8 * c + 4 + t4) : 0u;
         }
       } else {
         // Step (c, i) multiplies columns 64 c + 16 t4 + 4 i .. + 3: the order of a
@@ -143,20 +149,21 @@ __global__ void __launch_bounds__(32) tree_split(const __grid_constant__ TreeArg
 #pragma unroll
         for (int c = 0; c < D / 16; ++c) {
           qa[c][e] = pack_f16(f[4 * c] * up, f[4 * c + 1] * up);
-          qa[c][2 + e] = pack_f16(f[4 * c + 2] * up, f[4 * c + 3] * up);
+          qa[c][RL + e] = pack_f16(f[4 * c + 2] * up, f[4 * c + 3] * up);
         }
       }
     }
     // ---- what any row of the group sees
-    const uint32_t many = __reduce_or_sync(0xffffffffu, mrow[0] | mrow[1]);
-    const int nearest = __reduce_min_sync(0xffffffffu, min(near[0], near[1]));
-    const uint32_t wlo = __reduce_or_sync(0xffffffffu, (uint32_t)(word[0] | word[1]));
-    const uint32_t whi = __reduce_or_sync(0xffffffffu, (uint32_t)((word[0] | word[1]) >> 32));
+    const uint64_t any2 = word[0] | word[RL - 1];
+    const uint32_t many = __reduce_or_sync(0xffffffffu, mrow[0] | mrow[RL - 1]);
+    const int nearest = __reduce_min_sync(0xffffffffu, min(near[0], near[RL - 1]));
+    const uint32_t wlo = __reduce_or_sync(0xffffffffu, (uint32_t)any2);
+    const uint32_t whi = __reduce_or_sync(0xffffffffu, (uint32_t)(any2 >> 32));
     const uint64_t any_word = (uint64_t)whi << 32 | wlo;
 
     // ---- listing: keys of [js, je) in blocks, tiles issued from a block's list
     int jb = js, ncomp = 0, at = 0;
-    constexpr int MW = kTreeBlock / 32;
+    constexpr int MW = L::BLOCK / 32;
     uint32_t mw[MW];
 #pragma unroll
     for (int t = 0; t < MW; ++t) {
@@ -190,11 +197,11 @@ __global__ void __launch_bounds__(32) tree_split(const __grid_constant__ TreeArg
           if (ok) {
             const int x = ncomp + __popc(bal & lanemask_lt());
             idx[x] = j;
-            msk[x] = mw[t];
+            if (!one_token) msk[x] = mw[t];
           }
           ncomp += __popc(bal);
         }
-        jb += kTreeBlock;
+        jb += L::BLOCK;
 #pragma unroll
         for (int t = 0; t < MW; ++t) {  // the next block's words, in flight meanwhile
           const int j = jb + 32 * t + lane;
@@ -206,7 +213,7 @@ __global__ void __launch_bounds__(32) tree_split(const __grid_constant__ TreeArg
       const int n = min(kTreeTile, ncomp - at);
       const uint32_t st = ring + s * L::STAGE;
       if (lane == 0) cnt[s] = n;
-      if (lane < n) {
+      if (!one_token && lane < n) {
         int* key = reinterpret_cast<int*>(smem + s * L::STAGE + L::OFF_KEY);
         key[lane] = idx[at + lane];
         key[kTreeTile + lane] = (int)msk[at + lane];
@@ -232,10 +239,11 @@ __global__ void __launch_bounds__(32) tree_split(const __grid_constant__ TreeArg
       return true;
     };
 
-    float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.0f, 0.0f};
-    float acc[DB][4];
+    float m[RL], l[RL], acc[NB][4];
 #pragma unroll
-    for (int i = 0; i < DB; ++i)
+    for (int r = 0; r < RL; ++r) m[r] = -INFINITY, l[r] = 0.0f;
+#pragma unroll
+    for (int i = 0; i < NB; ++i)
 #pragma unroll
       for (int e = 0; e < 4; ++e) acc[i][e] = 0.0f;
     __syncwarp();  // zeroed stages (and the last stretch's reads) before the first copy
@@ -257,8 +265,9 @@ __global__ void __launch_bounds__(32) tree_split(const __grid_constant__ TreeArg
         for (int c = 0; c < D / 16; ++c) {
           uint32_t r0, r1, r2, r3;
           ldsm_x4(ka + 32 * c, r0, r1, r2, r3);
-          mma_bf16(c0, qa[c][0], qa[c][1], qa[c][2], qa[c][3], r0, r1);
-          mma_bf16(c1, qa[c][0], qa[c][1], qa[c][2], qa[c][3], r2, r3);
+          const uint32_t* A = qa[c];
+          mma_bf16(c0, A[0], RL == 2 ? A[1] : 0u, A[RL], RL == 2 ? A[2 * RL - 1] : 0u, r0, r1);
+          mma_bf16(c1, A[0], RL == 2 ? A[1] : 0u, A[RL], RL == 2 ? A[2 * RL - 1] : 0u, r2, r3);
         }
       } else {
 #pragma unroll
@@ -269,8 +278,11 @@ __global__ void __launch_bounds__(32) tree_split(const __grid_constant__ TreeArg
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
             const uint32_t* A = qa[4 * c + i];
-            mma_f16(c0, A[0], A[1], A[2], A[3], codes_f16<FMT>(xw[i]), codes_f16<FMT>(xw[i] >> 16));
-            mma_f16(c1, A[0], A[1], A[2], A[3], codes_f16<FMT>(yw[i]), codes_f16<FMT>(yw[i] >> 16));
+            uint32_t b0, b1, b2, b3;
+            codes_f16x2<FMT>(xw[i], b0, b1);
+            codes_f16x2<FMT>(yw[i], b2, b3);
+            mma_f16(c0, A[0], RL == 2 ? A[1] : 0u, A[RL], RL == 2 ? A[2 * RL - 1] : 0u, b0, b1);
+            mma_f16(c1, A[0], RL == 2 ? A[1] : 0u, A[RL], RL == 2 ? A[2 * RL - 1] : 0u, b2, b3);
           }
         }
       }
@@ -291,9 +303,9 @@ __global__ void __launch_bounds__(32) tree_split(const __grid_constant__ TreeArg
           lv[e] = __log2f(fmaxf(fabsf(vf[e]), kTinyScale)) - kPTop;
         }
       }
-      bool see[2][4];
+      bool see[RL][4];
 #pragma unroll
-      for (int e = 0; e < 4; ++e) see[0][e] = see[1][e] = kk[e] < n;
+      for (int e = 0; e < 4; ++e) see[0][e] = see[RL - 1][e] = kk[e] < n;
       if (!one_token) {
         const int* key = reinterpret_cast<const int*>(smem + s * L::STAGE + L::OFF_KEY);
         const bool drafts = key[n - 1] >= len;  // slots ascend in a list
@@ -309,14 +321,14 @@ __global__ void __launch_bounds__(32) tree_split(const __grid_constant__ TreeArg
             bit = 1ull << (j - len);
           }
 #pragma unroll
-          for (int r = 0; r < 2; ++r)
+          for (int r = 0; r < RL; ++r)
             see[r][e] = (word[r] & bit) != 0ull && (p >= near[r] || (mk & mrow[r]) != 0u);
         }
       }
-      float corr[2];
-      float p[2][4];
+      float corr[RL];
+      float p[RL][4];
 #pragma unroll
-      for (int r = 0; r < 2; ++r) {
+      for (int r = 0; r < RL; ++r) {
 #pragma unroll
         for (int e = 0; e < 4; ++e) sx[r][e] = see[r][e] ? sx[r][e] * kf[e] * fac[r] : -INFINITY;
         float mt = fmaxf(fmaxf(sx[r][0] + lv[0], sx[r][1] + lv[1]), fmaxf(sx[r][2] + lv[2], sx[r][3] + lv[3]));
@@ -330,46 +342,56 @@ __global__ void __launch_bounds__(32) tree_split(const __grid_constant__ TreeArg
         l[r] = l[r] * corr[r] + ((p[r][0] + p[r][1]) + (p[r][2] + p[r][3]));
         m[r] = mn;
       }
-      uint32_t pa[4];
-      if constexpr (B16) {
-        // P rounded to bf16 for the tensor core, as in the forward pass; l sums it unrounded
-        pa[0] = pack_bf16(p[0][0], p[0][1]);
-        pa[1] = pack_bf16(p[1][0], p[1][1]);
-        pa[2] = pack_bf16(p[0][2], p[0][3]);
-        pa[3] = pack_bf16(p[1][2], p[1][3]);
-      } else {
-        float y[2][4];
+      // P rounded for the tensor core (bf16 as in the forward pass, or fp16); l sums it
+      // unrounded.  pa[2 r + h]: row r's keys of half h.
+      uint32_t pa[2 * RL];
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          y[0][e] = see[0][e] ? p[0][e] * vf[e] : 0.0f;
-          y[1][e] = see[1][e] ? p[1][e] * vf[e] : 0.0f;
-        }
-        pa[0] = pack_f16(y[0][0], y[0][1]);
-        pa[1] = pack_f16(y[1][0], y[1][1]);
-        pa[2] = pack_f16(y[0][2], y[0][3]);
-        pa[3] = pack_f16(y[1][2], y[1][3]);
-      }
-      if (__any_sync(0xffffffffu, corr[0] != 1.0f || corr[1] != 1.0f)) {
+      for (int r = 0; r < RL; ++r) {
+        if constexpr (B16) {
+          pa[2 * r] = pack_bf16(p[r][0], p[r][1]);
+          pa[2 * r + 1] = pack_bf16(p[r][2], p[r][3]);
+        } else {
+          float y[4];
 #pragma unroll
-        for (int i = 0; i < DB; ++i) {
-          acc[i][0] *= corr[0];
-          acc[i][1] *= corr[0];
-          acc[i][2] *= corr[1];
-          acc[i][3] *= corr[1];
+          for (int e = 0; e < 4; ++e) y[e] = see[r][e] ? p[r][e] * vf[e] : 0.0f;
+          pa[2 * r] = pack_f16(y[0], y[1]);
+          pa[2 * r + 1] = pack_f16(y[2], y[3]);
         }
       }
+      if (__any_sync(0xffffffffu, corr[0] != 1.0f || corr[RL - 1] != 1.0f)) {
+        // the factor of accumulator e: NR = 8 has rows 2 t4, 2 t4 + 1 as columns (their
+        // statistics sit in lanes 8 t4, 8 t4 + 4), NR = 16 has rows g, g + 8
+        float f[4];
+        if constexpr (NR == 8) {
+          f[0] = f[2] = __shfl_sync(0xffffffffu, corr[0], 8 * t4);
+          f[1] = f[3] = __shfl_sync(0xffffffffu, corr[0], 8 * t4 + 4);
+        } else {
+          f[0] = f[1] = corr[0];
+          f[2] = f[3] = corr[RL - 1];
+        }
+#pragma unroll
+        for (int i = 0; i < NB; ++i)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) acc[i][e] *= f[e];
+      }
       if constexpr (B16) {
-        const uint32_t va = st + (kTreeTile + (lane & 15)) * L::ROW + (lane >> 4) * 16;
+        const uint32_t va = st + (kTreeTile + (NR == 8 ? (lane & 7) + ((lane >> 4) << 3) : (lane & 15))) * L::ROW +
+                            (NR == 8 ? (lane >> 3) & 1 : lane >> 4) * 16;
 #pragma unroll
         for (int i = 0; i < D / 16; ++i) {
           uint32_t r0, r1, r2, r3;
           ldsm_x4_t(va + 32 * i, r0, r1, r2, r3);
-          mma_bf16(acc[2 * i], pa[0], pa[1], pa[2], pa[3], r0, r1);
-          mma_bf16(acc[2 * i + 1], pa[0], pa[1], pa[2], pa[3], r2, r3);
+          if constexpr (NR == 8) {
+            mma_bf16(acc[i], r0, r1, r2, r3, pa[0], pa[1]);
+          } else {
+            mma_bf16(acc[2 * i], pa[0], pa[2], pa[1], pa[3], r0, r1);
+            mma_bf16(acc[2 * i + 1], pa[0], pa[2], pa[1], pa[3], r2, r3);
+          }
         }
       } else {
-        // rows 2 t4, 2 t4 + 1 and those + 8 of columns DB g .. DB g + DB - 1: byte i of a
-        // row pair is the B operand of block i, whose column g is column DB g + i of O
+        // keys 2 t4, 2 t4 + 1 and those + 8 of columns DB g .. DB g + DB - 1: byte i of a key
+        // pair is what the MMA takes for column DB g + i of O, as column g of block i
+        // (NR = 16) or as row g (+ 8) of block i / 2
         uint32_t vw[4][DB / 4];
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
@@ -387,9 +409,16 @@ __global__ void __launch_bounds__(32) tree_split(const __grid_constant__ TreeArg
           for (int hh = 0; hh < 2; ++hh) {
             const uint32_t sel = hh ? 0x7362u : 0x5140u;
             const uint32_t x = __byte_perm(vw[0][i], vw[1][i], sel), y = __byte_perm(vw[2][i], vw[3][i], sel);
-            const int blk = 4 * i + 2 * hh;
-            mma_f16(acc[blk], pa[0], pa[1], pa[2], pa[3], codes_f16<FMT>(x), codes_f16<FMT>(y));
-            mma_f16(acc[blk + 1], pa[0], pa[1], pa[2], pa[3], codes_f16<FMT>(x >> 16), codes_f16<FMT>(y >> 16));
+            uint32_t x0, x1, y0, y1;
+            codes_f16x2<FMT>(x, x0, x1);
+            codes_f16x2<FMT>(y, y0, y1);
+            if constexpr (NR == 8) {
+              mma_f16(acc[2 * i + hh], x0, x1, y0, y1, pa[0], pa[1]);
+            } else {
+              const int blk = 4 * i + 2 * hh;
+              mma_f16(acc[blk], pa[0], pa[2], pa[1], pa[3], x0, y0);
+              mma_f16(acc[blk + 1], pa[0], pa[2], pa[1], pa[3], x1, y1);
+            }
           }
         }
       }
@@ -398,34 +427,48 @@ __global__ void __launch_bounds__(32) tree_split(const __grid_constant__ TreeArg
       else cp_async_commit();
     }
     // ---- this segment's partial
-    const int64_t slot = partial * kTreeRows;
+    const int64_t slot = partial * NR;
 #pragma unroll
-    for (int r = 0; r < 2; ++r) {
+    for (int r = 0; r < RL; ++r) {
       l[r] += __shfl_xor_sync(0xffffffffu, l[r], 1);
       l[r] += __shfl_xor_sync(0xffffffffu, l[r], 2);
-      const int row = g + 8 * r;
-      if (row >= r_end) continue;
-      if (t4 == 0) a.part_ml[slot + row] = make_float2(m[r], l[r]);
-      float* dst = a.part_acc + (slot + row) * D;
-      if constexpr (B16) {
+      if (t4 == 0 && g + 8 * r < r_end) a.part_ml[slot + g + 8 * r] = make_float2(m[r], l[r]);
+    }
 #pragma unroll
-        for (int i = 0; i < DB; ++i)
-          *reinterpret_cast<float2*>(dst + 8 * i + 2 * t4) = make_float2(acc[i][2 * r], acc[i][2 * r + 1]);
-      } else {
+    for (int e = 0; e < 2; ++e) {
+      if constexpr (NR == 8) {  // row 2 t4 + e
+        if (2 * t4 + e >= r_end) continue;
+        float* dst = a.part_acc + (slot + 2 * t4 + e) * D;
 #pragma unroll
-        for (int e = 0; e < 2; ++e)
+        for (int i = 0; i < NB; ++i) {
+          if constexpr (B16) {
+            dst[16 * i + g] = acc[i][e];
+            dst[16 * i + g + 8] = acc[i][2 + e];
+          } else {
+            *reinterpret_cast<float2*>(dst + DB * g + 2 * i) = make_float2(acc[i][e], acc[i][2 + e]);
+          }
+        }
+      } else {  // row g + 8 e
+        if (g + 8 * e >= r_end) continue;
+        float* dst = a.part_acc + (slot + g + 8 * e) * D;
+        if constexpr (B16) {
 #pragma unroll
-          for (int i = 0; i < DB; i += 4)
-            *reinterpret_cast<float4*>(dst + DB * (2 * t4 + e) + i) =
-                make_float4(acc[i][2 * r + e], acc[i + 1][2 * r + e], acc[i + 2][2 * r + e], acc[i + 3][2 * r + e]);
+          for (int i = 0; i < NB; ++i)
+            *reinterpret_cast<float2*>(dst + 8 * i + 2 * t4) = make_float2(acc[i][2 * e], acc[i][2 * e + 1]);
+        } else {
+#pragma unroll
+          for (int c = 0; c < 2; ++c)
+#pragma unroll
+            for (int i = 0; i < NB; i += 4)
+              *reinterpret_cast<float4*>(dst + DB * (2 * t4 + c) + i) =
+                  make_float4(acc[i][2 * e + c], acc[i + 1][2 * e + c], acc[i + 2][2 * e + c], acc[i + 3][2 * e + c]);
+        }
       }
     }
   });
 }
 
 // ------------------------------------------------------------------------ combine --
-constexpr int kTreeCombWarps = 4;
-
 template <int FMT>
 __device__ __forceinline__ float cache_value(const void* x, int64_t at) {
   if constexpr (FMT == FOCUS_CACHE_BF16) return __bfloat162float(reinterpret_cast<const bf16*>(x)[at]);
@@ -439,9 +482,9 @@ __device__ __forceinline__ float cache_value(const void* x, int64_t at) {
 // One row again, key by key, without the keys that it does not see: a NaN or an infinity in
 // the V row of such a key, which other rows of the MMA do see, has met a zero weight there
 // and spoilt the sum.  Only rows that came out not finite get here.
-template <int D, int FMT>
+template <int D, int FMT, int NT>
 __device__ __noinline__ float row_by_hand(const TreeArgs& a, int b, int t, int h, int len, float lse2,
-                                          float* weight /* shared, 32 * kTreeCombWarps */) {
+                                          float* weight /* shared, NT */, unsigned* bits /* shared, NT / 32 */) {
   const int kvh = h / a.gq, rho = kvh / (a.H_kv / a.R);
   const uint32_t* M = a.mask + ((int64_t)b * a.R + rho) * a.cap;
   const uint64_t word = tree_word(a, b, t);
@@ -450,7 +493,6 @@ __device__ __noinline__ float row_by_hand(const TreeArgs& a, int b, int t, int h
   const bf16* q = a.q + (((int64_t)b * a.T + t) * a.H + h) * D;
   const int64_t sc = ((int64_t)b * a.H_kv + kvh) * a.cap;
   float out = 0.0f;
-  constexpr int NT = 32 * kTreeCombWarps;
   for (int j0 = 0; j0 < len + a.T; j0 += NT) {
     const int j = j0 + threadIdx.x;
     bool see = j < len + a.T;
@@ -473,7 +515,6 @@ __device__ __noinline__ float row_by_hand(const TreeArgs& a, int b, int t, int h
     __syncthreads();
     weight[threadIdx.x] = x;
     const unsigned seen = __ballot_sync(0xffffffffu, see);
-    unsigned* bits = reinterpret_cast<unsigned*>(weight + NT);
     if ((threadIdx.x & 31) == 0) bits[threadIdx.x >> 5] = seen;
     __syncthreads();
     if (threadIdx.x < D)
@@ -485,16 +526,21 @@ __device__ __noinline__ float row_by_hand(const TreeArgs& a, int b, int t, int h
   return out;
 }
 
-// Merge the partials of one row: grid (T * H, B).  Warp g folds partials g (mod the warps)
-// into a running (max, sum, acc), a lane D / 32 columns; then every thread folds the warps'
-// results in order.  A programmatic dependent of the kernel that writes the partials.
-template <int D, int FMT>
-__global__ void __launch_bounds__(32 * kTreeCombWarps) tree_combine(const __grid_constant__ TreeArgs a) {
-  constexpr int CPL = D / 32, W = kTreeCombWarps;
-  __shared__ float wm[W], wl[W];
-  __shared__ __align__(16) float wacc[W][D];
-  __shared__ float weight[33 * W];
-  const int g = threadIdx.x >> 5, lane = threadIdx.x & 31;
+// Merge the partials of one row: grid (T * H, B), NT threads.  A pass takes NT of the
+// slices that may hold a part of the row's sequence: a thread finds out whether its slice
+// does, and its partial's (max, sum); with the largest maximum of all the weights are known,
+// and NT / D groups of D threads sum the weighted partials, each a share of them, with no
+// chain from one to the next (merging them pair by pair, a warp's share in order, took 46 us
+// behind 128K tokens).  A programmatic dependent of the kernel that writes the partials.
+template <int D, int FMT, int NT>
+__global__ void __launch_bounds__(NT) tree_combine(const __grid_constant__ TreeArgs a) {
+  constexpr int NG = NT / D, NW = NT / 32;
+  __shared__ float weight[NT];
+  __shared__ int64_t place[NT];
+  __shared__ float sums[NG][D];
+  __shared__ float red[2][NW];
+  __shared__ unsigned bits[NW];
+  const int tid = threadIdx.x, wp = tid >> 5, lane = tid & 31, g = tid / D, d = tid % D;
   const int b = blockIdx.y, t = blockIdx.x / a.H, h = blockIdx.x % a.H;
   const int kvh = h / a.gq, row = t * a.gq + h % a.gq, rg = row / a.grp;
   const int64_t ln = (int64_t)kvh * a.nrg + rg;
@@ -514,63 +560,87 @@ __global__ void __launch_bounds__(32 * kTreeCombWarps) tree_combine(const __grid
   const Stretch s = stretch_of(a, len);
   const int64_t whole = total * a.H_kv * a.nrg;
   const int ns = slices_of(a, whole);
+  const bool live = s.units > 0 && tree_word(a, b, t) != 0ull;
+  const int first = live ? (int)max((int64_t)0, from * ns / whole - 1) : 0;
+  const int last = live ? (int)min((int64_t)ns - 1, (from + s.weight) * ns / whole + 1) : -1;
+  const int n = (last - first + 1) * a.parts;
   asm volatile("griddepcontrol.wait;" ::: "memory");
-  if (blockIdx.x == 0 && b == 0 && g == 0) {  // the call's status
+  if (blockIdx.x == 0 && b == 0 && wp == 0) {  // the call's status
     int code = 0;
     if (a.flags && total > 0)
       for (int x = lane; x < ns; x += 32) code = min(code, a.flags[x]);
     code = __reduce_min_sync(0xffffffffu, code);
     if (lane == 0) *a.status = code ? code : bad ? FOCUS_ERR_BOUNDS : 0;
   }
-  float m = -INFINITY, l = 0.0f, acc[CPL];
-#pragma unroll
-  for (int e = 0; e < CPL; ++e) acc[e] = 0.0f;
-  if (s.units > 0 && tree_word(a, b, t) != 0ull) {
-    const int64_t first = max((int64_t)0, from * ns / whole - 1);
-    const int64_t last = min((int64_t)ns - 1, (from + s.weight) * ns / whole + 1);
-    for (int64_t c = first * a.parts + g; c < (last + 1) * a.parts; c += W) {
-      const int64_t sl = c / a.parts;
+  float m = -INFINITY, l = 0.0f, acc = 0.0f;  // of all; this thread's shares
+  for (int base = 0; base < n; base += NT) {
+    const int c = base + tid;
+    float2 x = make_float2(-INFINITY, 0.0f);
+    int64_t slot = 0;
+    if (c < n) {
+      const int sl = first + c / a.parts;
       const int64_t lo = whole * sl / ns, hi = whole * (sl + 1) / ns;
-      if (units_before(a, s, lo - from) >= units_before(a, s, hi - from)) continue;  // no such partial
-      const int64_t slot = ((sl + ln * a.B + b) * a.parts + c % a.parts) * a.grp + row % a.grp;
-      const float2 x = a.part_ml[slot];
-      if (x.y == 0.0f) continue;  // no key of the slice is seen
-      float v[CPL];
-#pragma unroll
-      for (int e = 0; e < CPL; ++e) v[e] = a.part_acc[slot * D + 32 * e + lane];
-      const float mn = fmaxf(m, x.x), f0 = ex2(m - mn), f1 = ex2(x.x - mn);
-      l = l * f0 + x.y * f1;
-#pragma unroll
-      for (int e = 0; e < CPL; ++e) acc[e] = acc[e] * f0 + v[e] * f1;
-      m = mn;
+      if (units_before(a, s, lo - from) < units_before(a, s, hi - from)) {  // else no such partial
+        slot = ((sl + ln * a.B + b) * a.parts + c % a.parts) * a.grp + row % a.grp;
+        x = a.part_ml[slot];
+      }
     }
-  }
+    const bool some = x.y != 0.0f;  // a key of the slice is seen
+    float top = some ? x.x : -INFINITY;
 #pragma unroll
-  for (int e = 0; e < CPL; ++e) wacc[g][32 * e + lane] = acc[e];
-  if (lane == 0) wm[g] = m, wl[g] = l;
-  __syncthreads();
-  float top = -INFINITY, sum = 0.0f, out = 0.0f;
-  for (int i = 0; i < W; ++i)
-    if (wl[i] != 0.0f) top = fmaxf(top, wm[i]);
-  const int d = threadIdx.x;
-  for (int i = 0; i < W; ++i) {
-    if (wl[i] == 0.0f) continue;
-    const float f = ex2(wm[i] - top);
-    sum += wl[i] * f;
-    if (d < D) out += wacc[i][d] * f;
+    for (int o = 16; o; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+    if (lane == 0) red[0][wp] = top;
+    __syncthreads();
+    for (int i = 0; i < NW; ++i) top = fmaxf(top, red[0][i]);
+    // no maximum: nothing is seen, or all that is seen is NaN (a sum of NaN, which then makes
+    // the row NaN); the same in every thread
+    if (top == -INFINITY && !__syncthreads_or(some)) continue;
+    const float mn = fmaxf(m, top), f = m == -INFINITY ? 0.0f : ex2(m - mn);
+    const float w = some ? ex2(x.x - mn) : 0.0f;
+    l = l * f + (some ? x.y * w : 0.0f);
+    acc *= f;
+    m = mn;
+    weight[tid] = w;
+    place[tid] = slot * D;
+    __syncthreads();
+    const int end = min(NT, n - base);
+#pragma unroll 4
+    for (int i = g; i < end; i += NG) {
+      const float y = weight[i];
+      if (y != 0.0f) acc += y * a.part_acc[place[i] + d];
+    }
+    __syncthreads();
   }
-  const bool none = sum == 0.0f;
-  const float lse2 = top + log2f(sum);
-  out = none ? 0.0f : out / sum;
-  if (__syncthreads_or(d < D && !(fabsf(out) < INFINITY)))
-    out = row_by_hand<D, FMT>(a, b, t, h, len, lse2, weight);
-  if (d < D) a.o[(((int64_t)b * a.T + t) * a.H + h) * D + d] = __float2bfloat16_rn(out);
-  if (d == 0 && a.lse) a.lse[((int64_t)b * a.H + h) * a.T + t] = none ? -INFINITY : lse2 * kLn2;
+  sums[g][d] = acc;
+#pragma unroll
+  for (int o = 16; o; o >>= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
+  if (lane == 0) red[1][wp] = l;
+  __syncthreads();
+  float sum = 0.0f, out = 0.0f;
+  for (int i = 0; i < NW; ++i) sum += red[1][i];
+  if (tid < D)
+    for (int i = 0; i < NG; ++i) out += sums[i][d];
+  const bool empty = sum == 0.0f;
+  const float lse2 = m + log2f(sum);
+  out = empty ? 0.0f : out / sum;
+  if (__syncthreads_or(tid < D && !(fabsf(out) < INFINITY)))
+    out = row_by_hand<D, FMT, NT>(a, b, t, h, len, lse2, weight, bits);
+  if (tid < D) a.o[(((int64_t)b * a.T + t) * a.H + h) * D + d] = __float2bfloat16_rn(out);
+  if (tid == 0 && a.lse) a.lse[((int64_t)b * a.H + h) * a.T + t] = empty ? -INFINITY : lse2 * kLn2;
 }
 
 // ------------------------------------------------------------------------- launch --
 constexpr int kTreeTcRows = 128;  // rows of a product of the tensor-core kernel (the MMA's M)
-constexpr int kTreeTcSlices = 152;
+
+template <int NR>
+int split_warps_of(int d_head, int format) {  // per SM
+  constexpr int B = FOCUS_CACHE_BF16, E = FOCUS_CACHE_E4M3;
+  return d_head == 64 ? (format == B ? TreeLayout<64, B, NR>::WARPS : TreeLayout<64, E, NR>::WARPS)
+                      : (format == B ? TreeLayout<128, B, NR>::WARPS : TreeLayout<128, E, NR>::WARPS);
+}
+int split_warps(int d_head, int format, int rows) {
+  return rows == 8 ? split_warps_of<8>(d_head, format) : split_warps_of<16>(d_head, format);
+}
 
 struct TreePlan {
   int gq, rows, grp, nrg, parts, G, wfar;
@@ -582,11 +652,11 @@ TreePlan tree_plan(const focus_cache_params& p) {
   TreePlan t;
   t.gq = p.H / p.H_kv;
   t.rows = p.T * t.gq;
-  t.tc = t.rows > kTreeRows;
-  t.grp = !t.tc ? kTreeRows : t.rows > kTreeTcRows ? 2 * kTreeTcRows : kTreeTcRows;
+  t.tc = t.rows > 16;
+  t.grp = t.tc ? (t.rows > kTreeTcRows ? 2 * kTreeTcRows : kTreeTcRows) : t.rows > 8 ? 16 : 8;
   t.nrg = (t.rows + t.grp - 1) / t.grp;
   t.parts = t.grp == kTreeTcRows ? 2 : 1;
-  t.G = t.tc ? kTreeTcSlices : kTreeWarps;
+  t.G = kTreeSms * (t.tc ? 1 : split_warps(p.d_head, p.format, t.grp));
   const int64_t lanes = (int64_t)p.H_kv * t.nrg;
   const int64_t most = lanes * p.B * (((int64_t)p.cap + kTreeUnit - 1) / kTreeUnit) * kTreeNear;
   t.G = (int)std::max<int64_t>(1, std::min<int64_t>(t.G, most / kTreeNear));
@@ -602,32 +672,43 @@ TreePlan tree_plan(const focus_cache_params& p) {
   return t;
 }
 
-template <int D, int FMT>
-cudaError_t launch_tree(const TreeArgs& a, bool tc, cudaStream_t s) {
-  using L = TreeLayout<D, FMT>;
-  cudaError_t e;
-  if (tc) {
-    if ((e = launch_tree_tc(a, D, FMT, s)) != cudaSuccess) return e;
-  } else {
-    static std::atomic<uint64_t> done{0};
-    e = once_per_device(done, [] {
-      return cudaFuncSetAttribute(tree_split<D, FMT>, cudaFuncAttributePreferredSharedMemoryCarveout, 100);
-    });
-    if (e != cudaSuccess) return e;
-    tree_split<D, FMT><<<(unsigned)a.G, 32, L::BYTES, s>>>(a);
-    if ((e = cudaGetLastError()) != cudaSuccess) return e;
-  }
+template <int D, int FMT, int NR>
+cudaError_t launch_split(const TreeArgs& a, cudaStream_t s) {
+  static std::atomic<uint64_t> done{0};
+  const cudaError_t e = once_per_device(done, [] {
+    return cudaFuncSetAttribute(tree_split<D, FMT, NR>, cudaFuncAttributePreferredSharedMemoryCarveout, 100);
+  });
+  if (e != cudaSuccess) return e;
+  tree_split<D, FMT, NR><<<(unsigned)a.G, 32, TreeLayout<D, FMT, NR>::BYTES, s>>>(a);
+  return cudaGetLastError();
+}
+
+template <int D, int FMT, int NT>
+cudaError_t launch_combine(const TreeArgs& a, cudaStream_t s) {
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)(a.T * a.H), (unsigned)a.B);
-  cfg.blockDim = dim3(32 * kTreeCombWarps);
+  cfg.blockDim = dim3(NT);
   cfg.stream = s;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  if ((e = cudaLaunchKernelEx(&cfg, tree_combine<D, FMT>, a)) != cudaSuccess) return e;
-  return cudaGetLastError();
+  const cudaError_t e = cudaLaunchKernelEx(&cfg, tree_combine<D, FMT, NT>, a);
+  return e != cudaSuccess ? e : cudaGetLastError();
+}
+
+template <int D, int FMT>
+cudaError_t launch_tree(const TreeArgs& a, bool tc, cudaStream_t s) {
+  const cudaError_t e = tc             ? launch_tree_tc(a, D, FMT, s)
+                        : a.grp == 8 ? launch_split<D, FMT, 8>(a, s)
+                                     : launch_split<D, FMT, 16>(a, s);
+  if (e != cudaSuccess) return e;
+  // threads of the merge by the partials of a row, were all sequences alike
+  const int64_t each = (int64_t)a.G * a.parts / ((int64_t)a.H_kv * a.nrg * a.B);
+  return each > 256 ? launch_combine<D, FMT, 1024>(a, s)
+         : each > 16 ? launch_combine<D, FMT, 512>(a, s)
+                     : launch_combine<D, FMT, 128>(a, s);
 }
 
 }  // namespace
