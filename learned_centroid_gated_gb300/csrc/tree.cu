@@ -26,26 +26,28 @@ namespace {
 using namespace ptx;
 using namespace wmma16;
 
-constexpr int kTreeTile = 16;     // keys per pipeline tile (one MMA reduction step)
 constexpr int kTreeSms = 152;
 constexpr float kLn2 = 0.6931471805599453f;
 constexpr float kLog2e = 1.4426950408889634f;
-constexpr float kPTop = 14.0f;  // 8-bit formats: log2 of the largest P times V scale (in fp16)
+constexpr float kPTop = 14.0f;  // 8-bit formats: log2 of the largest P times V scale
 
-// Per-warp shared memory: a ring of tiles, each kTreeTile K rows, as many V rows and, in
-// the 8-bit formats, their scales; per stage its keys' slots and masks; the listing.
+// Per-warp shared memory: a ring of tiles, each KT K rows, as many V rows and, in the 8-bit
+// formats, their scales; per stage its keys' slots and masks; the listing.  8-bit tiles have
+// 32 keys: the work per key that is not a product (reference, exponentials, listing) and its
+// latency, not the memory, are what bounds them.
 // bf16 rows are padded by 16 bytes (the eight rows of an ldmatrix phase start in different
 // banks).  8-bit rows are read as 16-byte pieces (see below) and swizzled instead.
 template <int D, int FMT, int NR>
 struct TreeLayout {
   static constexpr bool B16 = FMT == FOCUS_CACHE_BF16;
-  static constexpr int STAGES = B16 ? (D == 128 ? 3 : 5) : (D == 128 ? 4 : 6);
+  static constexpr int KT = B16 ? 16 : 32;                  // keys per tile
+  static constexpr int STAGES = B16 ? (D == 128 ? 3 : 5) : (D == 128 ? 2 : 3);
   static constexpr int WARPS = B16 ? 8 : NR == 8 ? 11 : 8;  // per SM
   static constexpr int BLOCK = B16 && D == 128 ? 128 : 256;  // raw keys per listing step
   static constexpr int ROW = B16 ? 2 * D + 16 : D;
-  static constexpr int OFF_SCALE = 2 * kTreeTile * ROW;
-  static constexpr int OFF_KEY = OFF_SCALE + (B16 ? 0 : 2 * kTreeTile * 4);
-  static constexpr int STAGE = OFF_KEY + 2 * kTreeTile * 4;
+  static constexpr int OFF_SCALE = 2 * KT * ROW;
+  static constexpr int OFF_KEY = OFF_SCALE + (B16 ? 0 : 2 * KT * 4);
+  static constexpr int STAGE = OFF_KEY + 2 * KT * 4;
   static constexpr int OFF_IDX = STAGES * STAGE;
   static constexpr int OFF_MSK = OFF_IDX + BLOCK * 4;
   static constexpr int OFF_CNT = OFF_MSK + BLOCK * 4;
@@ -65,7 +67,7 @@ __device__ __forceinline__ int k_piece(int r, int c) {
 template <int D>
 __device__ __forceinline__ int v_piece(int r, int c) {
   if (D == 128) return r * D + 16 * (c ^ (2 * ((r >> 1) & 3)));
-  const int p = (r >> 1) | ((r & 1) << 3);
+  const int p = (r & 16) | ((r & 15) >> 1) | ((r & 1) << 3);
   return p * D + 16 * (c ^ (((p >> 1) & 1) << 1));
 }
 
@@ -77,6 +79,7 @@ __global__ void __launch_bounds__(32, (TreeLayout<D, FMT, NR>::WARPS))
 tree_split(const __grid_constant__ TreeArgs a) {
   using L = TreeLayout<D, FMT, NR>;
   constexpr bool B16 = L::B16;
+  constexpr int KT = L::KT, KH = KT / 16, KE = 4 * KH;  // keys of a tile, MMA steps, keys of a lane
   constexpr int RL = NR / 8;             // rows of a lane: g (and g + 8)
   constexpr int NB = NR == 8 ? D / 16 : D / 8;  // accumulator blocks
   constexpr int DB = D / 8;  // 8-bit formats: consecutive columns of a lane's V pieces
@@ -210,13 +213,13 @@ tree_split(const __grid_constant__ TreeArgs a) {
         at = 0;
         __syncwarp();
       }
-      const int n = min(kTreeTile, ncomp - at);
+      const int n = min(KT, ncomp - at);
       const uint32_t st = ring + s * L::STAGE;
       if (lane == 0) cnt[s] = n;
       if (!one_token && lane < n) {
         int* key = reinterpret_cast<int*>(smem + s * L::STAGE + L::OFF_KEY);
         key[lane] = idx[at + lane];
-        key[kTreeTile + lane] = (int)msk[at + lane];
+        key[KT + lane] = (int)msk[at + lane];
       }
       constexpr int CH = D * ES / 16, RPI = 32 / CH;  // 16-byte pieces per row, rows per instruction
       const int ch = lane % CH;
@@ -224,15 +227,17 @@ tree_split(const __grid_constant__ TreeArgs a) {
         const int64_t off = (int64_t)idx[at + rr] * kvrow * ES + 16 * ch;
         if constexpr (B16) {
           cp_async16(st + rr * L::ROW + 16 * ch, kb + off);
-          cp_async16(st + (kTreeTile + rr) * L::ROW + 16 * ch, vb + off);
+          cp_async16(st + (KT + rr) * L::ROW + 16 * ch, vb + off);
         } else {
           cp_async16(st + k_piece<D>(rr, ch), kb + off);
-          cp_async16(st + kTreeTile * D + v_piece<D>(rr, ch), vb + off);
+          cp_async16(st + KT * D + v_piece<D>(rr, ch), vb + off);
         }
       }
       if constexpr (!B16) {
-        const int rr = lane & 15;
-        if (rr < n) cp_async4(st + L::OFF_SCALE + 4 * lane, (lane < 16 ? ksc : vsc) + idx[at + rr]);
+        if (lane < n) {
+          cp_async4(st + L::OFF_SCALE + 4 * lane, ksc + idx[at + lane]);
+          cp_async4(st + L::OFF_SCALE + 4 * (KT + lane), vsc + idx[at + lane]);
+        }
       }
       cp_async_commit();
       at += n;
@@ -258,7 +263,11 @@ tree_split(const __grid_constant__ TreeArgs a) {
       __syncwarp();                    // ... and every lane's
       const int n = cnt[s];
       const uint32_t st = ring + s * L::STAGE;
-      float c0[4] = {0.0f, 0.0f, 0.0f, 0.0f}, c1[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+      float sc[2 * KH][4];  // scores of keys 8 i .. 8 i + 7
+#pragma unroll
+      for (int i = 0; i < 2 * KH; ++i)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) sc[i][e] = 0.0f;
       if constexpr (B16) {
         const uint32_t ka = st + ((lane & 7) + ((lane >> 4) << 3)) * L::ROW + ((lane >> 3) & 1) * 16;
 #pragma unroll
@@ -266,97 +275,115 @@ tree_split(const __grid_constant__ TreeArgs a) {
           uint32_t r0, r1, r2, r3;
           ldsm_x4(ka + 32 * c, r0, r1, r2, r3);
           const uint32_t* A = qa[c];
-          mma_bf16(c0, A[0], RL == 2 ? A[1] : 0u, A[RL], RL == 2 ? A[2 * RL - 1] : 0u, r0, r1);
-          mma_bf16(c1, A[0], RL == 2 ? A[1] : 0u, A[RL], RL == 2 ? A[2 * RL - 1] : 0u, r2, r3);
+          mma_bf16(sc[0], A[0], RL == 2 ? A[1] : 0u, A[RL], RL == 2 ? A[2 * RL - 1] : 0u, r0, r1);
+          mma_bf16(sc[1], A[0], RL == 2 ? A[1] : 0u, A[RL], RL == 2 ? A[2 * RL - 1] : 0u, r2, r3);
         }
       } else {
 #pragma unroll
         for (int c = 0; c < D / 64; ++c) {
-          const uint4 x = lds128(st + k_piece<D>(g, 4 * c + t4));
-          const uint4 y = lds128(st + k_piece<D>(g + 8, 4 * c + t4));
-          const uint32_t xw[4] = {x.x, x.y, x.z, x.w}, yw[4] = {y.x, y.y, y.z, y.w};
+          uint4 x[2 * KH];
+#pragma unroll
+          for (int h = 0; h < 2 * KH; ++h) x[h] = lds128(st + k_piece<D>(g + 8 * h, 4 * c + t4));
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
             const uint32_t* A = qa[4 * c + i];
-            uint32_t b0, b1, b2, b3;
-            codes_f16x2<FMT>(xw[i], b0, b1);
-            codes_f16x2<FMT>(yw[i], b2, b3);
-            mma_f16(c0, A[0], RL == 2 ? A[1] : 0u, A[RL], RL == 2 ? A[2 * RL - 1] : 0u, b0, b1);
-            mma_f16(c1, A[0], RL == 2 ? A[1] : 0u, A[RL], RL == 2 ? A[2 * RL - 1] : 0u, b2, b3);
+#pragma unroll
+            for (int h = 0; h < 2 * KH; ++h) {
+              uint32_t b0, b1;
+              codes_f16x2<FMT>(i == 0 ? x[h].x : i == 1 ? x[h].y : i == 2 ? x[h].z : x[h].w, b0, b1);
+              mma_f16(sc[h], A[0], RL == 2 ? A[1] : 0u, A[RL], RL == 2 ? A[2 * RL - 1] : 0u, b0, b1);
+            }
           }
         }
       }
-      // ---- logits of rows g, g + 8 and keys 2 t4, 2 t4 + 1, 8 + 2 t4, 9 + 2 t4
-      const int kk[4] = {2 * t4, 2 * t4 + 1, 2 * t4 + 8, 2 * t4 + 9};
-      float sx[2][4] = {{c0[0], c0[1], c1[0], c1[1]}, {c0[2], c0[3], c1[2], c1[3]}};
-      float kf[4] = {1.0f, 1.0f, 1.0f, 1.0f}, vf[4], lv[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-      if constexpr (!B16) {
-        const float* sc = reinterpret_cast<const float*>(smem + s * L::STAGE + L::OFF_SCALE);
+      // ---- logits (log2) of rows g, g + 8 and the lane's keys: 2 t4, 2 t4 + 1 of each eight
+      float sx[RL][KE], vf[KE], lv[KE];
+      const float* scale = reinterpret_cast<const float*>(smem + s * L::STAGE + L::OFF_SCALE);
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          kf[e] = sc[kk[e]];
-          vf[e] = kk[e] < n ? sc[kTreeTile + kk[e]] : 0.0f;
-          if (!(fabsf(vf[e]) < INFINITY)) vf[e] = __uint_as_float(0x7fc00000u);
-          // 8-bit formats: V's scales join P before it is rounded to fp16.  The reference m of
-          // a row is that of the product: the largest P vs of the keys that it sees is 2^14,
-          // so that what is smaller by up to 2^-38 still counts.
-          lv[e] = __log2f(fmaxf(fabsf(vf[e]), kTinyScale)) - kPTop;
-        }
+      for (int e = 0; e < KE; ++e) {
+        const int i = e >> 1, key = 8 * i + 2 * t4 + (e & 1);
+        const float kf = B16 ? 1.0f : scale[key];
+        if constexpr (!B16) vf[e] = scale[KT + key];
+#pragma unroll
+        for (int r = 0; r < RL; ++r) sx[r][e] = sc[i][2 * r + (e & 1)] * (kf * fac[r]);
       }
-      bool see[RL][4];
+      if (!one_token || n < KT) {  // keys beyond the tile's, and those that a row does not see
+        const int* keys = reinterpret_cast<const int*>(smem + s * L::STAGE + L::OFF_KEY);
+        const bool drafts = !one_token && keys[n - 1] >= len;  // slots ascend in a list
 #pragma unroll
-      for (int e = 0; e < 4; ++e) see[0][e] = see[RL - 1][e] = kk[e] < n;
-      if (!one_token) {
-        const int* key = reinterpret_cast<const int*>(smem + s * L::STAGE + L::OFF_KEY);
-        const bool drafts = key[n - 1] >= len;  // slots ascend in a list
+        for (int e = 0; e < KE; ++e) {
+          const int key = 8 * (e >> 1) + 2 * t4 + (e & 1);
+          bool see[RL];
+          see[0] = see[RL - 1] = key < n;
+          if (!B16 && key >= n) vf[e] = 0.0f;
+          if (!one_token && key < n) {
+            const int j = keys[key];
+            const uint32_t mk = (uint32_t)keys[KT + key];
+            int p = j;
+            uint64_t bit = ~0ull;
+            if (drafts && j >= len) {
+              p = len + __popcll(tree_word(a, b, j - len)) - 1;
+              bit = 1ull << (j - len);
+            }
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          if (kk[e] >= n) continue;
-          const int j = key[kk[e]];
-          const uint32_t mk = (uint32_t)key[kTreeTile + kk[e]];
-          int p = j;
-          uint64_t bit = ~0ull;
-          if (drafts && j >= len) {
-            p = len + __popcll(tree_word(a, b, j - len)) - 1;
-            bit = 1ull << (j - len);
+            for (int r = 0; r < RL; ++r)
+              see[r] = (word[r] & bit) != 0ull && (p >= near[r] || (mk & mrow[r]) != 0u);
           }
 #pragma unroll
           for (int r = 0; r < RL; ++r)
-            see[r][e] = (word[r] & bit) != 0ull && (p >= near[r] || (mk & mrow[r]) != 0u);
+            if (!see[r]) sx[r][e] = -INFINITY;
+        }
+      }
+      // ---- 8-bit formats: V's scales join P before it is rounded to fp16, and the reference
+      // m of a row is that of the product, which fp16 has to hold: its largest P vs is about
+      // 2^14, so that what is smaller by up to 2^-38 still counts.  Scales within 2^4 of
+      // another are bounded by one power of two, others (an outlier that a row may not even
+      // see) measured key by key.
+      float lift = 0.0f;
+      bool wide = false;
+      if constexpr (!B16) {
+        const uint32_t u = lane < n ? __float_as_uint(fabsf(scale[KT + lane])) : 0u;
+        const uint32_t top = __reduce_max_sync(0xffffffffu, u);
+        const uint32_t low = __reduce_min_sync(0xffffffffu, u ? u : 0x7f800000u);
+        wide = top >= 0x7f000000u || __uint_as_float(top) > 16.0f * __uint_as_float(low);
+        lift = (float)max((int)(top >> 23) - 126, -80) - kPTop;
+        if (wide) {
+#pragma unroll
+          for (int e = 0; e < KE; ++e) {
+            if (!(fabsf(vf[e]) < INFINITY)) vf[e] = __uint_as_float(0x7fc00000u);
+            lv[e] = __log2f(fmaxf(fabsf(vf[e]), kTinyScale)) - kPTop;
+          }
         }
       }
       float corr[RL];
-      float p[RL][4];
+      uint32_t pa[RL][2 * KH];  // P rounded for the tensor core; l sums it unrounded
 #pragma unroll
       for (int r = 0; r < RL; ++r) {
+        float mt = -INFINITY;
+        if (!B16 && wide) {
 #pragma unroll
-        for (int e = 0; e < 4; ++e) sx[r][e] = see[r][e] ? sx[r][e] * kf[e] * fac[r] : -INFINITY;
-        float mt = fmaxf(fmaxf(sx[r][0] + lv[0], sx[r][1] + lv[1]), fmaxf(sx[r][2] + lv[2], sx[r][3] + lv[3]));
+          for (int e = 0; e < KE; ++e) mt = fmaxf(mt, sx[r][e] + lv[e]);
+        } else {
+#pragma unroll
+          for (int e = 0; e < KE; e += 2) mt = max3(mt, sx[r][e], sx[r][e + 1]);
+          mt += lift;
+        }
         mt = fmaxf(mt, __shfl_xor_sync(0xffffffffu, mt, 1));
         mt = fmaxf(mt, __shfl_xor_sync(0xffffffffu, mt, 2));
         const float mn = fmaxf(m[r], mt);
         const float mu = mn == -INFINITY ? 0.0f : mn;  // a row without a key so far
         corr[r] = ex2(m[r] - mu);
+        float p[KE], sum = 0.0f;
 #pragma unroll
-        for (int e = 0; e < 4; ++e) p[r][e] = ex2(sx[r][e] - mu);
-        l[r] = l[r] * corr[r] + ((p[r][0] + p[r][1]) + (p[r][2] + p[r][3]));
+        for (int e = 0; e < KE; ++e) p[e] = ex2(sx[r][e] - mu);
+#pragma unroll
+        for (int e = 0; e < KE; e += 2) sum += p[e] + p[e + 1];
+        l[r] = l[r] * corr[r] + sum;
         m[r] = mn;
-      }
-      // P rounded for the tensor core (bf16 as in the forward pass, or fp16); l sums it
-      // unrounded.  pa[2 r + h]: row r's keys of half h.
-      uint32_t pa[2 * RL];
 #pragma unroll
-      for (int r = 0; r < RL; ++r) {
-        if constexpr (B16) {
-          pa[2 * r] = pack_bf16(p[r][0], p[r][1]);
-          pa[2 * r + 1] = pack_bf16(p[r][2], p[r][3]);
-        } else {
-          float y[4];
-#pragma unroll
-          for (int e = 0; e < 4; ++e) y[e] = see[r][e] ? p[r][e] * vf[e] : 0.0f;
-          pa[2 * r] = pack_f16(y[0], y[1]);
-          pa[2 * r + 1] = pack_f16(y[2], y[3]);
-        }
+        for (int i = 0; i < 2 * KH; ++i)
+          pa[r][i] = B16 ? pack_bf16(p[2 * i], p[2 * i + 1])
+                         : pack_f16(p[2 * i] * vf[2 * i], p[2 * i + 1] * vf[2 * i + 1]);
       }
       if (__any_sync(0xffffffffu, corr[0] != 1.0f || corr[RL - 1] != 1.0f)) {
         // the factor of accumulator e: NR = 8 has rows 2 t4, 2 t4 + 1 as columns (their
@@ -375,49 +402,53 @@ tree_split(const __grid_constant__ TreeArgs a) {
           for (int e = 0; e < 4; ++e) acc[i][e] *= f[e];
       }
       if constexpr (B16) {
-        const uint32_t va = st + (kTreeTile + (NR == 8 ? (lane & 7) + ((lane >> 4) << 3) : (lane & 15))) * L::ROW +
+        const uint32_t va = st + (KT + (NR == 8 ? (lane & 7) + ((lane >> 4) << 3) : (lane & 15))) * L::ROW +
                             (NR == 8 ? (lane >> 3) & 1 : lane >> 4) * 16;
 #pragma unroll
         for (int i = 0; i < D / 16; ++i) {
           uint32_t r0, r1, r2, r3;
           ldsm_x4_t(va + 32 * i, r0, r1, r2, r3);
           if constexpr (NR == 8) {
-            mma_bf16(acc[i], r0, r1, r2, r3, pa[0], pa[1]);
+            mma_bf16(acc[i], r0, r1, r2, r3, pa[0][0], pa[0][1]);
           } else {
-            mma_bf16(acc[2 * i], pa[0], pa[2], pa[1], pa[3], r0, r1);
-            mma_bf16(acc[2 * i + 1], pa[0], pa[2], pa[1], pa[3], r2, r3);
+            mma_bf16(acc[2 * i], pa[0][0], pa[RL - 1][0], pa[0][1], pa[RL - 1][1], r0, r1);
+            mma_bf16(acc[2 * i + 1], pa[0][0], pa[RL - 1][0], pa[0][1], pa[RL - 1][1], r2, r3);
           }
         }
       } else {
         // keys 2 t4, 2 t4 + 1 and those + 8 of columns DB g .. DB g + DB - 1: byte i of a key
         // pair is what the MMA takes for column DB g + i of O, as column g of block i
         // (NR = 16) or as row g (+ 8) of block i / 2
-        uint32_t vw[4][DB / 4];
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          if constexpr (D == 128) {
-            const uint4 x = lds128(st + kTreeTile * D + v_piece<D>(kk[e], g));
-            vw[e][0] = x.x, vw[e][1] = x.y, vw[e][2] = x.z, vw[e][3] = x.w;
-          } else {
-            const uint2 x = lds64(st + kTreeTile * D + v_piece<D>(kk[e], g >> 1) + 8 * (g & 1));
-            vw[e][0] = x.x, vw[e][1] = x.y;
-          }
-        }
+        for (int h = 0; h < KH; ++h) {
+          uint32_t vw[4][DB / 4];
 #pragma unroll
-        for (int i = 0; i < DB / 4; ++i) {
-#pragma unroll
-          for (int hh = 0; hh < 2; ++hh) {
-            const uint32_t sel = hh ? 0x7362u : 0x5140u;
-            const uint32_t x = __byte_perm(vw[0][i], vw[1][i], sel), y = __byte_perm(vw[2][i], vw[3][i], sel);
-            uint32_t x0, x1, y0, y1;
-            codes_f16x2<FMT>(x, x0, x1);
-            codes_f16x2<FMT>(y, y0, y1);
-            if constexpr (NR == 8) {
-              mma_f16(acc[2 * i + hh], x0, x1, y0, y1, pa[0], pa[1]);
+          for (int e = 0; e < 4; ++e) {
+            const int key = 16 * h + 8 * (e >> 1) + 2 * t4 + (e & 1);
+            if constexpr (D == 128) {
+              const uint4 x = lds128(st + KT * D + v_piece<D>(key, g));
+              vw[e][0] = x.x, vw[e][1] = x.y, vw[e][2] = x.z, vw[e][3] = x.w;
             } else {
-              const int blk = 4 * i + 2 * hh;
-              mma_f16(acc[blk], pa[0], pa[2], pa[1], pa[3], x0, y0);
-              mma_f16(acc[blk + 1], pa[0], pa[2], pa[1], pa[3], x1, y1);
+              const uint2 x = lds64(st + KT * D + v_piece<D>(key, g >> 1) + 8 * (g & 1));
+              vw[e][0] = x.x, vw[e][1] = x.y;
+            }
+          }
+          const uint32_t p0 = pa[0][2 * h], p1 = pa[0][2 * h + 1], p2 = pa[RL - 1][2 * h], p3 = pa[RL - 1][2 * h + 1];
+#pragma unroll
+          for (int i = 0; i < DB / 4; ++i) {
+#pragma unroll
+            for (int hh = 0; hh < 2; ++hh) {
+              const uint32_t sel = hh ? 0x7362u : 0x5140u;
+              uint32_t x0, x1, y0, y1;
+              codes_f16x2<FMT>(__byte_perm(vw[0][i], vw[1][i], sel), x0, x1);
+              codes_f16x2<FMT>(__byte_perm(vw[2][i], vw[3][i], sel), y0, y1);
+              if constexpr (NR == 8) {
+                mma_f16(acc[2 * i + hh], x0, x1, y0, y1, p0, p1);
+              } else {
+                const int blk = 4 * i + 2 * hh;
+                mma_f16(acc[blk], p0, p2, p1, p3, x0, y0);
+                mma_f16(acc[blk + 1], p0, p2, p1, p3, x1, y1);
+              }
             }
           }
         }
