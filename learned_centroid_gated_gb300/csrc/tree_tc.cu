@@ -8,12 +8,15 @@
 //   warps 8-11  (loaders) list the keys that any row sees and bring their K and V rows, 64
 //               keys a tile: 64 consecutive keys by TMA, others row by row with 16-byte
 //               asynchronous copies.  bf16 rows go straight into the 128-byte-swizzled
-//               operand tiles; 8-bit codes into a staging ring, whence the warps turn them
-//               into fp16 operands (exact).  For each tile one of them, in turn, works out
-//               which key each drafted token sees, as one 64-bit word per token.
-//   warp 12     issues the products: S = Q K^T (128 x 64, both operands in shared memory)
-//               into one of four tensor-memory tiles, and O += P V with P read from tensor
-//               memory.  It takes whichever is ready, the next S or the next P V.
+//               operand tiles; 8-bit codes into a staging ring, whence the loaders turn them
+//               into fp16 operands (exact).
+//   warp 12     issues the products: S = Q K^T (both operands in shared memory) into tensor
+//               memory, and O += P V with P read from tensor memory.  It takes whichever is
+//               ready.  An MMA costs its issuer about 75 cycles however narrow it is, so
+//               where both row halves use a tile (256 rows, bf16) S is made for two tiles at
+//               once (N = 128): 1.46 -> %s ms for 64 tokens behind a million.
+//   warps 13-15 (readers) take the tiles in turn and work out which key each drafted token
+//               sees, as one 64-bit word per token, and bring the scales of 8-bit rows.
 //   warps 0-7   the softmax of a product, a thread per row, in two warpgroups.  With up to
 //               128 rows (NT = 1) they take the tiles in turn, each with a reference, a sum
 //               and an O of its own (two partial results per segment); with more (NT = 2)
@@ -47,50 +50,47 @@ constexpr int kRows = 128;      // rows of a product (the MMA's M)
 constexpr int kTile = 64;       // keys per tile
 constexpr int kSBuf = 4;        // tensor-memory tiles for S and P
 constexpr int kMeta = 8;        // entries of the tile-metadata ring
-constexpr int kThreads = 512;   // 16 warps; 13 work, the rest fill the last warpgroup
-constexpr int kMmaWarp = 12, kLoadWarp = 8;
+constexpr int kOrders = 16;     // entries of the ring of orders
+constexpr int kScan = 256;      // raw keys per listing step
+constexpr int kList = 1024;     // entries of the list ring
+constexpr int kThreads = 512;
+constexpr int kLoadWarp = 8, kMmaWarp = 12, kReadWarp = 13, kReaders = 3;
 
-enum TileKind { kEnd = 1, kTma = 2 };  // no tile: the segment's end; its rows come by TMA
-
-// What the consumers have to know of a tile.
+// What the softmax has to know of a tile, from a reader.
 template <bool B16>
 struct alignas(16) TileMeta;
 template <>
 struct alignas(16) TileMeta<true> {
   uint64_t see[FOCUS_MAX_DRAFT];  // [token of the row group]: its keys of the tile
-  int end;                        // no tile: the segment's end (for the softmax)
-  int what;                       // for the MMA warp: kEnd, kTma
+  int end;                        // no tile: the segment's end
 };
 template <>
 struct alignas(16) TileMeta<false> {
   uint64_t see[FOCUS_MAX_DRAFT];
-  int end, what;
-  int pad[1];
+  int end;
   int wide;                       // V scales differ by more than 2^4
   float lv, unit;                 // V scales are below 2^lv; 2^-lv
-  int pad2[2];
   float ks[kTile], vs[kTile];     // scales
   __half vn[kTile];               // vs 2^-lv (not of a wide tile)
 };
 
-// What a drafted token of the row group sees.
-struct alignas(16) Token {
-  uint64_t word;  // ancestors
-  uint32_t mask;  // groups
-  int near;       // first position inside its window
+// What the readers and the MMA warp have to know of a tile, from a loader: its place in the
+// list and its keys; whether it is none but the segment's end; whether it comes by TMA.
+struct Order {
+  int tail, n;
 };
+enum TileKind { kEnd = -1, kTmaTile = 1 << 16 };  // n: kEnd, or the keys, + kTmaTile
 
 template <int D, int FMT, int NT>
 struct Tc {
   static constexpr bool B16 = FMT == FOCUS_CACHE_BF16;
+  static constexpr bool PAIR = B16 && NT == 2;  // S of two tiles at once
   using Meta = TileMeta<B16>;
   static constexpr int BOXES = D / 64;
-  // operand tiles; staging tiles of codes; tiles whose copies are in flight
+  // operand tiles; staging tiles of codes; tiles whose copies (row by row) are in flight
   static constexpr int STAGES = B16 ? (D == 128 ? (NT == 1 ? 5 : 4) : 6) : 3;
   static constexpr int RAW = B16 ? 0 : (D == 128 && NT == 2 ? 3 : 4);
   static constexpr int LAG = B16 ? STAGES - 2 : RAW - 1;
-  static constexpr int SCAN = !B16 && D == 128 && NT == 2 ? 256 : 512;  // raw keys per listing step
-  static constexpr int LIST = 2 * SCAN;                                 // entries of the list ring
   static constexpr int SLOTS = B16 ? STAGES : RAW;                      // tiles that copies go to
   static constexpr int QBOX = kRows * 128, KBOX = kTile * 128;          // bytes of 64 columns
   static constexpr int QT = BOXES * QBOX, KV = BOXES * KBOX;
@@ -98,19 +98,30 @@ struct Tc {
   static constexpr int OFF_KV = NT * QT;
   static constexpr int OFF_RAW = OFF_KV + STAGES * 2 * KV;
   static constexpr int OFF_META = OFF_RAW + RAW * RAW_TILE;
-  static constexpr int OFF_TOK = OFF_META + kMeta * (int)sizeof(Meta);
-  static constexpr int OFF_LIST = OFF_TOK + FOCUS_MAX_DRAFT * (int)sizeof(Token);
-  static constexpr int OFF_DOWN = OFF_LIST + LIST * 8;
+  static constexpr int OFF_ORDER = OFF_META + kMeta * (int)sizeof(Meta);
+  static constexpr int OFF_LIST = OFF_ORDER + kOrders * (int)sizeof(Order);
+  static constexpr int OFF_DOWN = OFF_LIST + kList * 4;
   static constexpr int OFF_SETS = OFF_DOWN + (B16 ? 0 : 2 * NT * kRows * 4);
-  static constexpr int OFF_CNT = OFF_SETS + 4 * 32 * 8;
+  static constexpr int OFF_CNT = OFF_SETS + 3 * 32 * 8;
   static constexpr int OFF_BAR = OFF_CNT + 2 * 4 * 4;
-  static constexpr int BARS = 2 * STAGES + 3 * kSBuf + 8 + 2 * SLOTS + kMeta;
+  static constexpr int BARS = 2 * STAGES + 3 * kSBuf + 8 + 2 * SLOTS + kMeta + kOrders;
   static constexpr int BYTES = OFF_BAR + 8 * (BARS + 2) + 1024;
-  // A metadata entry is written anew kMeta tiles later, when its tile has long been through
-  // the products: a tile is issued once the one AHEAD before it is.
+  // K rows of a stage: box stride and, of a pair, its tiles one behind the other
+  static constexpr int KSTEP = PAIR ? 2 * KBOX : KBOX;
+  __host__ __device__ static constexpr int k_at(int stage) {
+    return OFF_KV + (PAIR ? (stage >> 1) * 4 * KV + (stage & 1) * KBOX : stage * 2 * KV);
+  }
+  __host__ __device__ static constexpr int v_at(int stage) {
+    return OFF_KV + (PAIR ? (stage >> 1) * 4 * KV + 2 * KV + (stage & 1) * KV : stage * 2 * KV + KV);
+  }
+  // An entry of the metadata ring is written anew kMeta tiles later, when its tile has long
+  // been through the products: a tile is issued once the one AHEAD before it is.  So the
+  // readers are never kMeta tiles behind either, which is what the list holds on to (with
+  // less than a tile left over and a listing step ahead), and the orders twice over.
   static constexpr int AHEAD = B16 ? STAGES : RAW + STAGES;
-  static_assert(AHEAD < kMeta, "a metadata entry outlives its tile");
-  static_assert(OFF_META % 16 == 0 && sizeof(Meta) % 16 == 0 && OFF_BAR % 8 == 0, "alignment");
+  static_assert(AHEAD < kMeta && kMeta * kTile + kTile + kScan <= kList && kOrders >= 2 * kMeta, "rings");
+  static_assert(!PAIR || STAGES % 2 == 0, "pairs of stages");
+  static_assert(OFF_META % 16 == 0 && sizeof(Meta) % 16 == 0 && OFF_CNT % 16 == 0 && OFF_BAR % 8 == 0, "alignment");
   static_assert(KV % 1024 == 0 && OFF_KV % 1024 == 0 && RAW_TILE % 128 == 0, "operand tiles start a swizzle period");
   static_assert(BYTES <= 232448, "shared memory of a CTA");
 };
@@ -150,10 +161,12 @@ tree_tc(const __grid_constant__ TreeArgs a, const __grid_constant__ CUtensorMap 
   const uint32_t b_epi = b_qfree + 8;
   const uint32_t b_drain = b_epi + 32, b_load = b_drain + 8;              // the loader warps' meetings
   const uint32_t b_tma = b_load + 8, b_raw = b_tma + 8 * L::SLOTS;        // + 8 * slot: TMA there / codes read
-  const uint32_t b_meta = b_raw + 8 * L::SLOTS;                           // + 8 * entry (bf16): metadata there
+  const uint32_t b_meta = b_raw + 8 * L::SLOTS, b_order = b_meta + 8 * kMeta;  // + 8 * entry: written
   volatile uint32_t* tmem_slot = reinterpret_cast<volatile uint32_t*>(sm + L::OFF_BAR + 8 * L::BARS);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(sm + L::OFF_BAR + 8 * (L::BARS + 1));
   Meta* meta = reinterpret_cast<Meta*>(sm + L::OFF_META);
+  Order* orders = reinterpret_cast<Order*>(sm + L::OFF_ORDER);
+  int* lidx = reinterpret_cast<int*>(sm + L::OFF_LIST);
   float* down = reinterpret_cast<float*>(sm + L::OFF_DOWN);  // [segment & 1][row]: 8-bit row units
   int* status = a.flags + blockIdx.x;
 
@@ -182,6 +195,7 @@ tree_tc(const __grid_constant__ TreeArgs a, const __grid_constant__ CUtensorMap 
       mbar_init(b_raw + 8 * i, 4);
     }
     for (int i = 0; i < kMeta; ++i) mbar_init(b_meta + 8 * i, 1);
+    for (int i = 0; i < kOrders; ++i) mbar_init(b_order + 8 * i, 1);
     *abort_flag = 0;
     *status = 0;
     fence_barrier_init();
@@ -202,15 +216,11 @@ tree_tc(const __grid_constant__ TreeArgs a, const __grid_constant__ CUtensorMap 
     // ------------------------------------------------------------------ loaders --
     fewer_registers();
     const int lt = tid - 32 * kLoadWarp, lw = lt >> 5;
-    int* lidx = reinterpret_cast<int*>(sm + L::OFF_LIST);
-    uint32_t* lmsk = reinterpret_cast<uint32_t*>(lidx + L::LIST);
     int* cnt = reinterpret_cast<int*>(sm + L::OFF_CNT);  // [parity][warp]
-    Token* tok = reinterpret_cast<Token*>(sm + L::OFF_TOK);
     int t = 0;     // tiles, end marks among them
     int seg = 0, scans = 0, meets = 0;
     // by slot: the tile in it comes by TMA; TMA copies so far (their parity; whether any)
     uint32_t by_tma = 0u, tma_odd = 0u, tma_any = 0u;
-    uint64_t* sets = reinterpret_cast<uint64_t*>(sm + L::OFF_SETS) + 32 * lw;  // [group]: keys of a tile
     bool ok = true;
     // The loader warps meet: a barrier with a bounded wait.
     auto meet = [&]() {
@@ -262,35 +272,29 @@ tree_tc(const __grid_constant__ TreeArgs a, const __grid_constant__ CUtensorMap 
       fence_proxy_async_smem();
       __syncwarp();
       if (lane == 0) mbar_arrive(b_q);
-      // ---- what the tokens see (each warp for itself; the first one also for the tiles)
+      // ---- what the tokens see, taken together
       uint32_t many = 0u, wlo = 0u, whi = 0u;
-      int nearest = INT_MAX, farthest = INT_MIN;
+      int nearest = INT_MAX;
       for (int i = lane; i < ntok; i += 32) {
-        Token k;
-        k.word = tree_word(a, b, tok0 + i);
-        k.mask = k.word ? __ldg(M + len + tok0 + i) : 0u;
-        k.near = k.word ? len + __popcll(k.word) - a.w : INT_MAX;
-        if (lw == 0) tok[i] = k;
-        many |= k.mask;
-        wlo |= (uint32_t)k.word;
-        whi |= (uint32_t)(k.word >> 32);
-        nearest = min(nearest, k.near);
-        if (k.word) farthest = max(farthest, k.near);
+        const uint64_t word = tree_word(a, b, tok0 + i);
+        if (word) {
+          many |= __ldg(M + len + tok0 + i);
+          wlo |= (uint32_t)word;
+          whi |= (uint32_t)(word >> 32);
+          nearest = min(nearest, len + __popcll(word) - a.w);
+        }
       }
       many = __reduce_or_sync(0xffffffffu, many);
       const uint64_t any_word = (uint64_t)__reduce_or_sync(0xffffffffu, whi) << 32 | __reduce_or_sync(0xffffffffu, wlo);
       nearest = __reduce_min_sync(0xffffffffu, nearest);
-      farthest = __reduce_max_sync(0xffffffffu, farthest);
 
       const int64_t kvrow = (int64_t)a.H_kv * D * ES;  // bytes per slot
       const int64_t base = ((int64_t)b * a.cap * a.H_kv + kvh) * D * ES;
       const char* kb = reinterpret_cast<const char*>(a.kc) + base;
       const char* vb = reinterpret_cast<const char*>(a.vc) + base;
-      const float* ksc = B16 ? nullptr : a.ks + ((int64_t)b * a.H_kv + kvh) * a.cap;
-      const float* vsc = B16 ? nullptr : a.vs + ((int64_t)b * a.H_kv + kvh) * a.cap;
 
       int jb = js, head = 0, tail = 0;
-      constexpr int MW = L::SCAN / 128;
+      constexpr int MW = kScan / 128;
       uint32_t mw[MW];
       auto load_masks = [&]() {
 #pragma unroll
@@ -320,8 +324,8 @@ tree_tc(const __grid_constant__ TreeArgs a, const __grid_constant__ CUtensorMap 
         const int4 c4 = *reinterpret_cast<const int4*>(c);
         int all = c4.x + c4.y + c4.z + c4.w;
         int at = head + (lw > 0 ? c4.x : 0) + (lw > 1 ? c4.y : 0) + (lw > 2 ? c4.z : 0);
-        if (jb + L::SCAN <= min(len, je) && 4 * all >= 3 * L::SCAN) {
-          all = L::SCAN;
+        if (jb + kScan <= min(len, je) && 4 * all >= 3 * kScan) {
+          all = kScan;
           at = head + 32 * MW * lw;
 #pragma unroll
           for (int i = 0; i < MW; ++i) bal[i] = ~0u;
@@ -329,27 +333,28 @@ tree_tc(const __grid_constant__ TreeArgs a, const __grid_constant__ CUtensorMap 
 #pragma unroll
         for (int i = 0; i < MW; ++i) {
           if (bal[i] >> lane & 1u) {
-            const int x = (at + __popc(bal[i] & lanemask_lt())) & (L::LIST - 1);
+            const int x = (at + __popc(bal[i] & lanemask_lt())) & (kList - 1);
             lidx[x] = jb + 32 * (MW * lw + i) + lane;
-            lmsk[x] = mw[i];
           }
           at += __popc(bal[i]);
         }
         head += all;
-        jb += L::SCAN;
+        jb += kScan;
         load_masks();
         meet();  // entries there
       };
       // Starts the copies of the next tile (n keys of the list).
       auto issue = [&](int n) {
-        Meta& me = meta[t & (kMeta - 1)];
         const int sl = t % L::SLOTS;
-        const int first = lidx[tail & (L::LIST - 1)], last = lidx[(tail + n - 1) & (L::LIST - 1)];
+        const int first = lidx[tail & (kList - 1)], last = lidx[(tail + n - 1) & (kList - 1)];
         const bool run = a.tma && n == kTile && last - first == kTile - 1;
-        const uint32_t st = smem_u32(sm + (B16 ? L::OFF_KV + sl * 2 * L::KV : L::OFF_RAW + sl * L::RAW_TILE));
-        constexpr int VOFF = B16 ? L::KV : kTile * D;
+        const uint32_t kst = smem_u32(sm + (B16 ? L::k_at(sl) : L::OFF_RAW + sl * L::RAW_TILE));
+        const uint32_t vst = smem_u32(sm + (B16 ? L::v_at(sl) : L::OFF_RAW + sl * L::RAW_TILE + kTile * D));
         by_tma = (by_tma & ~(1u << sl)) | (uint32_t)run << sl;
-        if (lt == 0) me.what = run ? kTma : 0;
+        if (lt == 0) {
+          orders[t & (kOrders - 1)] = Order{tail, n + (run ? kTmaTile : 0)};
+          mbar_arrive(b_order + 8 * (t & (kOrders - 1)));
+        }
         if (run) {
           if (lt == 0) {
             if (!B16 && t >= L::SLOTS && !wait(b_raw + 8 * sl, t / L::SLOTS - 1)) ok = false;
@@ -360,12 +365,12 @@ tree_tc(const __grid_constant__ TreeArgs a, const __grid_constant__ CUtensorMap 
               if constexpr (B16) {
 #pragma unroll
                 for (int bx = 0; bx < L::BOXES; ++bx) {
-                  tma_load_3d(st + bx * L::KBOX, &map_k, 64 * bx, kvh, z, bt);
-                  tma_load_3d(st + VOFF + bx * L::KBOX, &map_v, 64 * bx, kvh, z, bt);
+                  tma_load_3d(kst + bx * L::KSTEP, &map_k, 64 * bx, kvh, z, bt);
+                  tma_load_3d(vst + bx * L::KBOX, &map_v, 64 * bx, kvh, z, bt);
                 }
               } else {
-                tma_load_3d(st, &map_k, 0, kvh, z, bt);
-                tma_load_3d(st + VOFF, &map_v, 0, kvh, z, bt);
+                tma_load_3d(kst, &map_k, 0, kvh, z, bt);
+                tma_load_3d(vst, &map_v, 0, kvh, z, bt);
               }
             }
           }
@@ -380,80 +385,17 @@ tree_tc(const __grid_constant__ TreeArgs a, const __grid_constant__ CUtensorMap 
           const int ch = lt % CH;
 #pragma unroll 4
           for (int r = lt / CH; r < kTile; r += RPI) {
-            uint32_t dst = st;
-            if constexpr (B16) dst += (ch / 8) * L::KBOX + r * 128 + (((ch & 7) ^ (r & 7)) << 4);
-            else dst += r * D + 16 * ch;
+            const int in = B16 ? r * 128 + (((ch & 7) ^ (r & 7)) << 4) : r * D + 16 * ch;
+            const uint32_t kd = kst + in + (B16 ? (ch / 8) * L::KSTEP : 0), vd = vst + in + (B16 ? (ch / 8) * L::KBOX : 0);
             if (r < n) {
-              const int64_t off = (int64_t)lidx[(tail + r) & (L::LIST - 1)] * kvrow + 16 * ch;
-              cp_async16(dst, kb + off);
-              cp_async16(dst + VOFF, vb + off);
+              const int64_t off = (int64_t)lidx[(tail + r) & (kList - 1)] * kvrow + 16 * ch;
+              cp_async16(kd, kb + off);
+              cp_async16(vd, vb + off);
             } else {  // no key: finite values under zero weights
-              sts128(dst, 0u, 0u, 0u, 0u);
-              sts128(dst + VOFF, 0u, 0u, 0u, 0u);
+              sts128(kd, 0u, 0u, 0u, 0u);
+              sts128(vd, 0u, 0u, 0u, 0u);
             }
           }
-        }
-        // ---- scales of the 8-bit rows: a warp's lanes bring V's, another's K's
-        if constexpr (!B16) {
-          const int who = (lw - t) & 3;
-          if (who == 1 || who == 2) {
-#pragma unroll
-            for (int e = 0; e < 2; ++e) {
-              const int r = 32 * e + lane;
-              float* dst = (who == 1 ? me.vs : me.ks) + r;
-              if (r < n) cp_async4(smem_u32(dst), (who == 1 ? vsc : ksc) + lidx[(tail + r) & (L::LIST - 1)]);
-              else *dst = 0.0f;
-            }
-          }
-        }
-        // ---- who sees its keys: one warp, the others go on; a lane has two keys, then two tokens
-        if (((lw - t) & 3) == 0) {
-          int j[2];
-          uint32_t mk[2], valid[2];
-#pragma unroll
-          for (int e = 0; e < 2; ++e) {
-            const int r = 32 * e + lane, x = (tail + r) & (L::LIST - 1);
-            j[e] = r < n ? lidx[x] : 0;
-            mk[e] = r < n ? lmsk[x] : 0u;
-            valid[e] = n >= 32 * e + 32 ? ~0u : n > 32 * e ? (1u << (n - 32 * e)) - 1u : 0u;
-          }
-          if (last < min(nearest, len)) {
-            // before every window and the drafted tokens: for each group some token has, the
-            // tile's keys that have it; a token sees the union of its groups' keys
-            for (uint32_t g = many; g; g &= g - 1) {
-              const int at = __ffs(g) - 1;
-              const unsigned s0 = __ballot_sync(0xffffffffu, mk[0] >> at & 1u), s1 = __ballot_sync(0xffffffffu, mk[1] >> at & 1u);
-              if (lane == 0) sets[at] = (uint64_t)s1 << 32 | s0;
-            }
-            __syncwarp();
-            for (int i = lane; i < ntok; i += 32) {
-              uint64_t w = 0ull;
-              for (uint32_t g = tok[i].mask; g; g &= g - 1) w |= sets[__ffs(g) - 1];
-              me.see[i] = w;
-            }
-          } else if (first >= farthest && last < len) {  // inside every window
-            for (int i = lane; i < ntok; i += 32)
-              me.see[i] = tok[i].word ? (uint64_t)valid[1] << 32 | valid[0] : 0ull;
-          } else {
-            uint64_t bit[2];
-#pragma unroll
-            for (int e = 0; e < 2; ++e) {
-              bit[e] = valid[e] >> lane & 1u ? ~0ull : 0ull;
-              if (bit[e] && j[e] >= len) {  // a drafted key: its token's bit, its position
-                bit[e] = 1ull << (j[e] - len);
-                j[e] = len + __popcll(tree_word(a, b, j[e] - len)) - 1;
-              }
-            }
-            for (int i = 0; i < ntok; ++i) {
-              const Token y = tok[i];
-              const unsigned s0 = __ballot_sync(0xffffffffu, (y.word & bit[0]) != 0ull && (j[0] >= y.near || (mk[0] & y.mask) != 0u));
-              const unsigned s1 = __ballot_sync(0xffffffffu, (y.word & bit[1]) != 0ull && (j[1] >= y.near || (mk[1] & y.mask) != 0u));
-              if (lane == 0) me.see[i] = (uint64_t)s1 << 32 | s0;
-            }
-          }
-          if (lane == 0) me.end = 0;
-          __syncwarp();
-          if (B16 && lane == 0) mbar_arrive(b_meta + 8 * (t & (kMeta - 1)));
         }
         tail += n;
       };
@@ -467,7 +409,6 @@ tree_tc(const __grid_constant__ TreeArgs a, const __grid_constant__ CUtensorMap 
           if (x >= S && !(ok = wait_all(b_empty + 8 * (x % S), x / S - 1))) return;
           if (!end) {
             const uint32_t raw = smem_u32(sm + L::OFF_RAW + sl * L::RAW_TILE);
-            const uint32_t st = smem_u32(sm + L::OFF_KV + (x % S) * 2 * L::KV);
             constexpr int CH = D / 16, RPI = 128 / CH;
             // (16 columns are two 16-byte chunks of the operand tile's row; lanes of the second
             // box store theirs in the other order, so that eight lanes meet all banks)
@@ -477,46 +418,14 @@ tree_tc(const __grid_constant__ TreeArgs a, const __grid_constant__ CUtensorMap 
               const uint4 y0 = lds128(raw + r * D + 16 * ch), y1 = lds128(raw + kTile * D + r * D + 16 * ch);
 #pragma unroll
               for (int v = 0; v < 2; ++v) {
-                const uint32_t w[4] = {v ? y1.x : y0.x, v ? y1.y : y0.y, v ? y1.z : y0.z, v ? y1.w : y0.w};
+                const uint4 y = v ? y1 : y0;
+                const uint32_t w[4] = {second ? y.z : y.x, second ? y.w : y.y, second ? y.x : y.z, second ? y.y : y.w};
                 uint32_t h[8];
 #pragma unroll
                 for (int i = 0; i < 4; ++i) codes_f16x2<FMT>(w[i], h[2 * i], h[2 * i + 1]);
-                const uint32_t dst = st + v * L::KV + (ch / 4) * L::KBOX + r * 128;
-                uint32_t u[4], y[4];
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                  u[i] = second ? h[4 + i] : h[i];
-                  y[i] = second ? h[i] : h[4 + i];
-                }
-                sts128(dst + (((c + second) ^ (r & 7)) << 4), u[0], u[1], u[2], u[3]);
-                sts128(dst + (((c + 1 - second) ^ (r & 7)) << 4), y[0], y[1], y[2], y[3]);
-              }
-            }
-            if (((lw - x) & 3) == 1) {  // V scales, by the warp that brought them (an infinite one reads as NaN)
-              Meta& me = meta[x & (kMeta - 1)];
-              float y[2] = {me.vs[lane], me.vs[32 + lane]};
-              uint32_t top = 0u, low = 0x7f800000u;
-#pragma unroll
-              for (int e = 0; e < 2; ++e) {
-                const uint32_t u = __float_as_uint(fabsf(y[e]));
-                if (u >= 0x7f800000u) {
-                  y[e] = __uint_as_float(0x7fc00000u);
-                  me.vs[32 * e + lane] = y[e];
-                } else {
-                  top = max(top, u);
-                  if (u) low = min(low, u);
-                }
-              }
-              top = __reduce_max_sync(0xffffffffu, top);
-              low = __reduce_min_sync(0xffffffffu, low);
-              const int ex = max((int)(top >> 23) - 126, -80);  // scales are below 2^ex
-              const float unit = __uint_as_float((uint32_t)(127 - min(ex, 126)) << 23);
-#pragma unroll
-              for (int e = 0; e < 2; ++e) me.vn[32 * e + lane] = __float2half_rn(y[e] * unit);
-              if (lane == 0) {
-                me.wide = ex > 126 || __uint_as_float(top) > 16.0f * __uint_as_float(low);
-                me.lv = (float)ex;
-                me.unit = unit;
+                const uint32_t dst = smem_u32(sm + (v ? L::v_at(x % S) : L::k_at(x % S))) + (ch / 4) * L::KBOX + r * 128;
+                sts128(dst + (((c + second) ^ (r & 7)) << 4), h[0], h[1], h[2], h[3]);
+                sts128(dst + (((c + 1 - second) ^ (r & 7)) << 4), h[4], h[5], h[6], h[7]);
               }
             }
           }
@@ -529,7 +438,6 @@ tree_tc(const __grid_constant__ TreeArgs a, const __grid_constant__ CUtensorMap 
         }
       };
       load_masks();
-      meet();  // tok is there
       int landed = t;  // tiles handed over so far
       while (ok) {
         while (ok && head - tail < kTile && jb < je) scan();
@@ -553,16 +461,14 @@ tree_tc(const __grid_constant__ TreeArgs a, const __grid_constant__ CUtensorMap 
         if constexpr (B16) {
           if (t >= S && !(ok = wait_all(b_empty + 8 * (t % S), t / S - 1))) break;
         }
-        Meta& me = meta[t & (kMeta - 1)];
-        if (lt == 0) me.what = kEnd;
-        if (((lw - t) & 3) == 0 && lane == 0) {
-          me.end = 1;
-          if (B16) mbar_arrive(b_meta + 8 * (t & (kMeta - 1)));
+        if (lt == 0) {
+          orders[t & (kOrders - 1)] = Order{0, kEnd};
+          mbar_arrive(b_order + 8 * (t & (kOrders - 1)));
         }
         finish(t++, true);
       }
       ++seg;
-      if (ok) meet();  // the list and the tokens start anew
+      if (ok) meet();  // the list starts anew
     });
     cp_async_wait<0>();
     if (lt == 0 && *abort_flag)  // giving up: copies in flight land before the CTA exits
@@ -570,62 +476,38 @@ tree_tc(const __grid_constant__ TreeArgs a, const __grid_constant__ CUtensorMap 
         if (tma_any >> i & 1u) mbar_drain(b_tma + 8 * i, (tma_odd >> i & 1u) ^ 1u);
     __syncwarp();
   } else if (warp >= kMmaWarp) {
-    // ---------------------------------------------------------------- MMA issue --
     fewer_registers();
     if (warp == kMmaWarp) {
-      constexpr uint32_t IS = B16 ? idesc_bf16(kRows, kTile, 0) : idesc_f16(kRows, kTile, 0);
+      // ---------------------------------------------------------------- MMA issue --
+      constexpr uint32_t IS = B16 ? idesc_bf16(kRows, L::PAIR ? 2 * kTile : kTile, 0) : idesc_f16(kRows, kTile, 0);
       constexpr uint32_t IPV = B16 ? idesc_bf16(kRows, D, 1) : idesc_f16(kRows, D, 1);
       int t = 0, c = 0, seg = 0;  // tiles with end marks, products, segments
       uint32_t tma_par = 0u;      // by stage: parity of its next TMA copy (bf16)
+      uint32_t p_par = 0u;        // pairs: by P tile, parity of its next P
       bool ok = true;
+      auto s_product = [&](uint32_t dst, int rt, int stage) {
+        const uint64_t da = sw128_desc(smem_u32(sm + rt * L::QT), 16, 1024);
+        const uint64_t db = sw128_desc(smem_u32(sm + L::k_at(stage)), 16, 1024);
+#pragma unroll
+        for (int kk = 0; kk < D / 16; ++kk)
+          umma_ss(dst, da + (((kk / 4) * L::QBOX + (kk % 4) * 32) >> 4), db + (((kk / 4) * L::KSTEP + (kk % 4) * 32) >> 4), IS,
+                  kk > 0);
+      };
+      auto pv_product = [&](int wg, int buf, int stage, bool add) {
+        const uint64_t dv = sw128_desc(smem_u32(sm + L::v_at(stage)), L::KBOX, 1024);
+#pragma unroll
+        for (int kk = 0; kk < kTile / 16; ++kk)
+          umma_ts(tmem + kSBuf * kTile + wg * 128, tmem + buf * kTile + 8 * kk, dv + ((kk * 2048) >> 4), IPV,
+                  add || kk > 0 ? 1u : 0u);
+      };
       for_segments(a, blockIdx.x, lane, [&](int64_t, int, int, int, int, int, int) {
         if (lane == 0 && ok) {
           ok = wait(b_q, seg);
           tc_fence_after();
-          int ts = t, cs = c, cp = c;
           bool ended = false, fresh[2] = {true, true};
-          int have = -1;  // the tile whose metadata and rows are there
           long long t0 = clock64();
-          while (ok && !(ended && cp == cs)) {
-            bool some = false;
-            const bool begun = NT == 2 && ((cs - c) & 1);  // this tile's second product
-            if (!ended && cs < cp + kSBuf && have != ts && mbar_test_wait(b_full + 8 * (ts % S), (ts / S) & 1)) {
-              const int what = meta[ts & (kMeta - 1)].what;
-              if (!B16 || what != kTma) {
-                have = ts;
-              } else if (mbar_test_wait(b_tma + 8 * (ts % S), tma_par >> (ts % S) & 1u)) {
-                tma_par ^= 1u << (ts % S);
-                have = ts;
-              }
-              if (what == kEnd) ended = some = true;
-            }
-            if (!ended && cs < cp + kSBuf && have == ts) {
-              some = true;
-              tc_fence_after();
-              const uint64_t da = sw128_desc(smem_u32(sm + (begun ? L::QT : 0)), 16, 1024);
-              const uint64_t db = sw128_desc(smem_u32(sm + L::OFF_KV + (ts % S) * 2 * L::KV), 16, 1024);
-#pragma unroll
-              for (int kk = 0; kk < D / 16; ++kk)
-                umma_ss(tmem + (cs % kSBuf) * kTile, da + (((kk / 4) * L::QBOX + (kk % 4) * 32) >> 4),
-                        db + (((kk / 4) * L::KBOX + (kk % 4) * 32) >> 4), IS, kk > 0);
-              umma_commit(b_s + 8 * (cs % kSBuf));
-              ++cs;
-              if (NT == 1 || begun) ++ts;
-            }
-            if (cp < cs && mbar_test_wait(b_p + 8 * (cp % kSBuf), (cp / kSBuf) & 1)) {
-              some = true;
-              tc_fence_after();
-              const int wg = cp & 1, st = (t + (cp - c) / NT) % S;
-              const uint64_t dv = sw128_desc(smem_u32(sm + L::OFF_KV + st * 2 * L::KV + L::KV), L::KBOX, 1024);
-#pragma unroll
-              for (int kk = 0; kk < kTile / 16; ++kk)
-                umma_ts(tmem + kSBuf * kTile + wg * 128, tmem + (cp % kSBuf) * kTile + 8 * kk, dv + ((kk * 2048) >> 4),
-                        IPV, !fresh[wg] || kk > 0 ? 1u : 0u);
-              fresh[wg] = false;
-              umma_commit(b_pv + 8 * (cp % kSBuf));
-              if (NT == 1 || ((cp - c) & 1)) umma_commit(b_empty + 8 * st);
-              ++cp;
-            }
+          bool some = false;
+          auto idle = [&]() {  // bounds the wait of a round without work
             if (some) {
               t0 = clock64();
             } else if (*abort_flag) {
@@ -635,6 +517,87 @@ tree_tc(const __grid_constant__ TreeArgs a, const __grid_constant__ CUtensorMap 
               raise_status(status, FOCUS_ERR_TIMEOUT);
               ok = false;
             }
+            some = false;
+          };
+          // Tile x is there (or the end mark in its place).
+          auto arrived = [&](int x) {
+            if (!mbar_test_wait(b_full + 8 * (x % S), (x / S) & 1)) return false;
+            const int n = orders[x & (kOrders - 1)].n;
+            if (n == kEnd) {
+              ended = true;
+            } else if (B16 && n >= kTmaTile) {
+              if (!mbar_test_wait(b_tma + 8 * (x % S), tma_par >> (x % S) & 1u)) return false;
+              tma_par ^= 1u << (x % S);
+            }
+            return true;
+          };
+          int ts = t;  // tiles looked at; at the end, the first end mark
+          if constexpr (L::PAIR) {
+            // Row halves rt: S of tiles [nx, sd) is made, P V up to nx done.  A pair of stages
+            // is made at once when both tiles (or the end) are there and the last pair's P V
+            // are issued; the half that a segment's odd start or end leaves out is not read.
+            int nx[2] = {t, t}, sd[2] = {t, t};
+            while (ok && !(ended && nx[0] == ts && nx[1] == ts)) {
+              if (!ended && ts < min(nx[0], nx[1]) + S && arrived(ts)) {
+                some = true;
+                if (!ended) ++ts;
+              }
+#pragma unroll
+              for (int rt = 0; rt < 2; ++rt) {
+                if (nx[rt] == sd[rt] && sd[rt] < ts) {
+                  const int up = (sd[rt] | 1) + 1;
+                  if (ended || ts >= up) {
+                    some = true;
+                    tc_fence_after();
+                    s_product(tmem + rt * 2 * kTile, rt, (sd[rt] & ~1) % S);
+                    umma_commit(b_s + 8 * rt);
+                    sd[rt] = min(up, ts);
+                  }
+                }
+                const int buf = 2 * rt + (nx[rt] & 1);
+                if (nx[rt] < sd[rt] && mbar_test_wait(b_p + 8 * buf, p_par >> buf & 1u)) {
+                  some = true;
+                  p_par ^= 1u << buf;
+                  tc_fence_after();
+                  pv_product(rt, buf, nx[rt] % S, !fresh[rt]);
+                  fresh[rt] = false;
+                  umma_commit(b_pv + 8 * buf);
+                  if (nx[1 - rt] > nx[rt]) umma_commit(b_empty + 8 * (nx[rt] % S));
+                  ++nx[rt];
+                }
+              }
+              idle();
+            }
+          } else {
+            int cs = c, cp = c;
+            int have = -1;  // the tile whose rows are there
+            while (ok && !(ended && cp == cs)) {
+              const bool begun = NT == 2 && ((cs - c) & 1);  // this tile's second product
+              if (!ended && cs < cp + kSBuf && have != ts && arrived(ts)) {
+                some = true;
+                have = ts;
+              }
+              if (!ended && cs < cp + kSBuf && have == ts) {
+                some = true;
+                tc_fence_after();
+                s_product(tmem + (cs % kSBuf) * kTile, begun, ts % S);
+                umma_commit(b_s + 8 * (cs % kSBuf));
+                ++cs;
+                if (NT == 1 || begun) ++ts;
+              }
+              if (cp < cs && mbar_test_wait(b_p + 8 * (cp % kSBuf), (cp / kSBuf) & 1)) {
+                some = true;
+                tc_fence_after();
+                const int wg = cp & 1, st = (t + (cp - c) / NT) % S;
+                pv_product(wg, cp % kSBuf, st, !fresh[wg]);
+                fresh[wg] = false;
+                umma_commit(b_pv + 8 * (cp % kSBuf));
+                if (NT == 1 || ((cp - c) & 1)) umma_commit(b_empty + 8 * st);
+                ++cp;
+              }
+              idle();
+            }
+            c = cs;
           }
           umma_commit(b_qfree);
           // The end marks' stages go back once both warpgroups have read them (and O): the
@@ -642,7 +605,6 @@ tree_tc(const __grid_constant__ TreeArgs a, const __grid_constant__ CUtensorMap 
           if (ok && (ok = wait(b_full + 8 * ((ts + MARKS - 1) % S), (ts + MARKS - 1) / S) && o_read(seg))) {
             for (int e = 0; e < MARKS; ++e) mbar_arrive(b_empty + 8 * ((ts + e) % S));
             t = ts + MARKS;
-            c = cs;
           }
           ++seg;
         }
@@ -653,6 +615,133 @@ tree_tc(const __grid_constant__ TreeArgs a, const __grid_constant__ CUtensorMap 
         mbar_drain(b_drain, 0);
       }
       __syncwarp();
+    } else {
+      // ------------------------------------------------------------------ readers --
+      const int me_no = warp - kReadWarp;
+      uint64_t* sets = reinterpret_cast<uint64_t*>(sm + L::OFF_SETS) + 32 * me_no;  // [group]: keys of a tile
+      int t = 0;  // tiles, end marks among them
+      bool ok = true;
+      for_segments(a, blockIdx.x, lane, [&](int64_t, int kvh, int rg, int b, int len, int, int) {
+        if (!ok) return;
+        const int rho = kvh / (a.H_kv / a.R);
+        const uint32_t* M = a.mask + ((int64_t)b * a.R + rho) * a.cap;
+        const int row0 = rg * NT * kRows, rows = min(NT * kRows, a.rows - row0);
+        const int tok0 = row0 / a.gq, ntok = (row0 + rows - 1) / a.gq - tok0 + 1;
+        // this lane's two tokens: ancestors, groups, first position inside the window
+        uint64_t word[2];
+        uint32_t grp[2];
+        int near[2];
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          const int i = 32 * e + lane;
+          word[e] = i < ntok ? tree_word(a, b, tok0 + i) : 0ull;
+          grp[e] = word[e] ? __ldg(M + len + tok0 + i) : 0u;
+          near[e] = word[e] ? len + __popcll(word[e]) - a.w : INT_MAX;
+        }
+        const uint32_t many = __reduce_or_sync(0xffffffffu, grp[0] | grp[1]);
+        const int nearest = __reduce_min_sync(0xffffffffu, min(near[0], near[1]));
+        const int farthest =
+            __reduce_max_sync(0xffffffffu, max(word[0] ? near[0] : INT_MIN, word[1] ? near[1] : INT_MIN));
+        const float* ksc = B16 ? nullptr : a.ks + ((int64_t)b * a.H_kv + kvh) * a.cap;
+        const float* vsc = B16 ? nullptr : a.vs + ((int64_t)b * a.H_kv + kvh) * a.cap;
+        for (int marks = 0; marks < MARKS; ++t) {
+          if (!(ok = wait_all(b_order + 8 * (t & (kOrders - 1)), t / kOrders))) return;
+          const Order o = orders[t & (kOrders - 1)];
+          const bool mine = t % kReaders == me_no;
+          Meta& me = meta[t & (kMeta - 1)];
+          if (o.n == kEnd) {
+            ++marks;
+            if (mine && lane == 0) me.end = 1;
+          } else if (mine) {
+            const int n = o.n & (kTmaTile - 1);
+            const int first = lidx[o.tail & (kList - 1)], last = lidx[(o.tail + n - 1) & (kList - 1)];
+            int j[2];
+            uint32_t mk[2], valid[2];
+            float ks[2], vs[2];
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+              const int r = 32 * e + lane;
+              j[e] = r < n ? lidx[(o.tail + r) & (kList - 1)] : 0;
+              mk[e] = r < n ? __ldg(M + j[e]) : 0u;
+              valid[e] = n >= 32 * e + 32 ? ~0u : n > 32 * e ? (1u << (n - 32 * e)) - 1u : 0u;
+              if constexpr (!B16) {
+                ks[e] = r < n ? __ldg(ksc + j[e]) : 0.0f;
+                vs[e] = r < n ? __ldg(vsc + j[e]) : 0.0f;
+              }
+            }
+            if (last < min(nearest, len)) {
+              // before every window and the drafted tokens: for each group some token has, the
+              // tile's keys that have it; a token sees the union of its groups' keys
+              for (uint32_t g = many; g; g &= g - 1) {
+                const int at = __ffs(g) - 1;
+                const unsigned s0 = __ballot_sync(0xffffffffu, mk[0] >> at & 1u), s1 = __ballot_sync(0xffffffffu, mk[1] >> at & 1u);
+                if (lane == 0) sets[at] = (uint64_t)s1 << 32 | s0;
+              }
+              __syncwarp();
+#pragma unroll
+              for (int e = 0; e < 2; ++e) {
+                uint64_t w = 0ull;
+                for (uint32_t g = grp[e]; g; g &= g - 1) w |= sets[__ffs(g) - 1];
+                if (32 * e + lane < ntok) me.see[32 * e + lane] = w;
+              }
+              __syncwarp();
+            } else if (first >= farthest && last < len) {  // inside every window
+#pragma unroll
+              for (int e = 0; e < 2; ++e)
+                if (32 * e + lane < ntok) me.see[32 * e + lane] = word[e] ? (uint64_t)valid[1] << 32 | valid[0] : 0ull;
+            } else {
+              uint64_t bit[2];
+#pragma unroll
+              for (int e = 0; e < 2; ++e) {
+                bit[e] = valid[e] >> lane & 1u ? ~0ull : 0ull;
+                if (bit[e] && j[e] >= len) {  // a drafted key: its token's bit, its position
+                  bit[e] = 1ull << (j[e] - len);
+                  j[e] = len + __popcll(tree_word(a, b, j[e] - len)) - 1;
+                }
+              }
+              for (int i = 0; i < ntok; ++i) {
+                const uint64_t w = __shfl_sync(0xffffffffu, i < 32 ? word[0] : word[1], i & 31);
+                const uint32_t g = __shfl_sync(0xffffffffu, i < 32 ? grp[0] : grp[1], i & 31);
+                const int from = __shfl_sync(0xffffffffu, i < 32 ? near[0] : near[1], i & 31);
+                const unsigned s0 = __ballot_sync(0xffffffffu, (w & bit[0]) != 0ull && (j[0] >= from || (mk[0] & g) != 0u));
+                const unsigned s1 = __ballot_sync(0xffffffffu, (w & bit[1]) != 0ull && (j[1] >= from || (mk[1] & g) != 0u));
+                if (lane == 0) me.see[i] = (uint64_t)s1 << 32 | s0;
+              }
+            }
+            if constexpr (!B16) {  // scales (an infinite one of V reads as NaN)
+              uint32_t top = 0u, low = 0x7f800000u;
+#pragma unroll
+              for (int e = 0; e < 2; ++e) {
+                const uint32_t u = __float_as_uint(fabsf(vs[e]));
+                if (u >= 0x7f800000u) {
+                  vs[e] = __uint_as_float(0x7fc00000u);
+                } else {
+                  top = max(top, u);
+                  if (u) low = min(low, u);
+                }
+              }
+              top = __reduce_max_sync(0xffffffffu, top);
+              low = __reduce_min_sync(0xffffffffu, low);
+              const int ex = max((int)(top >> 23) - 126, -80);  // scales are below 2^ex
+              const float unit = __uint_as_float((uint32_t)(127 - min(ex, 126)) << 23);
+#pragma unroll
+              for (int e = 0; e < 2; ++e) {
+                me.ks[32 * e + lane] = ks[e];
+                me.vs[32 * e + lane] = vs[e];
+                me.vn[32 * e + lane] = __float2half_rn(vs[e] * unit);
+              }
+              if (lane == 0) {
+                me.wide = ex > 126 || __uint_as_float(top) > 16.0f * __uint_as_float(low);
+                me.lv = (float)ex;
+                me.unit = unit;
+              }
+            }
+            if (lane == 0) me.end = 0;
+          }
+          __syncwarp();
+          if (mine && lane == 0) mbar_arrive(b_meta + 8 * (t & (kMeta - 1)));
+        }
+      });
     }
   } else {
     // ------------------------------------------------------------------ softmax --
@@ -665,6 +754,8 @@ tree_tc(const __grid_constant__ TreeArgs a, const __grid_constant__ CUtensorMap 
     constexpr float kSumCap = B16 ? 1.8446744e19f : 32768.0f;
     constexpr float kTop = B16 ? 0.0f : 7.0f;  // log2 of the largest weight when m is set
     int t = NT == 1 ? wg : 0, c = wg, seg = 0;
+    // pairs: parities of the next S of this warpgroup, and of the P V of its two P tiles
+    uint32_t s_par = 0u, pv_par = 0u;
     bool ok = true;
     for_segments(a, blockIdx.x, lane, [&](int64_t partial, int, int rg, int b, int, int, int) {
       if (!ok) return;
@@ -675,15 +766,32 @@ tree_tc(const __grid_constant__ TreeArgs a, const __grid_constant__ CUtensorMap 
       // a row that is no token sees nothing: its reference need not be looked for
       float m = alive ? -INFINITY : 0.0f, l = 0.0f, fac = a.sl2;
       const int c0 = c;
+      // This warpgroup's last product P V (that of tile t - 1, or c - 2) is done.
+      auto pv_done = [&]() {
+        if constexpr (L::PAIR) {
+          const int at = (t - 1) & 1;  // (its bit was turned when its P was handed over)
+          return wait_all(b_pv + 8 * (2 * wg + at), (pv_par >> at & 1u) ^ 1u);
+        } else {
+          return wait_all(b_pv + 8 * ((c - 2) % kSBuf), (c - 2) / kSBuf);
+        }
+      };
       for (;; t += NT == 1 ? 2 : 1, c += 2) {
         const Meta& me = meta[t & (kMeta - 1)];
-        if (!(ok = B16 ? wait_all(b_meta + 8 * (t & (kMeta - 1)), t / kMeta) : wait_all(b_full + 8 * (t % S), t / S))) return;
+        if (!(ok = wait_all(b_meta + 8 * (t & (kMeta - 1)), t / kMeta))) return;
         if (me.end) break;
         if (!B16 && c == c0) fac = a.sl2 * down[((seg & 1) * NT + (NT == 2 ? wg : 0)) * kRows + r];
         const uint64_t see = alive ? me.see[ti] : 0ull;
-        if (!(ok = wait_all(b_s + 8 * (c % kSBuf), c / kSBuf))) return;
+        const int buf = L::PAIR ? 2 * wg + (t & 1) : c % kSBuf;
+        if constexpr (L::PAIR) {
+          if (c == c0 || !(t & 1)) {  // a new pair's S
+            if (!(ok = wait_all(b_s + 8 * wg, s_par))) return;
+            s_par ^= 1u;
+          }
+        } else {
+          if (!(ok = wait_all(b_s + 8 * buf, c / kSBuf))) return;
+        }
         tc_fence_after();
-        const uint32_t tS = tmem + lane_off + (c % kSBuf) * kTile;
+        const uint32_t tS = tmem + lane_off + buf * kTile;
         uint32_t x0[32], x1[32];
         tmem_ld32(tS, x0);
         tmem_ld32(tS + 32, x1);
@@ -812,7 +920,7 @@ tree_tc(const __grid_constant__ TreeArgs a, const __grid_constant__ CUtensorMap 
         }
         if (__any_sync(0xffffffffu, f != 1.0f) && c > c0) {
           // O of this warpgroup's earlier products follows the reference
-          if (!(ok = wait_all(b_pv + 8 * ((c - 2) % kSBuf), (c - 2) / kSBuf))) return;
+          if (!(ok = pv_done())) return;
           tc_fence_after();
 #pragma unroll
           for (int k = 0; k < D / 32; ++k) {
@@ -827,15 +935,16 @@ tree_tc(const __grid_constant__ TreeArgs a, const __grid_constant__ CUtensorMap 
         tmem_st_wait();
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive(b_p + 8 * (c % kSBuf));
+        if (lane == 0) mbar_arrive(b_p + 8 * buf);
+        if (L::PAIR) pv_par ^= 1u << (t & 1);
       }
-      t += MARKS;
       // ---- this segment's partial
       const bool some = c > c0;
       if (some) {
-        if (!(ok = wait_all(b_pv + 8 * ((c - 2) % kSBuf), (c - 2) / kSBuf))) return;
+        if (!(ok = pv_done())) return;
         tc_fence_after();
       }
+      t += MARKS;  // the end mark
       // NT = 1: two partials of 128 rows; NT = 2: one of 256
       const int64_t slot = (partial * 2 + wg) * kRows + r;
       if (on) a.part_ml[slot] = make_float2(m, some ? l : 0.0f);
