@@ -504,7 +504,8 @@ tree_tc(const __grid_constant__ TreeArgs a, const __grid_constant__ CUtensorMap 
         if (lane == 0 && ok) {
           ok = wait(b_q, seg);
           tc_fence_after();
-          bool ended = false, fresh[2] = {true, true};
+          bool ended = false;
+          uint32_t fresh = 0u;  // by warpgroup: O has a product of this segment
           long long t0 = clock64();
           bool some = false;
           auto idle = [&]() {  // bounds the wait of a round without work
@@ -533,40 +534,63 @@ tree_tc(const __grid_constant__ TreeArgs a, const __grid_constant__ CUtensorMap 
           };
           int ts = t;  // tiles looked at; at the end, the first end mark
           if constexpr (L::PAIR) {
-            // Row halves rt: S of tiles [nx, sd) is made, P V up to nx done.  A pair of stages
-            // is made at once when both tiles (or the end) are there and the last pair's P V
-            // are issued; the half that a segment's odd start or end leaves out is not read.
-            int nx[2] = {t, t}, sd[2] = {t, t};
-            while (ok && !(ended && nx[0] == ts && nx[1] == ts)) {
-              if (!ended && ts < min(nx[0], nx[1]) + S && arrived(ts)) {
-                some = true;
-                if (!ended) ++ts;
+            // The S of a unit, the tiles of a pair of stages, is made at once for a row half rt
+            // when both tiles (or the end) are there and the half's last P V are issued; what
+            // a segment's odd start or end leaves out of it is not read.  The two halves
+            // alternate: while one's softmax works the tensor core has the other's products.
+            bool ready = false;  // the next unit's tiles are there
+            int nb = t;          // its first tile
+            auto look = [&](bool block) {
+              const int up = (nb | 1) + 1;
+              while (ok && !ended && ts < up) {
+                if (arrived(ts)) {
+                  some = true;
+                  if (!ended) ++ts;
+                } else if (!block) {
+                  return;
+                }
+                idle();
               }
+              ready = ok && nb < ts;
+            };
+            auto make_s = [&](int rt) {
+              tc_fence_after();
+              s_product(tmem + rt * 2 * kTile, rt, (nb & ~1) % S);
+              umma_commit(b_s + 8 * rt);
+            };
+            look(true);
+            if (ready) {
+              make_s(0);
+              make_s(1);
+            }
+            while (ready) {
+              const int cb = nb, ce = min((nb | 1) + 1, ts);  // the unit whose S are made
+              bool made[2] = {false, false};
+              nb = ce;
+              ready = false;
 #pragma unroll
               for (int rt = 0; rt < 2; ++rt) {
-                if (nx[rt] == sd[rt] && sd[rt] < ts) {
-                  const int up = (sd[rt] | 1) + 1;
-                  if (ended || ts >= up) {
-                    some = true;
-                    tc_fence_after();
-                    s_product(tmem + rt * 2 * kTile, rt, (sd[rt] & ~1) % S);
-                    umma_commit(b_s + 8 * rt);
-                    sd[rt] = min(up, ts);
-                  }
-                }
-                const int buf = 2 * rt + (nx[rt] & 1);
-                if (nx[rt] < sd[rt] && mbar_test_wait(b_p + 8 * buf, p_par >> buf & 1u)) {
-                  some = true;
+                for (int x = cb; ok && x < ce; ++x) {
+                  const int buf = 2 * rt + (x & 1);
+                  if (!(ok = wait(b_p + 8 * buf, p_par >> buf))) break;
                   p_par ^= 1u << buf;
                   tc_fence_after();
-                  pv_product(rt, buf, nx[rt] % S, !fresh[rt]);
-                  fresh[rt] = false;
+                  pv_product(rt, buf, x % S, fresh >> rt & 1u);
+                  fresh |= 1u << rt;
                   umma_commit(b_pv + 8 * buf);
-                  if (nx[1 - rt] > nx[rt]) umma_commit(b_empty + 8 * (nx[rt] % S));
-                  ++nx[rt];
+                  if (rt == 1) umma_commit(b_empty + 8 * (x % S));
+                }
+                if (!ready) look(false);
+                if (ready) {
+                  make_s(rt);
+                  made[rt] = true;
                 }
               }
-              idle();
+              if (!ready) look(true);
+              if (ready) {
+                if (!made[0]) make_s(0);
+                if (!made[1]) make_s(1);
+              }
             }
           } else {
             int cs = c, cp = c;
@@ -589,8 +613,8 @@ tree_tc(const __grid_constant__ TreeArgs a, const __grid_constant__ CUtensorMap 
                 some = true;
                 tc_fence_after();
                 const int wg = cp & 1, st = (t + (cp - c) / NT) % S;
-                pv_product(wg, cp % kSBuf, st, !fresh[wg]);
-                fresh[wg] = false;
+                pv_product(wg, cp % kSBuf, st, fresh >> wg & 1u);
+                fresh |= 1u << wg;
                 umma_commit(b_pv + 8 * (cp % kSBuf));
                 if (NT == 1 || ((cp - c) & 1)) umma_commit(b_empty + 8 * st);
                 ++cp;
@@ -884,11 +908,14 @@ tree_tc(const __grid_constant__ TreeArgs a, const __grid_constant__ CUtensorMap 
             emit(x0, 0);
             emit(x1, 1);
           };
-          if (__any_sync(0xffffffffu, m == -INFINITY)) take_max();
-          emit_all();
-          if (__any_sync(0xffffffffu, !(la + lb <= kSumCap))) {
-            take_max();
+          // (a loop, so that the code is there once: the warps' instructions share a cache)
+          bool again = __any_sync(0xffffffffu, m == -INFINITY);
+#pragma unroll 1
+          for (int pass = 0; pass < 2; ++pass) {
+            if (again) take_max();
             emit_all();
+            again = pass == 0 && __any_sync(0xffffffffu, !(la + lb <= kSumCap));
+            if (!again) break;
           }
           l += (la + lb) * unit;
         } else if constexpr (!B16) {
