@@ -75,11 +75,11 @@ struct alignas(16) TileMeta<false> {
 };
 
 // What the readers and the MMA warp have to know of a tile, from a loader: its place in the
-// list and its keys; whether it is none but the segment's end; whether it comes by TMA.
+// list and its keys, or kEnd where it is none but the segment's end.
 struct Order {
   int tail, n;
 };
-enum TileKind { kEnd = -1, kTmaTile = 1 << 16 };  // n: kEnd, or the keys, + kTmaTile
+constexpr int kEnd = -1;
 
 template <int D, int FMT, int NT>
 struct Tc {
@@ -352,14 +352,15 @@ tree_tc(const __grid_constant__ TreeArgs a, const __grid_constant__ CUtensorMap 
         const uint32_t vst = smem_u32(sm + (B16 ? L::v_at(sl) : L::OFF_RAW + sl * L::RAW_TILE + kTile * D));
         by_tma = (by_tma & ~(1u << sl)) | (uint32_t)run << sl;
         if (lt == 0) {
-          orders[t & (kOrders - 1)] = Order{tail, n + (run ? kTmaTile : 0)};
+          orders[t & (kOrders - 1)] = Order{tail, n};
           mbar_arrive(b_order + 8 * (t & (kOrders - 1)));
         }
         if (run) {
           if (lt == 0) {
             if (!B16 && t >= L::SLOTS && !wait(b_raw + 8 * sl, t / L::SLOTS - 1)) ok = false;
             if (ok) {
-              const uint32_t bt = b_tma + 8 * sl;
+              // bf16: on the stage's own barrier, as this warp's arrival; codes: on the slot's
+              const uint32_t bt = B16 ? b_full + 8 * sl : b_tma + 8 * sl;
               mbar_expect_tx(bt, 2 * kTile * D * ES);
               const int z = b * a.cap + first;
               if constexpr (B16) {
@@ -378,8 +379,7 @@ tree_tc(const __grid_constant__ TreeArgs a, const __grid_constant__ CUtensorMap 
           if (!ok) return;
           tma_odd ^= 1u << sl;
           tma_any |= 1u << sl;
-          // bf16: the MMA warp waits for the copy itself
-          if (B16 && lane == 0) mbar_arrive(b_full + 8 * sl);
+          if (B16 && lane == 0 && lw > 0) mbar_arrive(b_full + 8 * sl);
         } else {
           constexpr int CH = D * ES / 16, RPI = 128 / CH;  // pieces per row, rows per pass
           const int ch = lt % CH;
@@ -472,8 +472,11 @@ tree_tc(const __grid_constant__ TreeArgs a, const __grid_constant__ CUtensorMap 
     });
     cp_async_wait<0>();
     if (lt == 0 && *abort_flag)  // giving up: copies in flight land before the CTA exits
-      for (int i = 0; i < L::SLOTS; ++i)
-        if (tma_any >> i & 1u) mbar_drain(b_tma + 8 * i, (tma_odd >> i & 1u) ^ 1u);
+      for (int i = 0; i < L::SLOTS; ++i) {
+        if (!(tma_any >> i & 1u)) continue;
+        if constexpr (B16) mbar_drain(b_full + 8 * i, (uint32_t)((t - 1 - i) / S & 1));
+        else mbar_drain(b_tma + 8 * i, (tma_odd >> i & 1u) ^ 1u);
+      }
     __syncwarp();
   } else if (warp >= kMmaWarp) {
     fewer_registers();
@@ -482,7 +485,6 @@ tree_tc(const __grid_constant__ TreeArgs a, const __grid_constant__ CUtensorMap 
       constexpr uint32_t IS = B16 ? idesc_bf16(kRows, L::PAIR ? 2 * kTile : kTile, 0) : idesc_f16(kRows, kTile, 0);
       constexpr uint32_t IPV = B16 ? idesc_bf16(kRows, D, 1) : idesc_f16(kRows, D, 1);
       int t = 0, c = 0, seg = 0;  // tiles with end marks, products, segments
-      uint32_t tma_par = 0u;      // by stage: parity of its next TMA copy (bf16)
       uint32_t p_par = 0u;        // pairs: by P tile, parity of its next P
       bool ok = true;
       auto s_product = [&](uint32_t dst, int rt, int stage) {
@@ -520,16 +522,10 @@ tree_tc(const __grid_constant__ TreeArgs a, const __grid_constant__ CUtensorMap 
             }
             some = false;
           };
-          // Tile x is there (or the end mark in its place).
+          // Tile x, or the end mark in its place, is there.
           auto arrived = [&](int x) {
             if (!mbar_test_wait(b_full + 8 * (x % S), (x / S) & 1)) return false;
-            const int n = orders[x & (kOrders - 1)].n;
-            if (n == kEnd) {
-              ended = true;
-            } else if (B16 && n >= kTmaTile) {
-              if (!mbar_test_wait(b_tma + 8 * (x % S), tma_par >> (x % S) & 1u)) return false;
-              tma_par ^= 1u << (x % S);
-            }
+            ended = orders[x & (kOrders - 1)].n == kEnd;
             return true;
           };
           int ts = t;  // tiles looked at; at the end, the first end mark
@@ -542,14 +538,14 @@ tree_tc(const __grid_constant__ TreeArgs a, const __grid_constant__ CUtensorMap 
             int nb = t;          // its first tile
             auto look = [&](bool block) {
               const int up = (nb | 1) + 1;
-              while (ok && !ended && ts < up) {
-                if (arrived(ts)) {
-                  some = true;
-                  if (!ended) ++ts;
-                } else if (!block) {
+              while (!ended && ts < up) {
+                if (block) {
+                  if (!(ok = wait(b_full + 8 * (ts % S), ts / S))) break;
+                  ended = orders[ts & (kOrders - 1)].n == kEnd;
+                } else if (!arrived(ts)) {
                   return;
                 }
-                idle();
+                if (!ended) ++ts;
               }
               ready = ok && nb < ts;
             };
@@ -677,7 +673,7 @@ tree_tc(const __grid_constant__ TreeArgs a, const __grid_constant__ CUtensorMap 
             ++marks;
             if (mine && lane == 0) me.end = 1;
           } else if (mine) {
-            const int n = o.n & (kTmaTile - 1);
+            const int n = o.n;
             const int first = lidx[o.tail & (kList - 1)], last = lidx[(o.tail + n - 1) & (kList - 1)];
             int j[2];
             uint32_t mk[2], valid[2];
