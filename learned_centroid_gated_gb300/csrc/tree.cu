@@ -99,7 +99,8 @@ tree_split(const __grid_constant__ TreeArgs a) {
   const int64_t kvrow = (int64_t)a.H_kv * D;  // elements per slot
   constexpr int ES = B16 ? 2 : 1;
 
-  for_segments(a, blockIdx.x, lane, [&](int64_t partial, int kvh, int rg, int b, int len, int js, int je) {
+  const Slice slice = slice_of(a, blockIdx.x, lane);
+  for_segments(a, slice, blockIdx.x, lane, [&](int64_t partial, int kvh, int rg, int b, int len, int js, int je) {
     // The rows: row x of the group is query head x % gq of drafted token x / gq.  With all
     // rows of one token its list of keys is exact and needs no test per element.
     const int r_end = min(a.rows - rg * NR, NR);
@@ -557,6 +558,58 @@ __device__ __noinline__ float row_by_hand(const TreeArgs& a, int b, int t, int h
   return out;
 }
 
+// Where the partials of row (t, h) of sequence b are.
+struct RowParts {
+  int64_t ln, from, whole, part;
+  Stretch s;
+  int b, len, row, ns, first, last, n;  // slices first .. last may hold a part; n: partials to look at
+
+  __device__ __forceinline__ bool find(const TreeArgs& a, int c, int64_t& slot) const {
+    const int sl = first + c / a.parts;
+    const int64_t lo = slice_at(whole, ns, part, sl), hi = slice_at(whole, ns, part, sl + 1);
+    if (units_before(a, s, lo - from) >= units_before(a, s, hi - from)) return false;  // no such partial
+    slot = ((sl + ln * a.B + b) * a.parts + c % a.parts) * a.grp + row % a.grp;
+    return true;
+  }
+};
+
+// All of a warp's lanes; total: all sequences' weight, bad: some length is out of range.
+__device__ __forceinline__ RowParts row_parts(const TreeArgs& a, int b, int t, int h, int lane, int64_t& total, bool& bad) {
+  RowParts r;
+  r.b = b, r.row = t * a.gq + h % a.gq;
+  r.ln = (int64_t)(h / a.gq) * a.nrg + r.row / a.grp;
+  total = 0, r.from = 0, bad = false;
+  for (int x = lane; x < a.B; x += 32) {
+    const int n = __ldg(a.lens + x);
+    const int64_t wgt = stretch_of(a, n).weight;
+    bad = bad || !len_ok(a, n);
+    total += wgt;
+    r.from += x < b ? wgt : 0;  // those before sequence b
+  }
+  total = warp_sum(total);
+  r.from = warp_sum(r.from) + r.ln * total;
+  bad = __any_sync(0xffffffffu, bad);
+  r.len = __ldg(a.lens + b);
+  r.s = stretch_of(a, r.len);
+  r.whole = total * a.H_kv * a.nrg;
+  r.ns = slices_of(a, r.whole);
+  const bool live = r.s.units > 0 && tree_word(a, b, t) != 0ull;
+  r.part = quotient(r.whole, r.ns);  // a slice is `part` weights or one more
+  r.first = live ? (int)max((int64_t)0, quotient(r.from, r.part + 1) - 1) : 0;
+  r.last = live ? (int)min((int64_t)r.ns - 1, quotient(r.from + r.s.weight, r.part) + 1) : -1;
+  r.n = (r.last - r.first + 1) * a.parts;
+  return r;
+}
+
+// The call's status, by one warp.
+__device__ __forceinline__ void put_status(const TreeArgs& a, int ns, int64_t total, bool bad, int lane) {
+  int code = 0;
+  if (a.flags && total > 0)
+    for (int x = lane; x < ns; x += 32) code = min(code, a.flags[x]);
+  code = __reduce_min_sync(0xffffffffu, code);
+  if (lane == 0) *a.status = code ? code : bad ? FOCUS_ERR_BOUNDS : 0;
+}
+
 // Merge the partials of one row: grid (T * H, B), NT threads.  A pass takes NT of the
 // slices that may hold a part of the row's sequence: a thread finds out whether its slice
 // does, and its partial's (max, sum); with the largest maximum of all the weights are known,
@@ -565,7 +618,7 @@ __device__ __noinline__ float row_by_hand(const TreeArgs& a, int b, int t, int h
 // behind 128K tokens).  A programmatic dependent of the kernel that writes the partials.
 template <int D, int FMT, int NT>
 __global__ void __launch_bounds__(NT) tree_combine(const __grid_constant__ TreeArgs a) {
-  constexpr int NG = NT / D, NW = NT / 32;
+  constexpr int NG = NT / D, NW = NT / 32, U = 8;
   __shared__ float weight[NT];
   __shared__ int64_t place[NT];
   __shared__ float sums[NG][D];
@@ -573,49 +626,17 @@ __global__ void __launch_bounds__(NT) tree_combine(const __grid_constant__ TreeA
   __shared__ unsigned bits[NW];
   const int tid = threadIdx.x, wp = tid >> 5, lane = tid & 31, g = tid / D, d = tid % D;
   const int b = blockIdx.y, t = blockIdx.x / a.H, h = blockIdx.x % a.H;
-  const int kvh = h / a.gq, row = t * a.gq + h % a.gq, rg = row / a.grp;
-  const int64_t ln = (int64_t)kvh * a.nrg + rg;
-  int64_t total = 0, from = 0;  // all sequences' weight, and that before sequence b
-  bool bad = false;
-  for (int x = lane; x < a.B; x += 32) {
-    const int n = __ldg(a.lens + x);
-    const int64_t wgt = stretch_of(a, n).weight;
-    bad = bad || !len_ok(a, n);
-    total += wgt;
-    from += x < b ? wgt : 0;
-  }
-  total = warp_sum(total);
-  from = warp_sum(from) + ln * total;
-  bad = __any_sync(0xffffffffu, bad);
-  const int len = __ldg(a.lens + b);
-  const Stretch s = stretch_of(a, len);
-  const int64_t whole = total * a.H_kv * a.nrg;
-  const int ns = slices_of(a, whole);
-  const bool live = s.units > 0 && tree_word(a, b, t) != 0ull;
-  const int first = live ? (int)max((int64_t)0, from * ns / whole - 1) : 0;
-  const int last = live ? (int)min((int64_t)ns - 1, (from + s.weight) * ns / whole + 1) : -1;
-  const int n = (last - first + 1) * a.parts;
+  int64_t total;
+  bool bad;
+  const RowParts rp = row_parts(a, b, t, h, lane, total, bad);
   asm volatile("griddepcontrol.wait;" ::: "memory");
-  if (blockIdx.x == 0 && b == 0 && wp == 0) {  // the call's status
-    int code = 0;
-    if (a.flags && total > 0)
-      for (int x = lane; x < ns; x += 32) code = min(code, a.flags[x]);
-    code = __reduce_min_sync(0xffffffffu, code);
-    if (lane == 0) *a.status = code ? code : bad ? FOCUS_ERR_BOUNDS : 0;
-  }
+  if (blockIdx.x == 0 && b == 0 && wp == 0) put_status(a, rp.ns, total, bad, lane);
   float m = -INFINITY, l = 0.0f, acc = 0.0f;  // of all; this thread's shares
-  for (int base = 0; base < n; base += NT) {
+  for (int base = 0; base < rp.n; base += NT) {
     const int c = base + tid;
     float2 x = make_float2(-INFINITY, 0.0f);
     int64_t slot = 0;
-    if (c < n) {
-      const int sl = first + c / a.parts;
-      const int64_t lo = whole * sl / ns, hi = whole * (sl + 1) / ns;
-      if (units_before(a, s, lo - from) < units_before(a, s, hi - from)) {  // else no such partial
-        slot = ((sl + ln * a.B + b) * a.parts + c % a.parts) * a.grp + row % a.grp;
-        x = a.part_ml[slot];
-      }
-    }
+    if (c < rp.n && rp.find(a, c, slot)) x = a.part_ml[slot];
     const bool some = x.y != 0.0f;  // a key of the slice is seen
     float top = some ? x.x : -INFINITY;
 #pragma unroll
@@ -634,11 +655,25 @@ __global__ void __launch_bounds__(NT) tree_combine(const __grid_constant__ TreeA
     weight[tid] = w;
     place[tid] = slot * D;
     __syncthreads();
-    const int end = min(NT, n - base);
+    const int end = min(NT, rp.n - base);
+    if constexpr (NT == 128) {  // a thread has many to sum: U loads in flight
+      for (int i0 = g; i0 < end; i0 += U * NG) {
+        float y[U], p[U];
+#pragma unroll
+        for (int i = 0; i < U; ++i) {
+          const int at = i0 + i * NG;
+          y[i] = at < end ? weight[at] : 0.0f;
+          p[i] = y[i] != 0.0f ? a.part_acc[place[at] + d] : 0.0f;
+        }
+#pragma unroll
+        for (int i = 0; i < U; ++i) acc += y[i] * p[i];
+      }
+    } else {
 #pragma unroll 4
-    for (int i = g; i < end; i += NG) {
-      const float y = weight[i];
-      if (y != 0.0f) acc += y * a.part_acc[place[i] + d];
+      for (int i = g; i < end; i += NG) {
+        const float y = weight[i];
+        if (y != 0.0f) acc += y * a.part_acc[place[i] + d];
+      }
     }
     __syncthreads();
   }
@@ -655,9 +690,94 @@ __global__ void __launch_bounds__(NT) tree_combine(const __grid_constant__ TreeA
   const float lse2 = m + log2f(sum);
   out = empty ? 0.0f : out / sum;
   if (__syncthreads_or(tid < D && !(fabsf(out) < INFINITY)))
-    out = row_by_hand<D, FMT, NT>(a, b, t, h, len, lse2, weight, bits);
+    out = row_by_hand<D, FMT, NT>(a, b, t, h, rp.len, lse2, weight, bits);
   if (tid < D) a.o[(((int64_t)b * a.T + t) * a.H + h) * D + d] = __float2bfloat16_rn(out);
   if (tid == 0 && a.lse) a.lse[((int64_t)b * a.H + h) * a.T + t] = empty ? -INFINITY : lse2 * kLn2;
+}
+
+// The same with a warp per row, for calls of many rows: grid (T * H / 8 rounded up, B).
+template <int D, int FMT>
+__global__ void __launch_bounds__(256) tree_combine_rows(const __grid_constant__ TreeArgs a) {
+  constexpr int NT = 256, U = 8, V = D / 32;  // V: columns of a lane
+  using vec = std::conditional_t<V == 4, float4, float2>;
+  __shared__ float weight[NT];
+  __shared__ unsigned bits[NT / 32];
+  __shared__ float lse_of[NT / 32];
+  const int wp = threadIdx.x >> 5, lane = threadIdx.x & 31, b = blockIdx.y;
+  const int x = blockIdx.x * 8 + wp, t = min(x, a.T * a.H - 1) / a.H, h = x % a.H;
+  int64_t total;
+  bool bad;
+  const RowParts rp = row_parts(a, b, t, h, lane, total, bad);
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  if (x == 0 && b == 0) put_status(a, rp.ns, total, bad, lane);
+  const bool mine = x < a.T * a.H;
+  float m = -INFINITY, l = 0.0f, acc[V];
+#pragma unroll
+  for (int v = 0; v < V; ++v) acc[v] = 0.0f;
+  for (int base = 0; mine && base < rp.n; base += 32) {
+    float2 ml = make_float2(-INFINITY, 0.0f);
+    int64_t slot = 0;
+    if (base + lane < rp.n && rp.find(a, base + lane, slot)) ml = a.part_ml[slot];
+    const bool some = ml.y != 0.0f;  // a key of the slice is seen
+    float top = some ? ml.x : -INFINITY;
+#pragma unroll
+    for (int o = 16; o; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+    if (top == -INFINITY && !__any_sync(0xffffffffu, some)) continue;  // as above
+    const float mn = fmaxf(m, top), f = m == -INFINITY ? 0.0f : ex2(m - mn);
+    const float w = some ? ex2(ml.x - mn) : 0.0f;
+    l = l * f + (some ? ml.y * w : 0.0f);
+    m = mn;
+#pragma unroll
+    for (int v = 0; v < V; ++v) acc[v] *= f;
+    const int end = min(32, rp.n - base);
+    for (int i0 = 0; i0 < end; i0 += U) {  // U loads in flight
+      float y[U];
+      vec p[U];
+#pragma unroll
+      for (int i = 0; i < U; ++i) {
+        y[i] = __shfl_sync(0xffffffffu, w, i0 + i);
+        const int64_t from = __shfl_sync(0xffffffffu, slot, i0 + i) * D + V * lane;
+        p[i] = vec{};
+        if (y[i] != 0.0f) p[i] = *reinterpret_cast<const vec*>(a.part_acc + from);
+      }
+#pragma unroll
+      for (int i = 0; i < U; ++i) {
+        acc[0] += y[i] * p[i].x, acc[1] += y[i] * p[i].y;
+        if constexpr (V == 4) acc[2] += y[i] * p[i].z, acc[3] += y[i] * p[i].w;
+      }
+    }
+  }
+#pragma unroll
+  for (int o = 16; o; o >>= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
+  const bool empty = l == 0.0f;
+  const float lse2 = m + log2f(l);
+  bool odd = false;
+#pragma unroll
+  for (int v = 0; v < V; ++v) {
+    acc[v] = empty ? 0.0f : acc[v] / l;
+    odd = odd || !(fabsf(acc[v]) < INFINITY);
+  }
+  if (mine) {
+    bf16* o = a.o + (((int64_t)b * a.T + t) * a.H + h) * D + V * lane;
+    if constexpr (V == 4)
+      *reinterpret_cast<uint2*>(o) = make_uint2(pack_bf16(acc[0], acc[1]), pack_bf16(acc[2], acc[3]));
+    else
+      *reinterpret_cast<uint32_t*>(o) = pack_bf16(acc[0], acc[1]);
+    if (lane == 0 && a.lse) a.lse[((int64_t)b * a.H + h) * a.T + t] = empty ? -INFINITY : lse2 * kLn2;
+  }
+  odd = __any_sync(0xffffffffu, odd && mine);
+  if (!__syncthreads_or(odd)) return;
+  // rows that are not finite, one after another, by all warps
+  __shared__ int again[NT / 32];
+  if (lane == 0) again[wp] = odd, lse_of[wp] = lse2;
+  __syncthreads();
+  for (int i = 0; i < NT / 32; ++i) {
+    if (!again[i]) continue;
+    const int y = blockIdx.x * 8 + i, ty = y / a.H, hy = y % a.H;
+    const float out = row_by_hand<D, FMT, NT>(a, b, ty, hy, rp.len, lse_of[i], weight, bits);
+    if (threadIdx.x < D) a.o[(((int64_t)b * a.T + ty) * a.H + hy) * D + threadIdx.x] = __float2bfloat16_rn(out);
+    __syncthreads();
+  }
 }
 
 // ------------------------------------------------------------------------- launch --
@@ -683,7 +803,15 @@ TreePlan tree_plan(const focus_cache_params& p) {
   TreePlan t;
   t.gq = p.H / p.H_kv;
   t.rows = p.T * t.gq;
-  t.tc = t.rows > 16;
+  // Which kernel.  Up to 16 rows fill one warp's products.  With more, the one-warp kernel
+  // reads the keys once per 16 rows, the tensor-core kernel once per 256, but it takes 12 us
+  // more to set up and to merge.  Then 32 keys of a KV head cost it about 3.0 ns (5.5 with over 128 rows)
+  // against 2.5 ns per 16 rows: With the merge, 64 rows per KV head over 2K bf16 keys take
+  // 35 us against 26, over 16K 41 against 61, over 128K 126 against 334; 256 rows over 2K 36
+  // against 43.  The lengths are not known here: the capacity stands for them.
+  const double units = (double)p.B * p.H_kv * ((p.cap + kTreeUnit - 1) / kTreeUnit);
+  const int r16 = (t.rows + 15) / 16, r128 = (t.rows + 127) / 128;
+  t.tc = t.rows > 16 && 20e3 + units * (r128 == 1 ? 3.0 : 5.5 * ((r128 + 1) / 2)) < 8e3 + units * 2.5 * r16;
   t.grp = t.tc ? (t.rows > kTreeTcRows ? 2 * kTreeTcRows : kTreeTcRows) : t.rows > 8 ? 16 : 8;
   t.nrg = (t.rows + t.grp - 1) / t.grp;
   t.parts = t.grp == kTreeTcRows ? 2 : 1;
@@ -714,18 +842,18 @@ cudaError_t launch_split(const TreeArgs& a, cudaStream_t s) {
   return cudaGetLastError();
 }
 
-template <int D, int FMT, int NT>
-cudaError_t launch_combine(const TreeArgs& a, cudaStream_t s) {
+template <typename K>
+cudaError_t launch_combine(const TreeArgs& a, K* kernel, int rows, int threads, cudaStream_t s) {
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)(a.T * a.H), (unsigned)a.B);
-  cfg.blockDim = dim3(NT);
+  cfg.gridDim = dim3((unsigned)((a.T * a.H + rows - 1) / rows), (unsigned)a.B);
+  cfg.blockDim = dim3((unsigned)threads);
   cfg.stream = s;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  const cudaError_t e = cudaLaunchKernelEx(&cfg, tree_combine<D, FMT, NT>, a);
+  const cudaError_t e = cudaLaunchKernelEx(&cfg, kernel, a);
   return e != cudaSuccess ? e : cudaGetLastError();
 }
 
@@ -735,11 +863,17 @@ cudaError_t launch_tree(const TreeArgs& a, bool tc, cudaStream_t s) {
                         : a.grp == 8 ? launch_split<D, FMT, 8>(a, s)
                                      : launch_split<D, FMT, 16>(a, s);
   if (e != cudaSuccess) return e;
-  // threads of the merge by the partials of a row, were all sequences alike
+  // The merge, by its rows and by the partials of one, were all sequences alike.  Few rows with
+  // many partials: many threads for a row (32 rows of 210: 10 us with 1024 threads, 33 with a
+  // warp).  Many rows with few: 2048 of 19 take 8 us by warps, 12 by 128 threads, 41 by 512;
+  // 512 of 38 take 13, 9.5 and 14; 256 of 38 take 15, 11 and 9.
   const int64_t each = (int64_t)a.G * a.parts / ((int64_t)a.H_kv * a.nrg * a.B);
-  return each > 256 ? launch_combine<D, FMT, 1024>(a, s)
-         : each > 16 ? launch_combine<D, FMT, 512>(a, s)
-                     : launch_combine<D, FMT, 128>(a, s);
+  const int64_t rows = (int64_t)a.T * a.H * a.B;
+  if (each <= 32 && rows >= 1536) return launch_combine(a, tree_combine_rows<D, FMT>, 8, 256, s);
+  if (each <= 64 && rows >= 512) return launch_combine(a, tree_combine<D, FMT, 128>, 1, 128, s);
+  return each > 256 ? launch_combine(a, tree_combine<D, FMT, 1024>, 1, 1024, s)
+         : each > 16 ? launch_combine(a, tree_combine<D, FMT, 512>, 1, 512, s)
+                     : launch_combine(a, tree_combine<D, FMT, 128>, 1, 128, s);
 }
 
 }  // namespace

@@ -60,12 +60,26 @@ __device__ __forceinline__ Stretch stretch_of(const TreeArgs& a, int len) {
   s.weight = (int64_t)s.far * a.wfar + (int64_t)(s.units - s.far) * kTreeNear;
   return s;
 }
+// Quotient of non-negative numbers, the short way where they fit 32 bits.  They nearly always
+// do; beyond, bit by bit (the compiler's 64-bit division takes some hundred instructions at
+// each place, and code that is fetched only once costs more than it runs).
+__device__ __forceinline__ int64_t quotient(int64_t x, int64_t y) {
+  if (((uint64_t)x | (uint64_t)y) >> 32 == 0ull) return (int64_t)((uint32_t)x / (uint32_t)y);
+  int64_t q = 0;
+#pragma unroll 1
+  for (int i = __clzll(y) - __clzll(x | 1); i >= 0; --i)
+    if (y <= x >> i) {
+      x -= y << i;
+      q |= 1ll << i;
+    }
+  return q;
+}
 // Units of a stretch that begin before weight x.
 __device__ __forceinline__ int units_before(const TreeArgs& a, const Stretch& s, int64_t x) {
   if (x <= 0) return 0;
+  if (x >= s.weight) return s.units;
   const int64_t wf = (int64_t)s.far * a.wfar;
-  const int64_t u = x <= wf ? (x + a.wfar - 1) / a.wfar : s.far + (x - wf + kTreeNear - 1) / kTreeNear;
-  return (int)min((int64_t)s.units, u);
+  return x <= wf ? (int)quotient(x + a.wfar - 1, a.wfar) : s.far + (int)((x - wf + kTreeNear - 1) / kTreeNear);
 }
 __device__ __forceinline__ int64_t warp_sum(int64_t x) {
 #pragma unroll
@@ -88,26 +102,50 @@ __device__ __forceinline__ int64_t total_weight(const TreeArgs& a, int lane) {
   return warp_sum(t);
 }
 __device__ __forceinline__ int slices_of(const TreeArgs& a, int64_t row_weight) {
-  return (int)max((int64_t)1, min((int64_t)a.G, row_weight / kTreeNear));
+  int64_t n = min((int64_t)a.G, row_weight / kTreeNear);
+  // whole slices per (KV head, row group) where that leaves out little: the heads' slices then
+  // walk along the same tokens, whose rows lie side by side
+  const int lanes = a.H_kv * a.nrg, over = n > lanes ? (int)n % lanes : 0;
+  if (over * 16 <= n) n -= over;
+  return (int)max((int64_t)1, n);
+}
+
+// First weight of slice i: the row in ns nearly equal parts.
+__device__ __forceinline__ int64_t slice_at(int64_t row, int ns, int64_t part, int i) {  // part = row / ns
+  return part * i + (uint32_t)((uint32_t)(row - part * ns) * (uint32_t)i) / (uint32_t)ns;
+}
+
+// What a slice has of the row.  A whole warp.
+struct Slice {
+  int64_t W, lo, hi;  // weight of one (KV head, row group); first and last weight of the slice
+  int ln;             // the first (KV head, row group)
+};
+__device__ __forceinline__ Slice slice_of(const TreeArgs& a, int i, int lane) {
+  Slice s{total_weight(a, lane), 0, 0, 0};
+  const int64_t row = s.W * a.H_kv * a.nrg;
+  const int ns = slices_of(a, row);
+  if (s.W == 0 || i >= ns) return s;
+  const int64_t part = quotient(row, ns);
+  s.lo = slice_at(row, ns, part, i);
+  s.hi = slice_at(row, ns, part, i + 1);
+  s.ln = (int)quotient(s.lo, s.W);
+  return s;
 }
 
 // Calls f(number of the partial, KV head, row group, sequence, its length, first key, end)
 // for the segments of a slice, in order; a whole warp.
-template <typename F>
-__device__ __forceinline__ void for_segments(const TreeArgs& a, int slice, int lane, F&& f) {
-  const int64_t W = total_weight(a, lane), row = W * a.H_kv * a.nrg;
-  const int ns = slices_of(a, row);
-  if (W == 0 || slice >= ns) return;
-  const int64_t lo = row * slice / ns, hi = row * (slice + 1) / ns;
-  for (int64_t ln = lo / W; ln * W < hi; ++ln) {
-    int64_t before = ln * W;
-    const int rg = (int)(ln % a.nrg), kvh = (int)(ln / a.nrg);
-    for (int bc = 0; bc < a.B && before < hi; bc += 32) {
+// S: Slice, or a volatile one in shared memory (read where it is used, no registers held).
+template <typename S, typename F>
+__device__ __forceinline__ void for_segments(const TreeArgs& a, const S& sl, int slice, int lane, F&& f) {
+  for (int ln = sl.ln; ln * sl.W < sl.hi; ++ln) {
+    int64_t before = ln * sl.W;
+    const int kvh = ln / a.nrg, rg = ln - kvh * a.nrg;
+    for (int bc = 0; bc < a.B && before < sl.hi; bc += 32) {
       const int lb = bc + lane < a.B ? __ldg(a.lens + bc + lane) : -1;
       const Stretch mine = stretch_of(a, lb);
       const int64_t upto = warp_scan(mine.weight, lane);
       const int64_t from = before + upto - mine.weight;
-      const int my0 = units_before(a, mine, lo - from), my1 = units_before(a, mine, hi - from);
+      const int my0 = units_before(a, mine, sl.lo - from), my1 = units_before(a, mine, sl.hi - from);
       before += __shfl_sync(0xffffffffu, upto, 31);
       unsigned todo = __ballot_sync(0xffffffffu, my0 < my1);
       while (todo) {
@@ -117,7 +155,7 @@ __device__ __forceinline__ void for_segments(const TreeArgs& a, int slice, int l
         const int len = __shfl_sync(0xffffffffu, lb, src);
         const int js = __shfl_sync(0xffffffffu, my0, src) * kTreeUnit;
         const int je = min(len + a.T, __shfl_sync(0xffffffffu, my1, src) * kTreeUnit);
-        f(slice + ln * a.B + b, kvh, rg, b, len, js, je);
+        f(slice + (int64_t)ln * a.B + b, kvh, rg, b, len, js, je);
       }
     }
   }

@@ -105,7 +105,8 @@ struct Tc {
   static constexpr int OFF_CNT = OFF_SETS + 3 * 32 * 8;
   static constexpr int OFF_BAR = OFF_CNT + 2 * 4 * 4;
   static constexpr int BARS = 2 * STAGES + 3 * kSBuf + 8 + 2 * SLOTS + kMeta + kOrders;
-  static constexpr int BYTES = OFF_BAR + 8 * (BARS + 2) + 1024;
+  static constexpr int OFF_SLICE = OFF_BAR + 8 * (BARS + 2);
+  static constexpr int BYTES = OFF_SLICE + (int)sizeof(Slice) + 1024;
   // K rows of a stage: box stride and, of a pair, its tiles one behind the other
   static constexpr int KSTEP = PAIR ? 2 * KBOX : KBOX;
   __host__ __device__ static constexpr int k_at(int stage) {
@@ -171,11 +172,19 @@ tree_tc(const __grid_constant__ TreeArgs a, const __grid_constant__ CUtensorMap 
   int* status = a.flags + blockIdx.x;
 
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  volatile Slice& slice = *reinterpret_cast<volatile Slice*>(sm + L::OFF_SLICE);
+  if (warp == 0) {
+    const Slice mine = slice_of(a, blockIdx.x, lane);
+    if (lane == 0) {
+      slice.W = mine.W, slice.lo = mine.lo, slice.hi = mine.hi;
+      slice.ln = mine.ln;
+    }
+  }
   if (warp == kMmaWarp) {
     tmem_alloc(smem_u32(const_cast<uint32_t*>(tmem_slot)), 512);
     tmem_relinquish();
   }
-  if (tid == 0) {
+  if (tid == 32) {
     for (int i = 0; i < S; ++i) {
       mbar_init(b_full + 8 * i, 4);   // one arrival per loader warp
       mbar_init(b_empty + 8 * i, 1);
@@ -228,7 +237,7 @@ tree_tc(const __grid_constant__ TreeArgs a, const __grid_constant__ CUtensorMap 
       if (lane == 0) mbar_arrive(b_load);
       ok = wait_all(b_load, meets++);
     };
-    for_segments(a, blockIdx.x, lane, [&](int64_t, int kvh, int rg, int b, int len, int js, int je) {
+    for_segments(a, slice, blockIdx.x, lane, [&](int64_t, int kvh, int rg, int b, int len, int js, int je) {
       if (!ok) return;
       const int rho = kvh / (a.H_kv / a.R);
       const uint32_t* M = a.mask + ((int64_t)b * a.R + rho) * a.cap;
@@ -502,7 +511,7 @@ tree_tc(const __grid_constant__ TreeArgs a, const __grid_constant__ CUtensorMap 
           umma_ts(tmem + kSBuf * kTile + wg * 128, tmem + buf * kTile + 8 * kk, dv + ((kk * 2048) >> 4), IPV,
                   add || kk > 0 ? 1u : 0u);
       };
-      for_segments(a, blockIdx.x, lane, [&](int64_t, int, int, int, int, int, int) {
+      for_segments(a, slice, blockIdx.x, lane, [&](int64_t, int, int, int, int, int, int) {
         if (lane == 0 && ok) {
           ok = wait(b_q, seg);
           tc_fence_after();
@@ -641,7 +650,7 @@ tree_tc(const __grid_constant__ TreeArgs a, const __grid_constant__ CUtensorMap 
       uint64_t* sets = reinterpret_cast<uint64_t*>(sm + L::OFF_SETS) + 32 * me_no;  // [group]: keys of a tile
       int t = 0;  // tiles, end marks among them
       bool ok = true;
-      for_segments(a, blockIdx.x, lane, [&](int64_t, int kvh, int rg, int b, int len, int, int) {
+      for_segments(a, slice, blockIdx.x, lane, [&](int64_t, int kvh, int rg, int b, int len, int, int) {
         if (!ok) return;
         const int rho = kvh / (a.H_kv / a.R);
         const uint32_t* M = a.mask + ((int64_t)b * a.R + rho) * a.cap;
@@ -777,7 +786,7 @@ tree_tc(const __grid_constant__ TreeArgs a, const __grid_constant__ CUtensorMap 
     // pairs: parities of the next S of this warpgroup, and of the P V of its two P tiles
     uint32_t s_par = 0u, pv_par = 0u;
     bool ok = true;
-    for_segments(a, blockIdx.x, lane, [&](int64_t partial, int, int rg, int b, int, int, int) {
+    for_segments(a, slice, blockIdx.x, lane, [&](int64_t partial, int, int rg, int b, int, int, int) {
       if (!ok) return;
       const int row0 = rg * NT * kRows, x = row0 + (NT == 2 ? wg * kRows : 0) + r;
       const bool on = x < a.rows;

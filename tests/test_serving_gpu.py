@@ -342,12 +342,15 @@ TREES = {
 }
 
 
-def tree_case(name, fmt, seed=0):
+def tree_case(name, fmt, seed=0, big=False):
+    """big: in a cache of so many slots that more than 16 rows go to the tensor-core kernel."""
     kw = dict(TREES[name])
     T, lens, is_tree = kw.pop("T"), kw.pop("lens"), kw.pop("tree", False)
     dead, zero = kw.pop("dead", False), kw.pop("zero_masks", False)
     kw.setdefault("B", len(lens))
     p = cache_params(format=fmt, **kw)
+    if big:
+        p = dataclasses.replace(p, cap=max(p.cap, 32 * 6500 // (p.B * p.H_kv) + 7))
     c = filled_cache(p, seed + 11)
     if zero:
         c.mask.zero_()
@@ -360,8 +363,10 @@ def tree_case(name, fmt, seed=0):
 
 
 def check_tree(p, c, q, lens, words, o, lse, fmt):
-    want, want_lse, m, s, z = ref.decode_tree(q, ref.dequantise(c.k, c.k_scale), ref.dequantise(c.v, c.v_scale), c.mask,
-                                           lens, words, w=p.w, R=p.R, scale=p.scale, vs=c.v_scale)
+    n = max(lens) + q.shape[1]
+    kv = [ref.dequantise(x[:, :n], None if y is None else y[:, :, :n]) for x, y in ((c.k, c.k_scale), (c.v, c.v_scale))]
+    want, want_lse, m, s, z = ref.decode_tree(q, *kv, c.mask[:, :, :n], lens, words, w=p.w, R=p.R, scale=p.scale,
+                                           vs=None if c.v_scale is None else c.v_scale[:, :, :n].cpu())
     ds = p.d_head * 2.0 ** -22 * s
     up = u(torch.bfloat16 if fmt == "bf16" else torch.float16)
     bound = (up + 4 * ds.transpose(1, 2)[..., None] + 2.0 ** -18) * m + u(torch.bfloat16) * want.abs() + 2.0 ** -28 * z
@@ -378,10 +383,14 @@ def check_tree(p, c, q, lens, words, o, lse, fmt):
     assert bool((lerr <= lbound).all()), ratio
 
 
+ROWS = {n: kw["T"] * kw.get("H", 8) // kw.get("H_kv", 2) for n, kw in TREES.items()}
+SIZES = [(n, False) for n in TREES] + [(n, True) for n in TREES if ROWS[n] > 16]
+
+
 @pytest.mark.parametrize("fmt", ["bf16", "e4m3", "int8"])
-@pytest.mark.parametrize("name", list(TREES))
-def test_decode_tree_matches_the_definition(name, fmt):
-    p, c, q, T, lens, words, is_tree = tree_case(name, fmt)
+@pytest.mark.parametrize("name,big", SIZES)
+def test_decode_tree_matches_the_definition(name, big, fmt):
+    p, c, q, T, lens, words, is_tree = tree_case(name, fmt, big=big)
     ws = torch.empty(focus.decode_tree_workspace_size(p, T), dtype=torch.uint8, device="cuda")
     tree = torch.tensor(ref.signed(words), dtype=torch.int64, device="cuda") if is_tree else None
     n = torch.tensor(lens, dtype=torch.int32, device="cuda")
@@ -398,11 +407,12 @@ def test_decode_tree_matches_the_definition(name, fmt):
     assert focus.decode_tree(p, q.cuda(), c, n, tree, want_lse=False)[1] is None
 
 
+@pytest.mark.parametrize("big", [False, True])
 @pytest.mark.parametrize("fmt", ["bf16", "e4m3", "int8"])
-def test_decode_tree_ignores_what_it_must_not_see(fmt):
+def test_decode_tree_ignores_what_it_must_not_see(fmt, big):
     """NaN and infinities in slots behind the drafted tokens, in keys whose masks do not
     meet a row's and in other branches of the tree reach no row that does not see them."""
-    p, c, q, T, lens, words, _ = tree_case("tree16", fmt)
+    p, c, q, T, lens, words, _ = tree_case("tree16", fmt, big=big)
     lens, words = [500, 31], [[1 << t | 1 for t in range(T)] for _ in lens]   # leaves of one root
     tree = torch.tensor(ref.signed(words), dtype=torch.int64, device="cuda")
     n = torch.tensor(lens, dtype=torch.int32, device="cuda")
@@ -416,10 +426,8 @@ def test_decode_tree_ignores_what_it_must_not_see(fmt):
             c.k_scale[b, :, j] = value
             c.v_scale[b, :, j] = value
 
-    for j in range(lens[0] + T, p.cap):
-        spoil(0, j, math.nan)
-    for j in range(lens[1] + T, p.cap):
-        spoil(1, j, math.inf)
+    spoil(0, slice(lens[0] + T, p.cap), math.nan)
+    spoil(1, slice(lens[1] + T, p.cap), math.inf)
     o, lse = focus.decode_tree(p, q.cuda(), c, n, tree)
     assert torch.equal(o, clean) and torch.equal(lse, clean_lse)
     # a leaf's own key: only that leaf's rows change
@@ -443,15 +451,22 @@ def test_decode_tree_ignores_what_it_must_not_see(fmt):
                     assert bool(got.isfinite().all())
                     # such a row is computed again key by key: fp32 throughout
                     assert bool(((got.float() - want.float()).abs() <= 2.0 ** -6).all())
-                    assert torch.equal(lse[b, r * per:(r + 1) * per, t], ref_lse[b, r * per:(r + 1) * per, t])
+                    got_l, want_l = (x[b, r * per:(r + 1) * per, t].double() for x in (lse, ref_lse))
+                    # A scale that is no number has its tile's reference m taken key by key, not by
+                    # one power of two: the terms 2^(s - m) are rounded anew on both sides.  Terms
+                    # that count have |s - m| < 32, rounded by 2^-20, times ln 2; the exponential
+                    # adds 2^-22, a sum through at most 32 additions 2^-19, m + log2(l) below 64
+                    # 2^-19: twice their sum is below 2^-16.  bf16 caches have no scales.
+                    assert bool(((got_l - want_l).abs() <= (0.0 if fmt == "bf16" else 2.0 ** -16)).all())
 
 
 @pytest.mark.parametrize("fmt", ["e4m3", "int8"])
-@pytest.mark.parametrize("name", ["chain5", "tree16", "mha64"])
-def test_decode_tree_scales_far_apart(name, fmt):
+@pytest.mark.parametrize("name,big", [("chain5", False), ("chain5", True), ("tree16", False), ("tree16", True),
+                                      ("mha64", False), ("rows_300", True)])
+def test_decode_tree_scales_far_apart(name, big, fmt):
     """V scales of very different sizes, zeros among them, in keys that rows see and in keys
     that they do not: no row loses its own keys' digits to another key's scale."""
-    p, c, q, T, lens, words, is_tree = tree_case(name, fmt, seed=5)
+    p, c, q, T, lens, words, is_tree = tree_case(name, fmt, seed=5, big=big)
     g = torch.Generator().manual_seed(1)
     size = torch.randint(-24, 24, c.v_scale.shape, generator=g).double()
     size[:, :, ::3] = 0
@@ -469,11 +484,11 @@ def test_decode_tree_scales_far_apart(name, fmt):
 def test_decode_tree_logits_that_grow_and_fall():
     """Logits that rise by hundreds along the sequence, and fall again: the reference of the
     exponentials moves many times."""
-    for name in ("tree16", "chain5", "one_token"):
+    for name, big in (("tree16", False), ("tree16", True), ("chain5", False), ("one_token", False), ("rows_300", True)):
         for fmt in ("bf16", "int8"):
-            p, c, q, T, lens, words, is_tree = tree_case(name, fmt, seed=6)
-            up = torch.linspace(0, 30, p.cap)
-            up = torch.minimum(up, 40 - up)
+            p, c, q, T, lens, words, is_tree = tree_case(name, fmt, seed=6, big=big)
+            up = torch.linspace(0, 30, max(lens) + T)
+            up = torch.nn.functional.pad(torch.minimum(up, 40 - up), (0, p.cap - max(lens) - T))
             if fmt == "bf16":
                 c.k.copy_((q.mean((0, 1, 2)) * up[:, None]).to(torch.bfloat16)[None, :, None].expand(c.k.shape))
             else:
