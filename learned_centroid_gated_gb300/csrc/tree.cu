@@ -565,10 +565,10 @@ struct RowParts {
   int b, len, row, ns, first, last, n;  // slices first .. last may hold a part; n: partials to look at
 
   __device__ __forceinline__ bool find(const TreeArgs& a, int c, int64_t& slot) const {
-    const int sl = first + c / a.parts;
+    const int sl = first + c;
     const int64_t lo = slice_at(whole, ns, part, sl), hi = slice_at(whole, ns, part, sl + 1);
     if (units_before(a, s, lo - from) >= units_before(a, s, hi - from)) return false;  // no such partial
-    slot = ((sl + ln * a.B + b) * a.parts + c % a.parts) * a.grp + row % a.grp;
+    slot = (sl + ln * a.B + b) * a.grp + row % a.grp;
     return true;
   }
 };
@@ -597,7 +597,7 @@ __device__ __forceinline__ RowParts row_parts(const TreeArgs& a, int b, int t, i
   r.part = quotient(r.whole, r.ns);  // a slice is `part` weights or one more
   r.first = live ? (int)max((int64_t)0, quotient(r.from, r.part + 1) - 1) : 0;
   r.last = live ? (int)min((int64_t)r.ns - 1, quotient(r.from + r.s.weight, r.part) + 1) : -1;
-  r.n = (r.last - r.first + 1) * a.parts;
+  r.n = r.last - r.first + 1;
   return r;
 }
 
@@ -794,7 +794,7 @@ int split_warps(int d_head, int format, int rows) {
 }
 
 struct TreePlan {
-  int gq, rows, grp, nrg, parts, G, wfar;
+  int gq, rows, grp, nrg, G, wfar;
   bool tc;
   size_t flags, ml, acc, total;  // offsets and size of the workspace
 };
@@ -814,7 +814,6 @@ TreePlan tree_plan(const focus_cache_params& p) {
   t.tc = t.rows > 16 && 20e3 + units * (r128 == 1 ? 3.0 : 5.5 * ((r128 + 1) / 2)) < 8e3 + units * 2.5 * r16;
   t.grp = t.tc ? (t.rows > kTreeTcRows ? 2 * kTreeTcRows : kTreeTcRows) : t.rows > 8 ? 16 : 8;
   t.nrg = (t.rows + t.grp - 1) / t.grp;
-  t.parts = t.grp == kTreeTcRows ? 2 : 1;
   t.G = kTreeSms * (t.tc ? 1 : split_warps(p.d_head, p.format, t.grp));
   const int64_t lanes = (int64_t)p.H_kv * t.nrg;
   const int64_t most = lanes * p.B * (((int64_t)p.cap + kTreeUnit - 1) / kTreeUnit) * kTreeNear;
@@ -823,7 +822,7 @@ TreePlan tree_plan(const focus_cache_params& p) {
   double miss = 1.0;
   for (int i = 0; i < p.top_k; ++i) miss *= std::max(0.0, (double)(p.K - p.top_k - i)) / (p.K - i);
   t.wfar = std::max(1, (int)std::lround(kTreeNear * (1.0 - pow(miss, p.T))));
-  const size_t slots = (size_t)(t.G + lanes * p.B) * t.parts * t.grp;
+  const size_t slots = (size_t)(t.G + lanes * p.B) * t.grp;
   t.flags = 256;
   t.ml = t.flags + align_up(sizeof(int32_t) * t.G, 256);
   t.acc = t.ml + align_up(sizeof(float2) * slots, 256);
@@ -867,7 +866,7 @@ cudaError_t launch_tree(const TreeArgs& a, bool tc, cudaStream_t s) {
   // many partials: many threads for a row (32 rows of 210: 10 us with 1024 threads, 33 with a
   // warp).  Many rows with few: 2048 of 19 take 8 us by warps, 12 by 128 threads, 41 by 512;
   // 512 of 38 take 13, 9.5 and 14; 256 of 38 take 15, 11 and 9.
-  const int64_t each = (int64_t)a.G * a.parts / ((int64_t)a.H_kv * a.nrg * a.B);
+  const int64_t each = (int64_t)a.G / ((int64_t)a.H_kv * a.nrg * a.B);
   const int64_t rows = (int64_t)a.T * a.H * a.B;
   if (each <= 32 && rows >= 1536) return launch_combine(a, tree_combine_rows<D, FMT>, 8, 256, s);
   if (each <= 64 && rows >= 512) return launch_combine(a, tree_combine<D, FMT, 128>, 1, 128, s);
@@ -892,7 +891,7 @@ cudaError_t launch_decode_tree(const focus_cache_params& p, const bf16* q, const
   a.flags = t.tc ? reinterpret_cast<int32_t*>(ws + t.flags) : nullptr;
   a.o = o, a.lse = lse, a.status = reinterpret_cast<int32_t*>(ws);
   a.B = p.B, a.cap = p.cap, a.T = p.T, a.H = p.H, a.H_kv = p.H_kv, a.R = p.R, a.w = p.w;
-  a.gq = t.gq, a.rows = t.rows, a.grp = t.grp, a.nrg = t.nrg, a.parts = t.parts;
+  a.gq = t.gq, a.rows = t.rows, a.grp = t.grp, a.nrg = t.nrg;
   a.G = t.G, a.wfar = t.wfar, a.tma = 0;
   a.sl2 = scale * kLog2e;
   if (p.d_head == 64)

@@ -30,7 +30,6 @@ struct TreeArgs {
   int32_t* status;
   int B, cap, T, H, H_kv, R, w, gq, rows;
   int grp, nrg;      // rows per row group (16, or 128 or 256 on the tensor cores), row groups
-  int parts;         // partials per segment
   int G;             // slices at most
   int wfar;
   int tma;           // tensor-core kernel: tensor maps are there

@@ -54,7 +54,7 @@ constexpr int kOrders = 16;     // entries of the ring of orders
 constexpr int kScan = 256;      // raw keys per listing step
 constexpr int kList = 1024;     // entries of the list ring
 constexpr int kThreads = 512;
-constexpr int kLoadWarp = 8, kMmaWarp = 12, kReadWarp = 13, kReaders = 3;
+constexpr int kMmaWarp = 12, kReadWarp = 13, kReaders = 3;
 
 // What the softmax has to know of a tile, from a reader.
 template <bool B16>
@@ -85,6 +85,7 @@ template <int D, int FMT, int NT>
 struct Tc {
   static constexpr bool B16 = FMT == FOCUS_CACHE_BF16;
   static constexpr bool PAIR = B16 && NT == 2;  // S of two tiles at once
+  static constexpr int LOAD_WARP = 4 * NT, LW = kMmaWarp - LOAD_WARP;  // first loader warp; loader warps
   using Meta = TileMeta<B16>;
   static constexpr int BOXES = D / 64;
   // operand tiles; staging tiles of codes; tiles whose copies (row by row) are in flight
@@ -103,7 +104,7 @@ struct Tc {
   static constexpr int OFF_DOWN = OFF_LIST + kList * 4;
   static constexpr int OFF_SETS = OFF_DOWN + (B16 ? 0 : 2 * NT * kRows * 4);
   static constexpr int OFF_CNT = OFF_SETS + 3 * 32 * 8;
-  static constexpr int OFF_BAR = OFF_CNT + 2 * 4 * 4;
+  static constexpr int OFF_BAR = OFF_CNT + 2 * 8 * 4;
   static constexpr int BARS = 2 * STAGES + 3 * kSBuf + 8 + 2 * SLOTS + kMeta + kOrders;
   static constexpr int OFF_SLICE = OFF_BAR + 8 * (BARS + 2);
   static constexpr int BYTES = OFF_SLICE + (int)sizeof(Slice) + 1024;
@@ -134,7 +135,11 @@ __host__ __device__ constexpr uint32_t idesc_f16(int M, int N, int b_mn_major) {
 
 // Registers: 512 threads launch with 128 each; the two softmax warpgroups take 152, the
 // loaders and the last warpgroup keep 104 (2 x 152 + 2 x 104 = 4 x 128).
-__device__ __forceinline__ void more_registers() { asm volatile("setmaxnreg.inc.sync.aligned.u32 152;"); }
+template <int NT>
+__device__ __forceinline__ void more_registers() {
+  if constexpr (NT == 1) asm volatile("setmaxnreg.inc.sync.aligned.u32 200;");
+  else asm volatile("setmaxnreg.inc.sync.aligned.u32 152;");
+}
 __device__ __forceinline__ void fewer_registers() { asm volatile("setmaxnreg.dec.sync.aligned.u32 104;"); }
 
 __device__ __forceinline__ void sts128(uint32_t addr, uint32_t x, uint32_t y, uint32_t z, uint32_t w) {
@@ -149,7 +154,7 @@ tree_tc(const __grid_constant__ TreeArgs a, const __grid_constant__ CUtensorMap 
   using Meta = typename L::Meta;
   constexpr bool B16 = L::B16;
   constexpr int S = L::STAGES, ES = B16 ? 2 : 1;
-  constexpr int MARKS = NT == 1 ? 2 : 1;  // end marks: one for each warpgroup that steps over tiles
+  constexpr int LW = L::LW;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* sm = smem_raw + (-smem_u32(smem_raw) & 1023u);  // (stays a shared-memory pointer to the compiler)
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -186,7 +191,7 @@ tree_tc(const __grid_constant__ TreeArgs a, const __grid_constant__ CUtensorMap 
   }
   if (tid == 32) {
     for (int i = 0; i < S; ++i) {
-      mbar_init(b_full + 8 * i, 4);   // one arrival per loader warp
+      mbar_init(b_full + 8 * i, LW);  // one arrival per loader warp
       mbar_init(b_empty + 8 * i, 1);
     }
     for (int i = 0; i < kSBuf; ++i) {
@@ -194,14 +199,14 @@ tree_tc(const __grid_constant__ TreeArgs a, const __grid_constant__ CUtensorMap 
       mbar_init(b_p + 8 * i, 4);      // one arrival per softmax warp
       mbar_init(b_pv + 8 * i, 1);
     }
-    mbar_init(b_q, 4);
+    mbar_init(b_q, LW);
     mbar_init(b_qfree, 1);
     for (int i = 0; i < 4; ++i) mbar_init(b_epi + 8 * i, 4);
     mbar_init(b_drain, 1);
-    mbar_init(b_load, 4);
+    mbar_init(b_load, LW);
     for (int i = 0; i < L::SLOTS; ++i) {
       mbar_init(b_tma + 8 * i, 1);
-      mbar_init(b_raw + 8 * i, 4);
+      mbar_init(b_raw + 8 * i, LW);
     }
     for (int i = 0; i < kMeta; ++i) mbar_init(b_meta + 8 * i, 1);
     for (int i = 0; i < kOrders; ++i) mbar_init(b_order + 8 * i, 1);
@@ -216,17 +221,17 @@ tree_tc(const __grid_constant__ TreeArgs a, const __grid_constant__ CUtensorMap 
   const uint32_t tmem = *tmem_slot;
   auto wait = [&](uint32_t b, int phase) { return mbar_wait(b, phase & 1, abort_flag, status); };
   auto wait_all = [&](uint32_t b, int phase) { return __all_sync(0xffffffffu, wait(b, phase)) != 0; };
-  auto o_read = [&](int seg) {  // both warpgroups have read the O of segment seg
+  auto o_read = [&](int seg) {  // the softmax warps have read the O of segment seg
     const uint32_t b = b_epi + 8 * (seg & 1);
-    return wait(b, seg >> 1) && wait(b + 16, seg >> 1);
+    return wait(b, seg >> 1) && (NT == 1 || wait(b + 16, seg >> 1));
   };
 
-  if (warp >= kLoadWarp && warp < kMmaWarp) {
+  if (warp >= L::LOAD_WARP && warp < kMmaWarp) {
     // ------------------------------------------------------------------ loaders --
     fewer_registers();
-    const int lt = tid - 32 * kLoadWarp, lw = lt >> 5;
+    const int lt = tid - 32 * L::LOAD_WARP, lw = lt >> 5;
     int* cnt = reinterpret_cast<int*>(sm + L::OFF_CNT);  // [parity][warp]
-    int t = 0;     // tiles, end marks among them
+    int t = 0;     // tiles, an end mark per segment among them
     int seg = 0, scans = 0, meets = 0;
     // by slot: the tile in it comes by TMA; TMA copies so far (their parity; whether any)
     uint32_t by_tma = 0u, tma_odd = 0u, tma_any = 0u;
@@ -247,7 +252,8 @@ tree_tc(const __grid_constant__ TreeArgs a, const __grid_constant__ CUtensorMap 
       if (seg > 0 && !(ok = wait_all(b_qfree, seg - 1))) return;
 #pragma unroll 1
       for (int rt = 0; rt < NT; ++rt) {
-        const int y = rt * kRows + lt;
+        constexpr int HALVES = LW / 4, CQ = D / 8 / HALVES;  // threads per row, 16-byte chunks of each
+        const int qr = lt % kRows, y = rt * kRows + qr, from = HALVES == 1 ? 0 : lt / kRows * CQ;
         const bool on = y < rows;
         const int x = row0 + (on ? y : 0), tt = x / a.gq, h = kvh * a.gq + x % a.gq;
         const uint4* src = reinterpret_cast<const uint4*>(a.q + (((int64_t)b * a.T + tt) * a.H + h) * D);
@@ -263,19 +269,20 @@ tree_tc(const __grid_constant__ TreeArgs a, const __grid_constant__ CUtensorMap 
               mx = fmaxf(mx, fmaxf(fabsf(__uint_as_float(w[i] << 16)), fabsf(__uint_as_float(w[i] & 0xffff0000u))));
           }
           row_unit(mx, up, dn);
-          down[((seg & 1) * NT + rt) * kRows + lt] = dn;
+          if (from == 0) down[((seg & 1) * NT + rt) * kRows + qr] = dn;
         }
-        const uint32_t q0 = smem_u32(sm) + rt * L::QT + lt * 128;
+        const uint32_t q0 = smem_u32(sm) + rt * L::QT + qr * 128;
 #pragma unroll 4
-        for (int c = 0; c < D / 8; ++c) {
+        for (int i = 0; i < CQ; ++i) {
+          const int c = from + i;
           const uint4 v = on ? __ldg(src + c) : make_uint4(0u, 0u, 0u, 0u);
           uint32_t w[4] = {v.x, v.y, v.z, v.w};
           if constexpr (!B16) {
 #pragma unroll
-            for (int i = 0; i < 4; ++i)
-              w[i] = pack_f16(__uint_as_float(w[i] << 16) * up, __uint_as_float(w[i] & 0xffff0000u) * up);
+            for (int k = 0; k < 4; ++k)
+              w[k] = pack_f16(__uint_as_float(w[k] << 16) * up, __uint_as_float(w[k] & 0xffff0000u) * up);
           }
-          sts128(q0 + (c / 8) * L::QBOX + (((c & 7) ^ (lt & 7)) << 4), w[0], w[1], w[2], w[3]);
+          sts128(q0 + (c / 8) * L::QBOX + (((c & 7) ^ (qr & 7)) << 4), w[0], w[1], w[2], w[3]);
         }
       }
       fence_proxy_async_smem();
@@ -303,7 +310,7 @@ tree_tc(const __grid_constant__ TreeArgs a, const __grid_constant__ CUtensorMap 
       const char* vb = reinterpret_cast<const char*>(a.vc) + base;
 
       int jb = js, head = 0, tail = 0;
-      constexpr int MW = kScan / 128;
+      constexpr int MW = kScan / (32 * LW);
       uint32_t mw[MW];
       auto load_masks = [&]() {
 #pragma unroll
@@ -326,13 +333,17 @@ tree_tc(const __grid_constant__ TreeArgs a, const __grid_constant__ CUtensorMap 
           bal[i] = __ballot_sync(0xffffffffu, see);
           mine += __popc(bal[i]);
         }
-        int* c = cnt + 4 * (scans++ & 1);
+        int* c = cnt + 8 * (scans++ & 1);
         if (lane == 0) c[lw] = mine;
         meet();  // counts there
         if (!ok) return;
-        const int4 c4 = *reinterpret_cast<const int4*>(c);
-        int all = c4.x + c4.y + c4.z + c4.w;
-        int at = head + (lw > 0 ? c4.x : 0) + (lw > 1 ? c4.y : 0) + (lw > 2 ? c4.z : 0);
+        int all = 0, at = head;
+#pragma unroll
+        for (int i = 0; i < LW; ++i) {
+          const int n = c[i];
+          all += n;
+          at += i < lw ? n : 0;
+        }
         if (jb + kScan <= min(len, je) && 4 * all >= 3 * kScan) {
           all = kScan;
           at = head + 32 * MW * lw;
@@ -390,7 +401,7 @@ tree_tc(const __grid_constant__ TreeArgs a, const __grid_constant__ CUtensorMap 
           tma_any |= 1u << sl;
           if (B16 && lane == 0 && lw > 0) mbar_arrive(b_full + 8 * sl);
         } else {
-          constexpr int CH = D * ES / 16, RPI = 128 / CH;  // pieces per row, rows per pass
+          constexpr int CH = D * ES / 16, RPI = 32 * LW / CH;  // pieces per row, rows per pass
           const int ch = lt % CH;
 #pragma unroll 4
           for (int r = lt / CH; r < kTile; r += RPI) {
@@ -418,7 +429,7 @@ tree_tc(const __grid_constant__ TreeArgs a, const __grid_constant__ CUtensorMap 
           if (x >= S && !(ok = wait_all(b_empty + 8 * (x % S), x / S - 1))) return;
           if (!end) {
             const uint32_t raw = smem_u32(sm + L::OFF_RAW + sl * L::RAW_TILE);
-            constexpr int CH = D / 16, RPI = 128 / CH;
+            constexpr int CH = D / 16, RPI = 32 * LW / CH;
             // (16 columns are two 16-byte chunks of the operand tile's row; lanes of the second
             // box store theirs in the other order, so that eight lanes meet all banks)
             const int ch = lt % CH, c = 2 * (ch & 3), second = (ch / 4) & 1;
@@ -466,10 +477,10 @@ tree_tc(const __grid_constant__ TreeArgs a, const __grid_constant__ CUtensorMap 
       }
       cp_async_wait<0>();
       while (ok && landed < t) finish(landed++, false);
-      for (int e = 0; ok && e < MARKS; ++e) {
-        if constexpr (B16) {
-          if (t >= S && !(ok = wait_all(b_empty + 8 * (t % S), t / S - 1))) break;
-        }
+      if constexpr (B16) {
+        if (ok && t >= S) ok = wait_all(b_empty + 8 * (t % S), t / S - 1);
+      }
+      if (ok) {
         if (lt == 0) {
           orders[t & (kOrders - 1)] = Order{0, kEnd};
           mbar_arrive(b_order + 8 * (t & (kOrders - 1)));
@@ -537,7 +548,7 @@ tree_tc(const __grid_constant__ TreeArgs a, const __grid_constant__ CUtensorMap 
             ended = orders[x & (kOrders - 1)].n == kEnd;
             return true;
           };
-          int ts = t;  // tiles looked at; at the end, the first end mark
+          int ts = t;  // tiles looked at; at the end, the end mark
           if constexpr (L::PAIR) {
             // The S of a unit, the tiles of a pair of stages, is made at once for a row half rt
             // when both tiles (or the end) are there and the half's last P V are issued; what
@@ -617,7 +628,7 @@ tree_tc(const __grid_constant__ TreeArgs a, const __grid_constant__ CUtensorMap 
               if (cp < cs && mbar_test_wait(b_p + 8 * (cp % kSBuf), (cp / kSBuf) & 1)) {
                 some = true;
                 tc_fence_after();
-                const int wg = cp & 1, st = (t + (cp - c) / NT) % S;
+                const int wg = NT == 1 ? 0 : cp & 1, st = (t + (cp - c) / NT) % S;
                 pv_product(wg, cp % kSBuf, st, fresh >> wg & 1u);
                 fresh |= 1u << wg;
                 umma_commit(b_pv + 8 * (cp % kSBuf));
@@ -629,11 +640,11 @@ tree_tc(const __grid_constant__ TreeArgs a, const __grid_constant__ CUtensorMap 
             c = cs;
           }
           umma_commit(b_qfree);
-          // The end marks' stages go back once both warpgroups have read them (and O): the
-          // loaders cannot lap a warpgroup that still waits for its mark.
-          if (ok && (ok = wait(b_full + 8 * ((ts + MARKS - 1) % S), (ts + MARKS - 1) / S) && o_read(seg))) {
-            for (int e = 0; e < MARKS; ++e) mbar_arrive(b_empty + 8 * ((ts + e) % S));
-            t = ts + MARKS;
+          // The end mark's stage goes back once the softmax warps have read it (and O): the
+          // loaders cannot lap a warpgroup that still waits for the mark.
+          if (ok && (ok = wait(b_full + 8 * (ts % S), ts / S) && o_read(seg))) {
+            mbar_arrive(b_empty + 8 * (ts % S));
+            t = ts + 1;
           }
           ++seg;
         }
@@ -673,13 +684,13 @@ tree_tc(const __grid_constant__ TreeArgs a, const __grid_constant__ CUtensorMap 
             __reduce_max_sync(0xffffffffu, max(word[0] ? near[0] : INT_MIN, word[1] ? near[1] : INT_MIN));
         const float* ksc = B16 ? nullptr : a.ks + ((int64_t)b * a.H_kv + kvh) * a.cap;
         const float* vsc = B16 ? nullptr : a.vs + ((int64_t)b * a.H_kv + kvh) * a.cap;
-        for (int marks = 0; marks < MARKS; ++t) {
+        for (bool ended = false; !ended; ++t) {
           if (!(ok = wait_all(b_order + 8 * (t & (kOrders - 1)), t / kOrders))) return;
           const Order o = orders[t & (kOrders - 1)];
           const bool mine = t % kReaders == me_no;
           Meta& me = meta[t & (kMeta - 1)];
           if (o.n == kEnd) {
-            ++marks;
+            ended = true;
             if (mine && lane == 0) me.end = 1;
           } else if (mine) {
             const int n = o.n;
@@ -774,7 +785,7 @@ tree_tc(const __grid_constant__ TreeArgs a, const __grid_constant__ CUtensorMap 
     }
   } else {
     // ------------------------------------------------------------------ softmax --
-    more_registers();
+    more_registers<NT>();
     const int wg = warp >> 2, r = (warp & 3) * 32 + lane;  // warpgroup; row = TMEM lane
     const uint32_t lane_off = (uint32_t)((warp & 3) * 32) << 16;
     const uint32_t tO = tmem + lane_off + kSBuf * kTile + wg * 128;
@@ -782,7 +793,7 @@ tree_tc(const __grid_constant__ TreeArgs a, const __grid_constant__ CUtensorMap 
     // far inside fp32 (bf16 P has its exponents), or what fp16 holds.
     constexpr float kSumCap = B16 ? 1.8446744e19f : 32768.0f;
     constexpr float kTop = B16 ? 0.0f : 7.0f;  // log2 of the largest weight when m is set
-    int t = NT == 1 ? wg : 0, c = wg, seg = 0;
+    int t = 0, c = wg, seg = 0;  // tiles with end marks, products, segments
     // pairs: parities of the next S of this warpgroup, and of the P V of its two P tiles
     uint32_t s_par = 0u, pv_par = 0u;
     bool ok = true;
@@ -795,16 +806,16 @@ tree_tc(const __grid_constant__ TreeArgs a, const __grid_constant__ CUtensorMap 
       // a row that is no token sees nothing: its reference need not be looked for
       float m = alive ? -INFINITY : 0.0f, l = 0.0f, fac = a.sl2;
       const int c0 = c;
-      // This warpgroup's last product P V (that of tile t - 1, or c - 2) is done.
+      // This warpgroup's last product P V (that of tile t - 1) is done.
       auto pv_done = [&]() {
         if constexpr (L::PAIR) {
           const int at = (t - 1) & 1;  // (its bit was turned when its P was handed over)
           return wait_all(b_pv + 8 * (2 * wg + at), (pv_par >> at & 1u) ^ 1u);
         } else {
-          return wait_all(b_pv + 8 * ((c - 2) % kSBuf), (c - 2) / kSBuf);
+          return wait_all(b_pv + 8 * ((c - NT) % kSBuf), (c - NT) / kSBuf);
         }
       };
-      for (;; t += NT == 1 ? 2 : 1, c += 2) {
+      for (;; ++t, c += NT) {
         const Meta& me = meta[t & (kMeta - 1)];
         if (!(ok = wait_all(b_meta + 8 * (t & (kMeta - 1)), t / kMeta))) return;
         if (me.end) break;
@@ -976,9 +987,8 @@ tree_tc(const __grid_constant__ TreeArgs a, const __grid_constant__ CUtensorMap 
         if (!(ok = pv_done())) return;
         tc_fence_after();
       }
-      t += MARKS;  // the end mark
-      // NT = 1: two partials of 128 rows; NT = 2: one of 256
-      const int64_t slot = (partial * 2 + wg) * kRows + r;
+      ++t;  // the end mark
+      const int64_t slot = (partial * NT + wg) * kRows + r;
       if (on) a.part_ml[slot] = make_float2(m, some ? l : 0.0f);
       if (some) {
 #pragma unroll
