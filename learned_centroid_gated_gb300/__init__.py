@@ -584,7 +584,7 @@ def rope(plan: Rope, q: torch.Tensor, k: torch.Tensor | None = None, *, position
     """Rotary positions of q [B, N, H, d] and, in the same launch, k [B, N, H_kv, d] (bf16,
     fp16 or fp32; strided views with consecutive columns are fine).  Token n stands at
     offset + n, or at positions[b, n] (int32).  out / out_k may be q / k themselves.
-    Returns the rotated q, or (q, k)."""
+    An input may be a broadcast view, an output not.  Returns the rotated q, or (q, k)."""
     return _rope_call("focus_rope_apply", plan, q, k, positions, offset, out, out_k, 0, stream)
 
 
@@ -683,7 +683,8 @@ def cache_write(p: CacheParams, cache: KVCache, k: torch.Tensor, v: torch.Tensor
     token t < count[b] goes to slot start[b] + t (int32 device tensors; count None: all T),
     its key rotated by `rope` at positions[b, t], or at its slot.  status: an int32 device
     word that get_status reads (FOCUS_ERR_BOUNDS when a token had no slot).  A tree's accepted
-    path is committed by writing its tokens again from start on, in order."""
+    path is committed by writing its tokens again from start on, in order.  k and v are no
+    views of the cache."""
     what = "focus_cache_write"
     dev, kc, vc, ksc, vsc, mc = cache._args(p, what)
     _require(k.dim() == 4 and start is not None, what)
@@ -735,7 +736,9 @@ def decode_tree(p: CacheParams, q: torch.Tensor, cache: KVCache, lens: torch.Ten
     int32 tokens in the cache before them; the drafted tokens' own keys, values and masks stand
     in slots lens[b] + u.  tree [B, T] int64: bit u of word t set when drafted token u is an
     ancestor of t or t itself (None: a chain; a word of 0 marks a row that is no token).
-    T = 1 is the plain next token of sequences of different lengths.
+    T = 1 is the plain next token of sequences of different lengths.  ws: a workspace of
+    decode_tree_workspace_size(p, T) bytes, of one call at a time; get_status(ws) reads the
+    call's status (FOCUS_ERR_BOUNDS where a length does not fit).
     Returns (o [B, T, H, d] bf16, lse [B, H, T] fp32)."""
     what = "focus_decode_tree"
     dev, kc, vc, ksc, vsc, mc = cache._args(p, what)

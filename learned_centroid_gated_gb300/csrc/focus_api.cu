@@ -631,6 +631,19 @@ focus_strides dense(int N, int H, int d) {
   return focus_strides{(int64_t)N * H * d, (int64_t)H * d, (int64_t)d};
 }
 
+// Bytes from a tensor's first element to behind its last, strides in elements.
+int64_t span(int B, int N, int H, int d, const focus_strides& s, int size) {
+  return ((B - 1) * s.b + (N - 1) * s.n + (H - 1) * s.h + d) * size;
+}
+bool overlap(const void* a, int64_t na, const void* b, int64_t nb) {
+  const uintptr_t x = (uintptr_t)a, y = (uintptr_t)b;
+  return x < y + (uintptr_t)nb && y < x + (uintptr_t)na;
+}
+// An output whose rows share elements (an expanded view) would be written twice.
+bool broadcast(int B, int N, int H, const focus_strides& s) {
+  return (B > 1 && s.b == 0) || (N > 1 && s.n == 0) || (H > 1 && s.h == 0);
+}
+
 // Shape checks shared by the cache's entry points (host only).
 int check_cache_params(const focus_cache_params* p) {
   if (!p) return FOCUS_ERR_INVALID_ARG;
@@ -657,6 +670,10 @@ int check_cache_ptrs(const focus_cache_params* p, const void* kc, const void* vc
   if (!aligned(kc, 16) || !aligned(vc, 16) || !aligned(ks, 4) || !aligned(vs, 4))
     return FOCUS_ERR_ALIGNMENT;
   return FOCUS_OK;
+}
+
+int64_t cache_bytes(const focus_cache_params* p) {
+  return (int64_t)p->B * p->cap * p->H_kv * p->d_head * (p->format == FOCUS_CACHE_BF16 ? 2 : 1);
 }
 
 int check_draft_params(const focus_cache_params* p) {
@@ -695,6 +712,8 @@ int focus_rope_apply(const focus_rope* rope, int32_t dtype, int32_t B, int32_t N
   // a grid of one warp per token and part of its heads
   if ((double)B * N >= 8.0 * INT32_MAX) return FOCUS_ERR_UNSUPPORTED;
   const focus_strides dq = dense(N, H, d_head), dk = dense(N, hk, d_head);
+  if (broadcast(B, N, H, qos ? *qos : dq) || (k && broadcast(B, N, hk, kos ? *kos : dk)))
+    return FOCUS_ERR_INVALID_ARG;
   return cuda_rc(launch_rope(*rope, dtype, B, N, H, hk, d_head, q, qs ? *qs : dq, k, ks ? *ks : dk,
                              positions, offset, inverse != 0, q_out, qos ? *qos : dq, k_out,
                              kos ? *kos : dk, (cudaStream_t)stream));
@@ -716,6 +735,12 @@ int focus_cache_write(const focus_cache_params* p, const uint16_t* k, const focu
       !aligned(mask, 4) || !aligned(mask_cache, 4) || !aligned(start, 4) || !aligned(count, 4) ||
       !aligned(positions, 4) || !aligned(status, 4))
     return FOCUS_ERR_ALIGNMENT;
+  // rows leave for other slots while others are still read
+  const int64_t cache = cache_bytes(p), nk = span(p->B, p->T, p->H_kv, p->d_head, sk, 2),
+                nv = span(p->B, p->T, p->H_kv, p->d_head, sv, 2);
+  if (overlap(k_cache, cache, v_cache, cache) || overlap(k, nk, k_cache, cache) || overlap(k, nk, v_cache, cache) ||
+      overlap(v, nv, k_cache, cache) || overlap(v, nv, v_cache, cache))
+    return FOCUS_ERR_INVALID_ARG;
   return cuda_rc(launch_cache_write(*p, k, sk, v, sv, mask, start, count, rope, positions, k_cache,
                                     v_cache, k_scale, v_scale, mask_cache, status,
                                     (cudaStream_t)stream));
@@ -731,6 +756,10 @@ int focus_cache_read(const focus_cache_params* p, const void* k_cache, const voi
   if (!aligned(k, 16) || !aligned(v, 16) || !aligned(start, 4) || !aligned(count, 4) ||
       !aligned(status, 4))
     return FOCUS_ERR_ALIGNMENT;
+  const int64_t cache = cache_bytes(p), n = (int64_t)p->B * p->T * p->H_kv * p->d_head * 2;
+  if (overlap(k, n, v, n) || overlap(k, n, k_cache, cache) || overlap(k, n, v_cache, cache) ||
+      overlap(v, n, k_cache, cache) || overlap(v, n, v_cache, cache))
+    return FOCUS_ERR_INVALID_ARG;
   return cuda_rc(launch_cache_read(*p, k_cache, v_cache, k_scale, v_scale, start, count, k, v, status,
                                    (cudaStream_t)stream));
 }
@@ -754,6 +783,9 @@ int focus_decode_tree(const focus_cache_params* p, const uint16_t* q, const void
   if (!ws) return FOCUS_ERR_INVALID_ARG;
   if (!aligned(ws, 256)) return FOCUS_ERR_ALIGNMENT;
   if (ws_bytes < tree_workspace_bytes(*p)) return FOCUS_ERR_WORKSPACE;
+  // (q is read again, for rows that come out not finite, while other rows of o are written)
+  const int64_t n = (int64_t)p->B * p->T * p->H * p->d_head * 2;
+  if (overlap(q, n, o, n)) return FOCUS_ERR_INVALID_ARG;
   const float scale = p->softmax_scale > 0.0f ? p->softmax_scale : 1.0f / sqrtf((float)p->d_head);
   return cuda_rc(launch_decode_tree(*p, reinterpret_cast<const bf16*>(q), k_cache, v_cache, k_scale,
                                     v_scale, mask_cache, lens, tree, reinterpret_cast<bf16*>(o), lse,

@@ -29,7 +29,7 @@ struct TreeArgs {
   float* lse;
   int32_t* status;
   int B, cap, T, H, H_kv, R, w, gq, rows;
-  int grp, nrg;      // rows per row group (16, or 128 or 256 on the tensor cores), row groups
+  int grp, nrg;      // rows per row group (8 or 16, or 128 or 256 in tree_tc), row groups
   int G;             // slices at most
   int wfar;
   int tma;           // tensor-core kernel: tensor maps are there
@@ -204,7 +204,7 @@ __device__ __forceinline__ void codes_f16x2(uint32_t four, uint32_t& lo, uint32_
 // stays as it is (its results are NaN either way).
 __device__ __forceinline__ void row_unit(float largest, float& up, float& down) {
   uint32_t ex = __float_as_uint(largest) >> 23;
-  ex = ex == 0u || ex >= 254u ? 127u : ex;
+  ex = ex == 255u ? 127u : min(max(ex, 1u), 253u);  // (both powers are normal numbers)
   up = __uint_as_float((254u - ex) << 23);
   down = __uint_as_float(ex << 23);
 }

@@ -164,3 +164,28 @@ def test_reference_pins():
         y, _ = ref.rotate(x, pos, 48, layout)
         z, _ = ref.rotate(y, pos, 48, layout, inverse=True)
         assert (z - x.double()).abs().max() <= 1e-12 and (y - x.double()).abs().max() > 1
+
+
+@host_only
+def test_overlaps_are_refused():
+    """Outputs that share memory with what is still read, or with themselves."""
+    bad = E["FOCUS_ERR_INVALID_ARG"]
+    at = lambda i: P((1 << 12) + (i << 24))
+    size = 2 * 64 * 2 * 128 * 2  # the cache's bytes
+    free = dict(k=at(1), v=at(2), kc=at(3), vc=at(4), mc=at(5), mask=at(6), start=at(7))
+    assert _write(_cp(), **{**free, "vc": free["kc"]}) == bad
+    for x in ("k", "v"):
+        for y in ("kc", "vc"):
+            last = P(free[y].value + size - 256)
+            assert _write(_cp(), **{**free, x: free[y]}) == _write(_cp(), **{**free, x: last}) == bad, (x, y)
+
+    def read(kc, vc, k, v):
+        return focus._lib.focus_cache_read(ctypes.byref(_cp()), kc, vc, None, None, None, None, k, v, None, None)
+    assert read(at(1), at(2), at(3), at(3)) == read(at(1), at(2), at(1), at(3)) == read(at(1), at(2), at(3), at(2)) == bad
+    assert _decode(_cp(), q=at(1), o=at(1), kc=at(2), vc=at(3)) == bad
+    assert _decode(_cp(), q=at(1), o=P(at(1).value + 256), kc=at(2), vc=at(3)) == bad
+    plan = focus.Rope(dim=64)._plan
+    for st in ((0, 256, 128), (1024, 0, 128), (1024, 256, 0)):
+        rc = focus._lib.focus_rope_apply(ctypes.addressof(plan), 0, 2, 4, 2, 0, 128, at(1), None, None, None, None, 0, 0,
+                                         at(2), ctypes.byref(focus._Strides(*st)), None, None, None)
+        assert rc == bad, st

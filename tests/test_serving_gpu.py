@@ -498,6 +498,67 @@ def test_decode_tree_logits_that_grow_and_fall():
             check_tree(p, c, q, lens, words, o, lse, fmt)
 
 
+@pytest.mark.parametrize("fmt", ["e4m3", "int8"])
+@pytest.mark.parametrize("name,big", [("one_token", False), ("chain5", False), ("tree16", True)])
+def test_decode_tree_queries_at_the_ends_of_the_range(name, big, fmt):
+    """Queries near the largest and below the smallest normal bf16 number, against key scales
+    that bring the logits back: rows are scaled by powers of two, exactly."""
+    for e in (126, -127):
+        p, c, q, T, lens, words, is_tree = tree_case(name, fmt, seed=8, big=big)
+        q = (q.double().clamp(-3.9, 3.9) * 2.0 ** e).to(torch.bfloat16)
+        half = 2.0 ** (-60 if e > 0 else 60)
+        c.k_scale.mul_(half)
+        p = dataclasses.replace(p, softmax_scale=2.0 ** -e / half / math.sqrt(p.d_head))
+        tree = torch.tensor(ref.signed(words), dtype=torch.int64, device="cuda") if is_tree else None
+        o, lse = focus.decode_tree(p, q.cuda(), c, torch.tensor(lens, dtype=torch.int32, device="cuda"), tree)
+        check_tree(p, c, q, lens, words, o, lse, fmt)
+
+
+def test_decode_tree_of_queries_that_are_not_finite():
+    """A NaN or an infinity in a query shows in its own row only."""
+    for name, big in (("one_token", False), ("chain5", False), ("tree16", True), ("rows_300", True)):
+        for fmt in ("bf16", "int8"):
+            p, c, q, T, lens, words, is_tree = tree_case(name, fmt, seed=9, big=big)
+            tree = torch.tensor(ref.signed(words), dtype=torch.int64, device="cuda") if is_tree else None
+            n = torch.tensor(lens, dtype=torch.int32, device="cuda")
+            want, want_lse = focus.decode_tree(p, q.cuda(), c, n, tree)
+            hit = torch.zeros(q.shape[:3], dtype=torch.bool)
+            for i, value in enumerate((math.nan, math.inf, -math.inf)):
+                q[0, (3 * i) % T, i % p.H, 7] = value
+                hit[0, (3 * i) % T, i % p.H] = True
+            got, lse = focus.decode_tree(p, q.cuda(), c, n, tree)
+            assert torch.equal(got.cpu()[~hit], want.cpu()[~hit])
+            assert torch.equal(lse.transpose(1, 2).cpu()[~hit], want_lse.transpose(1, 2).cpu()[~hit])
+            assert bool(got.cpu()[hit].isnan().all(-1).any())
+
+
+def test_rotation_of_broadcast_views():
+    """One key head shown to all, as an expanded view: like its copies.  Outputs that share
+    elements are refused."""
+    plan = focus.Rope(dim=64)
+    q, one = randn(2, 5, 4, 128, seed=1).cuda(), randn(2, 5, 1, 128, seed=2).cuda()
+    k = one.expand(2, 5, 4, 128)
+    want, got = focus.rope(plan, q, k.contiguous()), focus.rope(plan, q, k)
+    assert torch.equal(want[0], got[0]) and torch.equal(want[1], got[1])
+    with pytest.raises(focus.FocusError):
+        focus.rope(plan, q, k, out_k=k)
+    with pytest.raises(focus.FocusError):
+        focus.rope(plan, q, out=one.expand(2, 5, 4, 128))
+
+
+def test_calls_whose_tensors_overlap_are_refused():
+    p = cache_params(B=1, cap=40)
+    c = focus.KVCache.empty(p)
+    n = torch.zeros(1, dtype=torch.int32, device="cuda")
+    with pytest.raises(focus.FocusError):
+        focus.cache_write(p, c, c.k[:, 3:6], c.v[:, 3:6], None, n)
+    with pytest.raises(focus.FocusError):
+        focus.cache_read(p, c, 3, out=(c.k[:, :3], c.v[:, :3]))
+    q = randn(1, 2, p.H, p.d_head).cuda()
+    with pytest.raises(focus.FocusError):
+        focus.decode_tree(p, q, c, n, out=q)
+
+
 def test_decode_tree_refuses_lengths_outside_the_cache():
     p, c, q, T, lens, words, _ = tree_case("ragged_40", "int8")
     n = torch.tensor(lens, dtype=torch.int32)
