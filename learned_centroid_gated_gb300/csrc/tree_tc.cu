@@ -5,22 +5,32 @@
 // Up to 256 rows share a K/V row that is read once: at most 4 d x 256 flops for 4 d bytes
 // (bf16), about the balance of the tensor cores and the memory, so the K/V stream has to
 // stay the bound.  One CTA per SM takes a slice and works through its segments with
-//   warps 8-11  (loaders) list the keys that any row sees and bring their K and V rows, 64
-//               keys a tile: 64 consecutive keys by TMA, others row by row with 16-byte
-//               asynchronous copies.  bf16 rows go straight into the 128-byte-swizzled
-//               operand tiles; 8-bit codes into a staging ring, whence the loaders turn them
-//               into fp16 operands (exact).
+//   loader warps   list the keys that any row sees and bring their K and V rows, 64 keys a
+//               tile: 64 consecutive keys by TMA, others row by row with 16-byte asynchronous
+//               copies.  bf16 rows go straight into the 128-byte-swizzled operand tiles;
+//               8-bit codes into a staging ring, whence the loaders turn them into fp16
+//               operands (exact).
 //   warp 12     issues the products: S = Q K^T (both operands in shared memory) into tensor
 //               memory, and O += P V with P read from tensor memory.  It takes whichever is
 //               ready.  An MMA costs its issuer about 75 cycles however narrow it is, so
 //               where both row halves use a tile (256 rows, bf16) S is made for two tiles at
-//               once (N = 128): 1.46 -> %s ms for 64 tokens behind a million.
+//               once (N = 128) and the products follow a fixed order: 1.46 -> 1.20 ms for 64
+//               tokens behind a million.
 //   warps 13-15 (readers) take the tiles in turn and work out which key each drafted token
 //               sees, as one 64-bit word per token, and bring the scales of 8-bit rows.
-//   warps 0-7   the softmax of a product, a thread per row, in two warpgroups.  With up to
-//               128 rows (NT = 1) they take the tiles in turn, each with a reference, a sum
-//               and an O of its own (two partial results per segment); with more (NT = 2)
-//               each takes 128 rows of every tile, and the K/V tile serves both.
+//   softmax warps   a thread per row.  More than 128 rows (NT = 2): two warpgroups, each with
+//               128 rows of every tile, and four loader warps.  Up to 128 (NT = 1): one
+//               warpgroup, and eight loader warps, since the codes' conversion, not the
+//               softmax, is the longer chain (64 rows over 128K int8 keys: 158 us with two
+//               softmax warpgroups by turns and four loader warps, 141 so; bf16 114 and 117).
+// Measured: 64 drafts of 32 / 8 heads over a million bf16 keys 1.19 ms, 3.4 TB/s and 0.88
+// PFLOP/s (the products alone would take 0.53 ms at the peak rate); 16 drafts over 128K keys
+// 117 us bf16 (4.6 TB/s), 141 us int8 (2.0 TB/s).  What bounds it: with 256 rows the thread
+// that issues the MMAs; with fewer rows the softmax warps' instructions (1800 cycles a tile of
+// int8, 1200 of bf16, against 740 and 1400 that its bytes take); 8-bit codes cost the
+// conversion and the scales on top, so that they save less time than bytes.
+// The roles' loops share the instruction cache: the code is kept short rather than unrolled
+// (the conversion's loop unrolled by 4: 157 -> 172 us, by 2 the least).
 // The scales of 8-bit rows: K's multiplies the logits; V's multiplies P, and the reference of
 // the exponentials is that of the product, which is what fp16 has to hold.
 // Every wait is bounded; a wait that runs out raises FOCUS_ERR_TIMEOUT.
@@ -133,8 +143,9 @@ __host__ __device__ constexpr uint32_t idesc_f16(int M, int N, int b_mn_major) {
   return (1u << 4) | ((uint32_t)b_mn_major << 16) | ((uint32_t)(N >> 3) << 17) | ((uint32_t)(M >> 4) << 24);
 }
 
-// Registers: 512 threads launch with 128 each; the two softmax warpgroups take 152, the
-// loaders and the last warpgroup keep 104 (2 x 152 + 2 x 104 = 4 x 128).
+// Registers: 512 threads launch with 128 each; the loaders and the last warpgroup keep 104, the
+// softmax takes what that leaves: 152 in each of two warpgroups, or 200 in one
+// (2 x 152 + 2 x 104 = 200 + 3 x 104 = 4 x 128).
 template <int NT>
 __device__ __forceinline__ void more_registers() {
   if constexpr (NT == 1) asm volatile("setmaxnreg.inc.sync.aligned.u32 200;");
@@ -319,9 +330,12 @@ tree_tc(const __grid_constant__ TreeArgs a, const __grid_constant__ CUtensorMap 
           mw[i] = j < je ? __ldg(M + j) : 0u;
         }
       };
-      // Appends the keys of the next SCAN that some row sees to the list, in order.  Where
-      // three quarters of them are seen all are listed: 64 keys in a row come by TMA, which
-      // costs less than leaving a quarter out.
+      // Appends the keys of the next SCAN that some row sees to the list, in order.  bf16: where
+      // three quarters of them are seen all are listed, since 64 keys in a row come by TMA,
+      // which costs less than leaving a quarter out (128K keys of which 0.66, 0.74 and 0.88 are
+      // seen: 113, 130 and 129 us without the rest, 116, 116 and 116 with it).  Codes are half
+      // the bytes, and each key has a conversion: the rest stays out (117, 140 and 141 us
+      // against 142, 141 and 141).
       auto scan = [&]() {
         unsigned bal[MW];
         int mine = 0;
@@ -344,7 +358,7 @@ tree_tc(const __grid_constant__ TreeArgs a, const __grid_constant__ CUtensorMap 
           all += n;
           at += i < lw ? n : 0;
         }
-        if (jb + kScan <= min(len, je) && 4 * all >= 3 * kScan) {
+        if (B16 && jb + kScan <= min(len, je) && 4 * all >= 3 * kScan) {
           all = kScan;
           at = head + 32 * MW * lw;
 #pragma unroll
