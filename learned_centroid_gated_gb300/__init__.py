@@ -753,7 +753,7 @@ def decode_tree(p: CacheParams, q: torch.Tensor, cache: KVCache, lens: torch.Ten
         out = torch.empty_like(q) if out is None else out
         if lse is None and want_lse:
             lse = torch.empty((p.B, p.H, T), dtype=torch.float32, device=q.device)
-        ws = q.new_empty((c.tree_ws + 1) // 2) if ws is None else ws  # (bytes, in the type at hand)
+        ws = torch.empty(c.tree_ws, dtype=torch.uint8, device=q.device) if ws is None else ws
         _require(ws.get_device() == dev and ws.is_contiguous(), what)
         _check(_lib.focus_decode_tree(
             c.addr, qp, kc, vc, ksc, vsc, mc, _vector(lens, (p.B,), dev, what),

@@ -6,10 +6,10 @@
 // (int8).  Memory-bound: each bf16 row is read once, its codes written once.  A warp takes
 // one token: a key's cosines and sines are computed once and serve all KV heads, the row
 // maximum is a shuffle over the row's D / 16 lanes, and the codes leave from registers.
-// Measured, 8 KV heads of 128: 32K tokens of 4 sequences in e4m3 with rotation, 136 us (6.0
-// TB/s; the instructions, 0.59 of the issue slots, come next after the memory); 128K tokens of
-// bf16 read back, 115 us (7.1 TB/s); one token of each of 32 sequences, 4.2 us, which is the
-// launch and three dependent reads.
+// Measured, e4m3, d = 128: 32K tokens of 32 KV heads written with rotation, 136 us (6.0 TB/s;
+// after the memory come the instructions, 0.59 of the issue slots); 128K tokens of 8 KV heads
+// read back, 116 us (7.0 TB/s); one token of each of 32 sequences, 4.2 us, which is the launch
+// and three dependent reads.
 #include <cuda_fp8.h>
 #include <math.h>
 

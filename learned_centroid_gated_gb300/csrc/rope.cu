@@ -6,7 +6,9 @@
 // is read once and written once.  The cosines and sines depend on the token only, so a
 // warp takes one token, computes them once into registers and applies them to that
 // token's heads, queries and keys in one launch.
-// Measured: @@ROPE@@
+// Measured: bf16, d = 128: 32K tokens of 32 + 32 heads out of a packed projection 154 us (7.0
+// TB/s), the gradients of 128K tokens of 32 + 8 heads 379 us (7.1 TB/s); 16 tokens 3.7 us (the
+// launch, the angles and one trip to memory).
 #include <math.h>
 
 #include "rope.cuh"
