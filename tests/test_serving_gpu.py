@@ -282,6 +282,33 @@ def test_cache_rows_of_zeros_tiny_and_not_finite_values():
         assert err.max().item() <= (2.0 ** -4 if fmt == "e4m3" else 0.5 / 127) + 2.0 ** -8
 
 
+@pytest.mark.parametrize("fmt", ["bf16", "e4m3", "int8"])
+@pytest.mark.parametrize("H_kv,d", [(1, 64), (1, 128), (2, 64), (3, 64), (2, 128), (7, 64)])
+def test_cache_of_few_heads_and_many_tokens(fmt, H_kv, d):
+    """The same bits as head by head in a cache of many heads, where a warp takes one token."""
+    B, T, wide = 3, 1201, 16
+    p = cache_params(B=B, cap=T + 30, H=H_kv, H_kv=H_kv, d_head=d, K=8, R=H_kv, format=fmt)
+    pw = dataclasses.replace(p, H=wide, H_kv=wide, R=1)
+    k, v = randn(B, T, H_kv, d, seed=1).cuda(), randn(B, T, H_kv, d, seed=2).cuda()
+    mask = random_masks(3, 8, 2, B, H_kv, T).cuda()
+    i32 = dict(dtype=torch.int32, device="cuda")
+    start, count = torch.tensor([0, 29, 7], **i32), torch.tensor([T, T, 600], **i32)
+    c, cw = focus.KVCache.empty(p), focus.KVCache.empty(pw)
+    plan = focus.Rope(dim=d)
+    rep = lambda x: torch.nn.functional.pad(x, (0, 0, 0, wide - H_kv))
+    focus.cache_write(p, c, k, v, mask, start, count, rope=plan)
+    focus.cache_write(pw, cw, rep(k), rep(v), None, start, count, rope=plan)
+    assert torch.equal(raw(c.k), raw(cw.k)[:, :, :H_kv]) and torch.equal(raw(c.v), raw(cw.v)[:, :, :H_kv])
+    if fmt != "bf16":
+        assert torch.equal(c.k_scale, cw.k_scale[:, :H_kv]) and torch.equal(c.v_scale, cw.v_scale[:, :H_kv])
+    for b, (s, n) in enumerate(((0, T), (29, T), (7, 600))):
+        assert torch.equal(c.mask[b, :, s:s + n], mask[b, :, :n])
+        assert not bool(c.mask[b, :, :s].any()) and not bool(c.mask[b, :, s + n:].any())
+    for x, y in zip(focus.cache_read(p, c, T, start, count), focus.cache_read(pw, cw, T, start, count)):
+        assert torch.equal(x, y[:, :, :H_kv])
+        assert bool((x[2, 600:] == 0).all())
+
+
 def test_cache_slots_outside_are_reported_and_not_touched():
     """Device-side refusals: tokens without a slot and counts outside [0, T] set the status
     word; nothing outside [start, start + count) changes, reads give zeros."""
