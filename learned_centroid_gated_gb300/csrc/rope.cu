@@ -25,6 +25,7 @@ struct RopeArgs {
   int64_t offset, tokens;  // tokens = B * N
   int N, H, heads;         // heads = H + H_kv
   int splits, per;         // warps per token, heads of each
+  int lanes_of;            // several tokens per warp: groups of lanes of a token
   float sign;              // +1 forward, -1 backward
 };
 
@@ -46,18 +47,20 @@ __device__ __forceinline__ void row_of(const RopeArgs& a, int64_t b, int64_t n, 
 //   HALF (dim a multiple of 2 V): lane c < P = dim / 2 / V holds chunks c and c + P, the
 //     two halves of its V pairs; the lanes behind hold two chunks that are copied.
 //   INTERLEAVED: chunks c and c + D / (2 V), V / 2 pairs each.
-template <typename T, int D, bool HALF>
+// FEW: fewer heads than a warp's RPW rows.  A warp then takes U times RPW / a.lanes_of tokens, a
+// lane's group one row of each.  400K bf16 tokens of 1 + 1 heads of 64: 197 us with a warp per
+// token, 65 so; of 128: 264 and 131; 3000 tokens, where latency counts: 3.9 and 4.4.
+template <typename T, int D, bool HALF, bool FEW>
 __global__ void __launch_bounds__(256) rope_rows(const __grid_constant__ RopeArgs a) {
   using C = RowChunk<T>;
   constexpr int V = C::V, LPR = D / (2 * V), RPW = 32 / LPR;
   constexpr int U = 2;  // head groups whose loads are in flight together
   const int64_t warp = (int64_t)blockIdx.x * (blockDim.x >> 5) + (threadIdx.x >> 5);
-  const int64_t tk = warp / a.splits;
-  if (tk >= a.tokens) return;
-  const int sp = (int)(warp - tk * a.splits);
   const int lane = threadIdx.x & 31, c = lane % LPR, sub = lane / LPR;
+  const int64_t tk = FEW ? 0 : warp / a.splits;
+  if (!FEW && tk >= a.tokens) return;
+  const int sp = FEW ? 0 : (int)(warp - tk * a.splits);
   const int64_t b = tk / a.N, n = tk - b * a.N;
-  const int64_t pos = a.positions ? (int64_t)__ldg(a.positions + tk) : a.offset + n;
   const int np = a.rope.dim / 2, P = np / V;
   const bool turned = HALF ? c < P : true;
   const int ca = HALF ? (turned ? c : 2 * P + 2 * (c - P)) : c;
@@ -65,12 +68,65 @@ __global__ void __launch_bounds__(256) rope_rows(const __grid_constant__ RopeArg
   float cs[V], sn[V];
   bool rot[V];
   auto pair = [&](int e) { return HALF ? c * V + e : (e < V / 2 ? ca * (V / 2) + e : cb * (V / 2) + e - V / 2); };
+#pragma unroll
+  for (int e = 0; e < V; ++e) rot[e] = pair(e) < np;
+  // Both chunks of a row turned (where they are).
+  auto turn = [&](uint4& xa, uint4& xb) {
+    if (!turned) return;
+    float fa[V], fb[V];
+    C::unpack(xa, fa);
+    C::unpack(xb, fb);
+    if constexpr (HALF) {
+#pragma unroll
+      for (int e = 0; e < V; ++e) rope_turn(fa[e], fb[e], cs[e], sn[e]);
+    } else {
+#pragma unroll
+      for (int e = 0; e < V / 2; ++e) {
+        if (rot[e]) rope_turn(fa[2 * e], fa[2 * e + 1], cs[e], sn[e]);
+        if (rot[e + V / 2]) rope_turn(fb[2 * e], fb[2 * e + 1], cs[e + V / 2], sn[e + V / 2]);
+      }
+    }
+    xa = C::pack(fa);
+    xb = C::pack(fb);
+  };
+  if constexpr (FEW) {
+    const int tpw = RPW / a.lanes_of, h = sub & (a.lanes_of - 1);
+    uint4 xa[U], xb[U];
+    T* y[U];
+    int64_t at[U];
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int64_t k = (warp * U + u) * tpw + sub / a.lanes_of;
+      y[u] = nullptr;
+      at[u] = 0;
+      if (k < a.tokens && h < a.heads) {
+        const int64_t kb = k / a.N, kn = k - kb * a.N;
+        const T* x;
+        row_of<T>(a, kb, kn, h, x, y[u]);
+        xa[u] = *reinterpret_cast<const uint4*>(x + ca * V);
+        xb[u] = *reinterpret_cast<const uint4*>(x + cb * V);
+        at[u] = a.positions ? (int64_t)__ldg(a.positions + k) : a.offset + kn;
+      }
+    }
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      if (!y[u]) continue;
+#pragma unroll
+      for (int e = 0; e < V; ++e) {
+        cs[e] = 1.0f, sn[e] = 0.0f;
+        if (rot[e]) rope_angle(at[u], a.rope.turn[pair(e)], a.rope.attn_factor, cs[e], sn[e]);
+        sn[e] *= a.sign;
+      }
+      turn(xa[u], xb[u]);
+      *reinterpret_cast<uint4*>(y[u] + ca * V) = xa[u];
+      *reinterpret_cast<uint4*>(y[u] + cb * V) = xb[u];
+    }
+    return;
+  }
+  const int64_t pos = a.positions ? (int64_t)__ldg(a.positions + tk) : a.offset + n;
   rope_angles<V, LPR>(a.rope, pos, lane, pair, cs, sn);
 #pragma unroll
-  for (int e = 0; e < V; ++e) {
-    rot[e] = pair(e) < np;
-    sn[e] *= a.sign;
-  }
+  for (int e = 0; e < V; ++e) sn[e] *= a.sign;
   const int h1 = min(a.heads, (sp + 1) * a.per);
   for (int h0 = sp * a.per + sub; h0 < h1; h0 += U * RPW) {
     uint4 xa[U], xb[U];
@@ -87,23 +143,7 @@ __global__ void __launch_bounds__(256) rope_rows(const __grid_constant__ RopeArg
 #pragma unroll
     for (int u = 0; u < U; ++u) {
       if (h0 + u * RPW >= h1) continue;
-      if (turned) {
-        float fa[V], fb[V];
-        C::unpack(xa[u], fa);
-        C::unpack(xb[u], fb);
-        if constexpr (HALF) {
-#pragma unroll
-          for (int e = 0; e < V; ++e) rope_turn(fa[e], fb[e], cs[e], sn[e]);
-        } else {
-#pragma unroll
-          for (int e = 0; e < V / 2; ++e) {
-            if (rot[e]) rope_turn(fa[2 * e], fa[2 * e + 1], cs[e], sn[e]);
-            if (rot[e + V / 2]) rope_turn(fb[2 * e], fb[2 * e + 1], cs[e + V / 2], sn[e + V / 2]);
-          }
-        }
-        xa[u] = C::pack(fa);
-        xb[u] = C::pack(fb);
-      }
+      turn(xa[u], xb[u]);
       *reinterpret_cast<uint4*>(y[u] + ca * V) = xa[u];
       *reinterpret_cast<uint4*>(y[u] + cb * V) = xb[u];
     }
@@ -175,6 +215,16 @@ constexpr int kRopeWarps = 2432;  // warps that fill the GPU: 16 per SM on 152 S
 template <typename T, int D>
 cudaError_t launch(RopeArgs& a, bool chunks, cudaStream_t s) {
   constexpr int V = RowChunk<T>::V, RPW = 64 * V / D;
+  const bool half = a.rope.layout == FOCUS_ROPE_HALF;
+  a.lanes_of = 1;
+  while (a.lanes_of < a.heads && a.lanes_of < RPW) a.lanes_of *= 2;
+  if (chunks && a.lanes_of < RPW && a.tokens > 2 * kRopeWarps) {
+    const int64_t per = 8 * 2 * (RPW / a.lanes_of), blocks = (a.tokens + per - 1) / per;  // tokens of a block
+    if (blocks > INT32_MAX) return cudaErrorInvalidConfiguration;
+    if (half) rope_rows<T, D, true, true><<<(unsigned)blocks, 256, 0, s>>>(a);
+    else rope_rows<T, D, false, true><<<(unsigned)blocks, 256, 0, s>>>(a);
+    return cudaGetLastError();
+  }
   // few tokens: several warps share a token's heads, each computing the angles anew (16 tokens of
   // 40 heads: 3.7 us, with one warp per token 7.1)
   const int step = chunks ? RPW : 1;
@@ -188,10 +238,10 @@ cudaError_t launch(RopeArgs& a, bool chunks, cudaStream_t s) {
   const unsigned g = (unsigned)blocks;
   if (!chunks)
     rope_elems<T, D><<<g, 256, 0, s>>>(a);
-  else if (a.rope.layout == FOCUS_ROPE_HALF)
-    rope_rows<T, D, true><<<g, 256, 0, s>>>(a);
+  else if (half)
+    rope_rows<T, D, true, false><<<g, 256, 0, s>>>(a);
   else
-    rope_rows<T, D, false><<<g, 256, 0, s>>>(a);
+    rope_rows<T, D, false, false><<<g, 256, 0, s>>>(a);
   return cudaGetLastError();
 }
 

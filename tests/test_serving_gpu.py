@@ -559,6 +559,24 @@ def test_decode_tree_of_queries_that_are_not_finite():
             assert bool(got.cpu()[hit].isnan().all(-1).any())
 
 
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16, torch.float32])
+@pytest.mark.parametrize("layout", ["half", "interleaved"])
+@pytest.mark.parametrize("H,H_kv,d", [(1, 0, 64), (1, 1, 64), (2, 1, 64), (1, 0, 128), (1, 1, 128), (3, 2, 64)])
+def test_rotation_of_few_heads_and_many_tokens(H, H_kv, d, layout, dtype):
+    """The same bits as in a call of many heads, where a warp takes one token."""
+    B, N = 3, 1701
+    plan = focus.Rope(dim=d if H > 1 else d // 2, layout=layout, scaling="by_parts", factor=4.0)
+    q = randn(B, N, H, d, seed=1, dtype=dtype).cuda()
+    k = randn(B, N, H_kv, d, seed=2, dtype=dtype).cuda() if H_kv else None
+    pos = torch.randint(-5, 1 << 20, (B, N), generator=torch.Generator().manual_seed(3), dtype=torch.int32).cuda()
+    for call, kw in ((focus.rope, dict(offset=77)), (focus.rope_bwd, dict(positions=pos))):
+        wide = call(plan, torch.cat([q] * 16, 2), **kw)
+        got = call(plan, q, k, **kw)
+        assert torch.equal(got[0] if H_kv else got, wide[:, :, :H])
+        if H_kv:
+            assert torch.equal(got[1], call(plan, torch.cat([k] * 16, 2), **kw)[:, :, :H_kv])
+
+
 def test_rotation_of_broadcast_views():
     """One key head shown to all, as an expanded view: like its copies.  Outputs that share
     elements are refused."""
