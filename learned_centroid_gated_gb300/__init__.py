@@ -449,6 +449,11 @@ class _CacheParams(ctypes.Structure):
     _fields_ = [(n, ctypes.c_int32) for n in ("B", "cap", "T", "H", "H_kv", "d_head", "R", "K", "top_k", "w",
                                               "format")] + [("softmax_scale", ctypes.c_float)]
 
+    @property
+    def addr(self) -> int:
+        """Where this struct stands: worked out anew, since a copy stands elsewhere."""
+        return ctypes.addressof(self)
+
 
 _I32, _I64 = ctypes.c_int32, ctypes.c_int64
 _lib.focus_rope_init.argtypes = [_P, _P]
@@ -479,6 +484,12 @@ def _require(ok, what: str):
         raise FocusError(-1, what)
 
 
+def _made_anew(x):
+    """What copy and pickle keep of a frozen parameter object: its fields.  The copy makes its
+    own C structs, in its own process, with the library that is loaded there."""
+    return type(x), tuple(getattr(x, f.name) for f in dataclasses.fields(x))
+
+
 @dataclasses.dataclass(frozen=True)
 class Rope:
     """Rotary positions (focus_rope_params): dim rotated columns of each head, pairs
@@ -503,7 +514,13 @@ class Rope:
                              self.base, self.factor, self.beta_fast, self.beta_slow, self.attn_factor)
         _check(_lib.focus_rope_init(ctypes.byref(params), ctypes.byref(plan)), "focus_rope_init")
         object.__setattr__(self, "_plan", plan)
-        object.__setattr__(self, "_addr", ctypes.addressof(plan))
+
+    @property
+    def _addr(self) -> int:
+        return ctypes.addressof(self._plan)
+
+    def __reduce__(self):
+        return _made_anew(self)
 
 
 # Device and stream look-ups of the serving calls, which a program makes for every token:
@@ -624,11 +641,13 @@ class CacheParams:
         if c is None:
             c = _CacheParams(self.B, self.cap, T, self.H, self.H_kv, self.d_head, self.R, self.K, self.top_k, self.w,
                              CACHE_FORMATS[self.format], self.softmax_scale)
-            c.addr = ctypes.addressof(c)
             c.tree_ws = int(_lib.focus_decode_tree_workspace_size(c.addr))
             if len(self._by_tokens) < 4096:
                 self._by_tokens[T] = c
         return c
+
+    def __reduce__(self):
+        return _made_anew(self)
 
     @property
     def scale(self) -> float:
