@@ -32,7 +32,9 @@
 // The roles' loops share the instruction cache: the code is kept short rather than unrolled
 // (the conversion's loop unrolled by 4: 157 -> 172 us, by 2 the least).
 // The scales of 8-bit rows: K's multiplies the logits; V's multiplies P, and the reference of
-// the exponentials is that of the product, which is what fp16 has to hold.
+// the exponentials is that of the product, which is what fp16 has to hold.  P times V's scale is
+// an fp32 product and is rounded once (as fp16 times an fp16 scale, three roundings, it took the
+// same time: 64 rows over 128K int8 keys 147 us both).
 // Every wait is bounded; a wait that runs out raises FOCUS_ERR_TIMEOUT.
 #include <cuda.h>
 #include <math.h>
@@ -81,7 +83,6 @@ struct alignas(16) TileMeta<false> {
   int wide;                       // V scales differ by more than 2^4
   float lv, unit;                 // V scales are below 2^lv; 2^-lv
   float ks[kTile], vs[kTile];     // scales
-  __half vn[kTile];               // vs 2^-lv (not of a wide tile)
 };
 
 // What the readers and the MMA warp have to know of a tile, from a loader: its place in the
@@ -782,7 +783,6 @@ tree_tc(const __grid_constant__ TreeArgs a, const __grid_constant__ CUtensorMap 
               for (int e = 0; e < 2; ++e) {
                 me.ks[32 * e + lane] = ks[e];
                 me.vs[32 * e + lane] = vs[e];
-                me.vn[32 * e + lane] = __float2half_rn(vs[e] * unit);
               }
               if (lane == 0) {
                 me.wide = ex > 126 || __uint_as_float(top) > 16.0f * __uint_as_float(low);
@@ -804,7 +804,7 @@ tree_tc(const __grid_constant__ TreeArgs a, const __grid_constant__ CUtensorMap 
     const uint32_t lane_off = (uint32_t)((warp & 3) * 32) << 16;
     const uint32_t tO = tmem + lane_off + kSBuf * kTile + wg * 128;
     // A tile keeps the row's reference while its exponentials sum up to no more than the cap:
-    // far inside fp32 (bf16 P has its exponents), or what fp16 holds.
+    // far inside fp32 (bf16 P has its exponents), or what fp16 holds of them times V's scale.
     constexpr float kSumCap = B16 ? 1.8446744e19f : 32768.0f;
     constexpr float kTop = B16 ? 0.0f : 7.0f;  // log2 of the largest weight when m is set
     int t = 0, c = wg, seg = 0;  // tiles with end marks, products, segments
@@ -903,7 +903,7 @@ tree_tc(const __grid_constant__ TreeArgs a, const __grid_constant__ CUtensorMap 
             refer(fmaxf(fmaxf(mm[0], mm[1]), fmaxf(mm[2], mm[3])) * fac + (lv - kTop));
           };
           auto emit_all = [&]() {
-            const float nms = m == -INFINITY ? 0.0f : lv - m;
+            const float nms = m == -INFINITY ? 0.0f : -m;
             la = 0.0f;
             lb = 0.0f;
             auto emit = [&](uint32_t(&xx)[32], int k) {  // P over its S, which is in registers
@@ -923,13 +923,14 @@ tree_tc(const __grid_constant__ TreeArgs a, const __grid_constant__ CUtensorMap 
 #pragma unroll
                   for (int e = 0; e < 4; ++e) pk[i + e] = pack_bf16(y[2 * e], y[2 * e + 1]);
                 } else {
-                  const uint4 s = *reinterpret_cast<const uint4*>(me.vn + 32 * k + 2 * i);
-                  const uint32_t sw[4] = {s.x, s.y, s.z, s.w};
 #pragma unroll
-                  for (int e = 0; e < 4; ++e) {
-                    const uint32_t p = pack_f16(y[2 * e], y[2 * e + 1]);
-                    const __half2 z = __hmul2(*reinterpret_cast<const __half2*>(&p), *reinterpret_cast<const __half2*>(&sw[e]));
-                    pk[i + e] = *reinterpret_cast<const uint32_t*>(&z);
+                  for (int e = 0; e < 4; e += 2) {  // times V's scale in fp32, rounded once
+                    const float4 s = *reinterpret_cast<const float4*>(me.vs + 32 * k + 2 * (i + e));
+                    float z0, z1;
+                    fmul2(z0, z1, y[2 * e], y[2 * e + 1], s.x, s.y);
+                    pk[i + e] = pack_f16(z0, z1);
+                    fmul2(z0, z1, y[2 * e + 2], y[2 * e + 3], s.z, s.w);
+                    pk[i + e + 1] = pack_f16(z0, z1);
                   }
                 }
               }
@@ -944,10 +945,10 @@ tree_tc(const __grid_constant__ TreeArgs a, const __grid_constant__ CUtensorMap 
           for (int pass = 0; pass < 2; ++pass) {
             if (again) take_max();
             emit_all();
-            again = pass == 0 && __any_sync(0xffffffffu, !(la + lb <= kSumCap));
+            again = pass == 0 && __any_sync(0xffffffffu, !(la + lb <= kSumCap * unit));
             if (!again) break;
           }
-          l += (la + lb) * unit;
+          l += la + lb;
         } else if constexpr (!B16) {
           float mx = -INFINITY;
 #pragma unroll

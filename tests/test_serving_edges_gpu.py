@@ -1,0 +1,102 @@
+"""The ends of the range of the serving operators: scales far apart, roundings counted one by
+one, codes at ties, keys that are not finite in long sequences.
+
+References are 64-bit, on the device for long sequences.  Where all cached keys lie in the
+window and the drafted tokens form a chain, attention is causal attention: `dense`.
+u(t) = eps(t) / 2 is the largest relative error of one rounding to type t.
+"""
+import math
+
+import pytest
+import torch
+
+focus = pytest.importorskip("learned_centroid_gated_gb300")
+
+pytestmark = pytest.mark.gpu
+
+I32 = dict(dtype=torch.int32, device="cuda")
+
+
+def u(dtype):
+    return torch.finfo(dtype).eps / 2
+
+
+def randn(*shape, seed=0, dtype=torch.bfloat16):
+    g = torch.Generator().manual_seed(seed)
+    return torch.randn(*shape, generator=g).to(dtype)
+
+
+def dense(p, c, q, lens):
+    """o [B, T, H, d], lse [B, H, T], m = sum_j p_j |v_j| and z = max_j (p_j vs_j) sum_j |code_j|
+    in 64 bits, every key of the chain seen."""
+    B, T, H, d = q.shape
+    gq = H // p.H_kv
+    o, m, z = (torch.zeros(B, T, H, d, dtype=torch.float64, device="cuda") for _ in range(3))
+    lse = torch.zeros(B, H, T, dtype=torch.float64, device="cuda")
+    for b in range(B):
+        n = lens[b] + T
+        see = torch.arange(n, device="cuda")[None] <= lens[b] + torch.arange(T, device="cuda")[:, None]
+        for g in range(p.H_kv):
+            k, v = c.k[b, :n, g].double(), c.v[b, :n, g].double()
+            vs = None
+            if c.k_scale is not None:
+                k = k * c.k_scale[b, g, :n, None].double()
+                vs = c.v_scale[b, g, :n].double()
+            code, v = v, v if vs is None else v * vs[:, None]
+            for h in range(g * gq, (g + 1) * gq):
+                s = (q[b, :, h].cuda().double() @ k.T) * p.scale
+                s = s.masked_fill(~see, -math.inf)
+                lse[b, h] = torch.logsumexp(s, 1)
+                w = (s - lse[b, h][:, None]).exp()
+                o[b, :, h], m[b, :, h] = w @ v, w @ v.abs()
+                if vs is not None:
+                    z[b, :, h] = (w * vs).amax(1)[:, None] * (see.double() @ code.abs())
+    return o, lse, m, z
+
+
+# rows per KV head of the four forms of the kernels: one warp with 8 and with 16 rows, tensor
+# cores with up to 128 and up to 256 rows (a capacity of 8000 slots makes them worth it)
+FORMS = {"rows_8": 1, "rows_16": 4, "rows_128": 16, "rows_256": 64}
+
+
+def codes_cache(fmt, B=2, cap=8000, seed=0, **kw):
+    p = focus.CacheParams(B=B, cap=cap, **{**dict(H=16, H_kv=4, d_head=128, R=1, K=1, top_k=1, w=1 << 30), **kw}, format=fmt)
+    c = focus.KVCache.empty(p)
+    g = torch.Generator(device="cuda").manual_seed(seed)
+    for t in (c.k, c.v):
+        x = torch.randn(t.shape, generator=g, device="cuda")
+        t.copy_((x * 40).clamp(-127, 127).round().to(torch.int8) if fmt == "int8" else (x * 140).clamp(-448, 448).to(t.dtype))
+    unit = 40.0 if fmt == "int8" else 140.0
+    for t in (c.k_scale, c.v_scale):
+        t.copy_((torch.rand(t.shape, generator=g, device="cuda") + 0.5) / unit)
+    c.mask.fill_(1)
+    return p, c
+
+
+@pytest.mark.parametrize("fmt", ["e4m3", "int8"])
+@pytest.mark.parametrize("form", FORMS)
+def test_weights_of_8_bit_rows_are_rounded_once(form, fmt):
+    """One key with a value among keys whose values are zero, weights from the query: the result
+    before its own rounding is off by the one rounding of its weight times its scale to fp16,
+    u(fp16), and by 2^-18 of the exponentials and the sum, no more."""
+    T = FORMS[form]
+    p, c = codes_cache(fmt, H=32, H_kv=8, softmax_scale=1.0)
+    lens = [40, 40]
+    c.v_scale.zero_(), c.k_scale.zero_()
+    g = torch.Generator().manual_seed(9)
+    code = torch.randint(1, 127, (p.B, p.H_kv, p.d_head), generator=g).float() * (1 if fmt == "int8" else 3.5)
+    c.k[:, 11] = torch.zeros(()).to(c.k.dtype).cuda()
+    c.k[:, 11, :, 0] = torch.ones(()).to(c.k.dtype).cuda()
+    c.v[:, 11] = code.to(c.v.dtype).cuda()
+    c.k_scale[:, :, 11] = 1.0
+    c.v_scale[:, :, 11] = 1 + torch.rand(p.B, p.H_kv, generator=g).cuda()
+    q = torch.zeros(p.B, T, p.H, p.d_head)
+    q[..., 0] = -4 * torch.rand(p.B, T, p.H, generator=g)
+    q = q.to(torch.bfloat16)
+    o, lse = focus.decode_tree(p, q.cuda(), c, torch.tensor(lens, **I32))
+    want, want_lse, _, _ = dense(p, c, q, lens)
+    off = (u(torch.float16) + 2.0 ** -18) * want.abs()
+    ulp = torch.exp2(torch.floor(torch.log2(want.abs() + off))) * 2.0 ** -7
+    err = (o.double() - want).abs() - ulp / 2
+    assert bool((err <= off).all()), float((err / want.abs()).max() * 2 ** 11)
+    assert float((lse.double() - want_lse).abs().max()) <= 2.0 ** -18 * 8
