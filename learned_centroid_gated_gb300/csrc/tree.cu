@@ -252,13 +252,27 @@ tree_split(const __grid_constant__ TreeArgs a) {
       return true;
     };
 
-    float m[RL], l[RL], acc[NB][4];
+    // m: reference of the logits and of their sum l.  8-bit formats: mo is that of acc, that is of
+    // P times V's scale.  The two are apart since V's scales may lie further from another than
+    // fp32's exponents reach, and a key counts in l whatever its V row's size.
+    float m[RL], mo[RL], l[RL], acc[NB][4];
 #pragma unroll
-    for (int r = 0; r < RL; ++r) m[r] = -INFINITY, l[r] = 0.0f;
+    for (int r = 0; r < RL; ++r) m[r] = mo[r] = -INFINITY, l[r] = 0.0f;
 #pragma unroll
     for (int i = 0; i < NB; ++i)
 #pragma unroll
       for (int e = 0; e < 4; ++e) acc[i][e] = 0.0f;
+    // Accumulator e's share of a number per row: NR = 8 has rows 2 t4, 2 t4 + 1 as columns
+    // (their statistics sit in lanes 8 t4, 8 t4 + 4), NR = 16 has rows g, g + 8.
+    auto of_rows = [&](const float(&x)[RL], float(&f)[4]) {
+      if constexpr (NR == 8) {
+        f[0] = f[2] = __shfl_sync(0xffffffffu, x[0], 8 * t4);
+        f[1] = f[3] = __shfl_sync(0xffffffffu, x[0], 8 * t4 + 4);
+      } else {
+        f[0] = f[1] = x[0];
+        f[2] = f[3] = x[RL - 1];
+      }
+    };
     __syncwarp();  // zeroed stages (and the last stretch's reads) before the first copy
     int issued = 0;  // one copy group per stage and per refill, empty or not
     for (int s = 0; s < L::STAGES; ++s) {
@@ -343,7 +357,7 @@ tree_split(const __grid_constant__ TreeArgs a) {
         }
       }
       // ---- 8-bit formats: V's scales join P before it is rounded to fp16, and the reference
-      // m of a row is that of the product, which fp16 has to hold: its largest P vs is about
+      // mo of a row is that of the product, which fp16 has to hold: its largest P vs is about
       // 2^14, so that what is smaller by up to 2^-38 still counts.  Scales within 2^4 of
       // another are bounded by one power of two, others (an outlier that a row may not even
       // see) measured key by key.
@@ -363,47 +377,53 @@ tree_split(const __grid_constant__ TreeArgs a) {
           }
         }
       }
-      float corr[RL];
+      float corr[RL];           // of acc
       uint32_t pa[RL][2 * KH];  // P rounded for the tensor core; l sums it unrounded
 #pragma unroll
       for (int r = 0; r < RL; ++r) {
-        float mt = -INFINITY;
+        float mt = -INFINITY, mv = -INFINITY;  // largest logit; 8-bit formats: with V's scale
         if (!B16 && wide) {
 #pragma unroll
-          for (int e = 0; e < KE; ++e) mt = fmaxf(mt, sx[r][e] + lv[e]);
-        } else {
-#pragma unroll
-          for (int e = 0; e < KE; e += 2) mt = max3(mt, sx[r][e], sx[r][e + 1]);
-          mt += lift;
+          for (int e = 0; e < KE; ++e) mv = fmaxf(mv, sx[r][e] + lv[e]);
+          mv = fmaxf(mv, __shfl_xor_sync(0xffffffffu, mv, 1));
+          mv = fmaxf(mv, __shfl_xor_sync(0xffffffffu, mv, 2));
         }
+#pragma unroll
+        for (int e = 0; e < KE; e += 2) mt = max3(mt, sx[r][e], sx[r][e + 1]);
         mt = fmaxf(mt, __shfl_xor_sync(0xffffffffu, mt, 1));
         mt = fmaxf(mt, __shfl_xor_sync(0xffffffffu, mt, 2));
         const float mn = fmaxf(m[r], mt);
         const float mu = mn == -INFINITY ? 0.0f : mn;  // a row without a key so far
-        corr[r] = ex2(m[r] - mu);
+        const float fl = ex2(m[r] - mu);
         float p[KE], sum = 0.0f;
 #pragma unroll
         for (int e = 0; e < KE; ++e) p[e] = ex2(sx[r][e] - mu);
 #pragma unroll
         for (int e = 0; e < KE; e += 2) sum += p[e] + p[e + 1];
-        l[r] = l[r] * corr[r] + sum;
+        l[r] = l[r] * fl + sum;
         m[r] = mn;
+        if constexpr (B16) {
+          corr[r] = fl;
 #pragma unroll
-        for (int i = 0; i < 2 * KH; ++i)
-          pa[r][i] = B16 ? pack_bf16(p[2 * i], p[2 * i + 1])
-                         : pack_f16(p[2 * i] * vf[2 * i], p[2 * i + 1] * vf[2 * i + 1]);
+          for (int i = 0; i < 2 * KH; ++i) pa[r][i] = pack_bf16(p[2 * i], p[2 * i + 1]);
+        } else {
+          const float on = fmaxf(mo[r], wide ? mv : mt + lift);
+          const float ou = on == -INFINITY ? 0.0f : on;
+          corr[r] = ex2(mo[r] - ou);
+          mo[r] = on;
+          const float c = ex2(mu - ou);  // (2^-114 .. 2^94)
+#pragma unroll
+          for (int i = 0; i < 2 * KH; ++i) {
+            float y0, y1;
+            fmul2(y0, y1, p[2 * i], p[2 * i + 1], vf[2 * i], vf[2 * i + 1]);
+            fmul2(y0, y1, y0, y1, c, c);
+            pa[r][i] = pack_f16(y0, y1);
+          }
+        }
       }
       if (__any_sync(0xffffffffu, corr[0] != 1.0f || corr[RL - 1] != 1.0f)) {
-        // the factor of accumulator e: NR = 8 has rows 2 t4, 2 t4 + 1 as columns (their
-        // statistics sit in lanes 8 t4, 8 t4 + 4), NR = 16 has rows g, g + 8
         float f[4];
-        if constexpr (NR == 8) {
-          f[0] = f[2] = __shfl_sync(0xffffffffu, corr[0], 8 * t4);
-          f[1] = f[3] = __shfl_sync(0xffffffffu, corr[0], 8 * t4 + 4);
-        } else {
-          f[0] = f[1] = corr[0];
-          f[2] = f[3] = corr[RL - 1];
-        }
+        of_rows(corr, f);
 #pragma unroll
         for (int i = 0; i < NB; ++i)
 #pragma unroll
@@ -465,8 +485,18 @@ tree_split(const __grid_constant__ TreeArgs a) {
       if (issue(s)) ++issued;
       else cp_async_commit();
     }
-    // ---- this segment's partial
+    // ---- this segment's partial (8-bit formats: acc goes over to the reference of l)
     const int64_t slot = partial * NR;
+    if constexpr (!B16) {
+      float f[4], back[RL];
+#pragma unroll
+      for (int r = 0; r < RL; ++r) back[r] = ex2(mo[r] - m[r]);
+      of_rows(back, f);
+#pragma unroll
+      for (int i = 0; i < NB; ++i)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) acc[i][e] *= f[e];
+    }
 #pragma unroll
     for (int r = 0; r < RL; ++r) {
       l[r] += __shfl_xor_sync(0xffffffffu, l[r], 1);

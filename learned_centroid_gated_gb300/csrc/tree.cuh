@@ -11,8 +11,8 @@ namespace focus {
 
 constexpr int kTreeUnit = 32;        // keys per unit of work
 constexpr int kTreeNear = 64;        // weight of a unit near the window
-// 8-bit formats: V scales count as at least 2^-80 where the reference of the exponentials is
-// chosen, so that a row of (next to) zeros cannot push the sum of exponentials out of fp32.
+// 8-bit formats: V scales count as at least 2^-80 where the reference of O is chosen, so that it
+// stays within 2^113 of that of the logits and the factor between them is a normal number.
 constexpr float kTinyScale = 8.271806e-25f;
 
 struct TreeArgs {

@@ -80,7 +80,7 @@ template <>
 struct alignas(16) TileMeta<false> {
   uint64_t see[FOCUS_MAX_DRAFT];
   int end;
-  int wide;                       // V scales differ by more than 2^4
+  int wide;                       // V scales differ by more than 2^4, or are above 2^kFarGap
   float lv, unit;                 // V scales are below 2^lv; 2^-lv
   float ks[kTile], vs[kTile];     // scales
 };
@@ -91,6 +91,7 @@ struct Order {
   int tail, n;
 };
 constexpr int kEnd = -1;
+constexpr float kFarGap = 60.0f;  // log2
 
 template <int D, int FMT, int NT>
 struct Tc {
@@ -785,7 +786,7 @@ tree_tc(const __grid_constant__ TreeArgs a, const __grid_constant__ CUtensorMap 
                 me.vs[32 * e + lane] = vs[e];
               }
               if (lane == 0) {
-                me.wide = ex > 126 || __uint_as_float(top) > 16.0f * __uint_as_float(low);
+                me.wide = ex > (int)kFarGap || __uint_as_float(top) > 16.0f * __uint_as_float(low);
                 me.lv = (float)ex;
                 me.unit = unit;
               }
@@ -807,6 +808,7 @@ tree_tc(const __grid_constant__ TreeArgs a, const __grid_constant__ CUtensorMap 
     // far inside fp32 (bf16 P has its exponents), or what fp16 holds of them times V's scale.
     constexpr float kSumCap = B16 ? 1.8446744e19f : 32768.0f;
     constexpr float kTop = B16 ? 0.0f : 7.0f;  // log2 of the largest weight when m is set
+    constexpr float kLogitCap = 1.8446744e19f;   // 8-bit formats: a tile's share of l, before its reference follows
     int t = 0, c = wg, seg = 0;  // tiles with end marks, products, segments
     // pairs: parities of the next S of this warpgroup, and of the P V of its two P tiles
     uint32_t s_par = 0u, pv_par = 0u;
@@ -818,7 +820,14 @@ tree_tc(const __grid_constant__ TreeArgs a, const __grid_constant__ CUtensorMap 
       const int tt = min(x, a.rows - 1) / a.gq, ti = tt - row0 / a.gq;  // token; its place in the row group
       const bool alive = on && tree_word(a, b, tt) != 0ull;
       // a row that is no token sees nothing: its reference need not be looked for
+      // 8-bit formats: m is the reference of O, that is of P times V's scale; the sum l has one of
+      // its own, ml, of the logits alone, since V's scales may lie further apart than fp32's
+      // exponents reach and a key counts in l whatever its V row's size.  The exponentials are
+      // taken against m, or ml while m is far above it (the scales are large), and multiplied by
+      // back = 2^(ml - m) for P then; gap = 2^(ref - ml) brings their sums to l.
       float m = alive ? -INFINITY : 0.0f, l = 0.0f, fac = a.sl2;
+      float ml = m, ref = m, gap = 0.0f, back = 1.0f, most = INFINITY;  // most: kLogitCap / gap
+      bool far = false;  // some row of the warp is far
       const int c0 = c;
       // This warpgroup's last product P V (that of tile t - 1) is done.
       auto pv_done = [&]() {
@@ -856,7 +865,7 @@ tree_tc(const __grid_constant__ TreeArgs a, const __grid_constant__ CUtensorMap 
         if constexpr (!B16) {
           lv = me.lv;
           unit = me.unit;
-          wide = me.wide != 0;
+          wide = far || me.wide != 0;
           auto by_k = [&](uint32_t(&xx)[32], int cb) {
 #pragma unroll
             for (int i = 0; i < 32; i += 4) {
@@ -881,101 +890,101 @@ tree_tc(const __grid_constant__ TreeArgs a, const __grid_constant__ CUtensorMap 
           }
         }
         // ---- exponentials against the row's reference m, which moves only when a tile's
-        // sum passes the cap or while the row has seen no key.  8-bit formats: m is the
-        // reference of P times V's scale (below 2^lv in this tile); a tile whose scales are
-        // far apart (an outlier that this row may not even see) is measured key by key.
+        // sum passes the cap or while the row has seen no key.  8-bit formats: V's scales are
+        // below 2^lv in this tile; a tile whose scales are far apart (an outlier that this row
+        // may not even see) is measured key by key, and so are all while some row is far.
         float f = 1.0f;                    // what O has to be multiplied by
         const bool seen = m != -INFINITY;  // without a key so far O is zero
-        auto refer = [&](float mx) {
-          if (mx > m) {
+        float la, lb;
+        auto take_max = [&]() {
+          float mm[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+          for (int i = 0; i < 32; ++i)
+            mm[i & 3] = max3(mm[i & 3], __uint_as_float(x0[i]), __uint_as_float(x1[i]));
+          const float top = fmaxf(fmaxf(mm[0], mm[1]), fmaxf(mm[2], mm[3])) * fac;
+          float mx = top + lv;
+          if constexpr (!B16) {
+            if (wide) {
+              mx = -INFINITY;
+#pragma unroll
+              for (int i = 0; i < 32; ++i) {
+                mx = fmaxf(mx, __uint_as_float(x0[i]) * fac + __log2f(fmaxf(fabsf(me.vs[i]), kTinyScale)));
+                mx = fmaxf(mx, __uint_as_float(x1[i]) * fac + __log2f(fmaxf(fabsf(me.vs[32 + i]), kTinyScale)));
+              }
+            }
+          }
+          if (mx - kTop > m + (wide ? 7.0f : 0.0f)) {  // (key by key, fp16 has room for another 2^7)
+            mx -= kTop;
             if (seen) f = ex2(m - mx);
-            l *= f;
+            if (B16) l *= f;
             m = mx;
           }
+          if constexpr (!B16) {
+            if (top > ml) {
+              l *= ex2(ml - top);
+              ml = top;
+            }
+            const bool mine = m - ml > kFarGap;
+            far = __any_sync(0xffffffffu, mine);
+            ref = mine ? ml : m;
+            back = mine ? ex2(ml - m) : 1.0f;
+            gap = m == -INFINITY ? 0.0f : ex2(ref - ml);
+            most = kLogitCap / gap;
+          } else {
+            ref = m;
+          }
         };
-        float la, lb;
-        if (B16 || !wide) {
-          auto take_max = [&]() {
-            float mm[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-#pragma unroll
-            for (int i = 0; i < 32; ++i)
-              mm[i & 3] = max3(mm[i & 3], __uint_as_float(x0[i]), __uint_as_float(x1[i]));
-            refer(fmaxf(fmaxf(mm[0], mm[1]), fmaxf(mm[2], mm[3])) * fac + (lv - kTop));
-          };
-          auto emit_all = [&]() {
-            const float nms = m == -INFINITY ? 0.0f : -m;
-            la = 0.0f;
-            lb = 0.0f;
-            auto emit = [&](uint32_t(&xx)[32], int k) {  // P over its S, which is in registers
-              uint32_t pk[16];
-#pragma unroll
-              for (int i = 0; i < 16; i += 4) {
-                float y[8];
-#pragma unroll
-                for (int e = 0; e < 8; e += 2)
-                  ffma2(y[e], y[e + 1], __uint_as_float(xx[2 * i + e]), __uint_as_float(xx[2 * i + e + 1]), fac, fac,
-                        nms, nms);
-#pragma unroll
-                for (int e = 0; e < 8; ++e) y[e] = ex2(y[e]);
-#pragma unroll
-                for (int e = 0; e < 8; e += 2) fadd2(la, lb, la, lb, y[e], y[e + 1]);
-                if constexpr (B16) {
-#pragma unroll
-                  for (int e = 0; e < 4; ++e) pk[i + e] = pack_bf16(y[2 * e], y[2 * e + 1]);
-                } else {
-#pragma unroll
-                  for (int e = 0; e < 4; e += 2) {  // times V's scale in fp32, rounded once
-                    const float4 s = *reinterpret_cast<const float4*>(me.vs + 32 * k + 2 * (i + e));
-                    float z0, z1;
-                    fmul2(z0, z1, y[2 * e], y[2 * e + 1], s.x, s.y);
-                    pk[i + e] = pack_f16(z0, z1);
-                    fmul2(z0, z1, y[2 * e + 2], y[2 * e + 3], s.z, s.w);
-                    pk[i + e + 1] = pack_f16(z0, z1);
-                  }
-                }
-              }
-              tmem_st16(tS + 16 * k, pk);
-            };
-            emit(x0, 0);
-            emit(x1, 1);
-          };
-          // (a loop, so that the code is there once: the warps' instructions share a cache)
-          bool again = __any_sync(0xffffffffu, m == -INFINITY);
-#pragma unroll 1
-          for (int pass = 0; pass < 2; ++pass) {
-            if (again) take_max();
-            emit_all();
-            again = pass == 0 && __any_sync(0xffffffffu, !(la + lb <= kSumCap * unit));
-            if (!again) break;
-          }
-          l += la + lb;
-        } else if constexpr (!B16) {
-          float mx = -INFINITY;
-#pragma unroll
-          for (int i = 0; i < 32; ++i) {
-            mx = fmaxf(mx, __uint_as_float(x0[i]) * fac + __log2f(fmaxf(fabsf(me.vs[i]), kTinyScale)));
-            mx = fmaxf(mx, __uint_as_float(x1[i]) * fac + __log2f(fmaxf(fabsf(me.vs[32 + i]), kTinyScale)));
-          }
-          if (mx - kTop > m + 7.0f || !seen) refer(mx - kTop);
-          const float nms = m == -INFINITY ? 0.0f : -m;
+        auto emit_all = [&]() {
+          const float nms = m == -INFINITY ? 0.0f : -ref;
           la = 0.0f;
           lb = 0.0f;
-          auto emit = [&](uint32_t(&xx)[32], int k) {
+          auto emit = [&](uint32_t(&xx)[32], int k) {  // P over its S, which is in registers
             uint32_t pk[16];
 #pragma unroll
-            for (int i = 0; i < 16; ++i) {
-              const float y0 = ex2(fmaf(__uint_as_float(xx[2 * i]), fac, nms));
-              const float y1 = ex2(fmaf(__uint_as_float(xx[2 * i + 1]), fac, nms));
-              la += y0;
-              lb += y1;
-              pk[i] = pack_f16(y0 * me.vs[32 * k + 2 * i], y1 * me.vs[32 * k + 2 * i + 1]);
+            for (int i = 0; i < 16; i += 4) {
+              float y[8];
+#pragma unroll
+              for (int e = 0; e < 8; e += 2)
+                ffma2(y[e], y[e + 1], __uint_as_float(xx[2 * i + e]), __uint_as_float(xx[2 * i + e + 1]), fac, fac,
+                      nms, nms);
+#pragma unroll
+              for (int e = 0; e < 8; ++e) y[e] = ex2(y[e]);
+#pragma unroll
+              for (int e = 0; e < 8; e += 2) fadd2(la, lb, la, lb, y[e], y[e + 1]);
+              if constexpr (B16) {
+#pragma unroll
+                for (int e = 0; e < 4; ++e) pk[i + e] = pack_bf16(y[2 * e], y[2 * e + 1]);
+              } else {
+#pragma unroll
+                for (int e = 0; e < 8; e += 4) {  // times V's scale in fp32, rounded once
+                  const float4 s = *reinterpret_cast<const float4*>(me.vs + 32 * k + 2 * i + e);
+                  fmul2(y[e], y[e + 1], y[e], y[e + 1], s.x, s.y);
+                  fmul2(y[e + 2], y[e + 3], y[e + 2], y[e + 3], s.z, s.w);
+                }
+                if (far) {
+#pragma unroll
+                  for (int e = 0; e < 8; e += 2) fmul2(y[e], y[e + 1], y[e], y[e + 1], back, back);
+                }
+#pragma unroll
+                for (int e = 0; e < 4; ++e) pk[i + e] = pack_f16(y[2 * e], y[2 * e + 1]);
+              }
             }
             tmem_st16(tS + 16 * k, pk);
           };
           emit(x0, 0);
           emit(x1, 1);
-          l += la + lb;
+        };
+        // (a loop, so that the code is there once: the warps' instructions share a cache)
+        bool again = wide || __any_sync(0xffffffffu, m == -INFINITY);
+#pragma unroll 1
+        for (int pass = 0; pass < 2; ++pass) {
+          if (again) take_max();
+          emit_all();
+          const float cap = B16 ? kSumCap : wide ? INFINITY : fminf(kSumCap * unit, most);
+          again = pass == 0 && __any_sync(0xffffffffu, !(la + lb <= cap));
+          if (!again) break;
         }
+        l += B16 ? la + lb : (la + lb) * gap;
         if (__any_sync(0xffffffffu, f != 1.0f) && c > c0) {
           // O of this warpgroup's earlier products follows the reference
           if (!(ok = pv_done())) return;
@@ -1004,8 +1013,10 @@ tree_tc(const __grid_constant__ TreeArgs a, const __grid_constant__ CUtensorMap 
       }
       ++t;  // the end mark
       const int64_t slot = (partial * NT + wg) * kRows + r;
-      if (on) a.part_ml[slot] = make_float2(m, some ? l : 0.0f);
+      if (on) a.part_ml[slot] = make_float2(B16 ? m : ml, some ? l : 0.0f);
       if (some) {
+        // (8-bit formats: O goes over to the reference that the merge knows, that of l)
+        const float to_l = B16 ? 1.0f : ex2(m - ml);
 #pragma unroll
         for (int k = 0; k < D / 32; ++k) {
           uint32_t y[32];
@@ -1014,9 +1025,12 @@ tree_tc(const __grid_constant__ TreeArgs a, const __grid_constant__ CUtensorMap 
           if (on) {
             float4* dst = reinterpret_cast<float4*>(a.part_acc + slot * D + 32 * k);
 #pragma unroll
-            for (int i = 0; i < 8; ++i)
-              dst[i] = make_float4(__uint_as_float(y[4 * i]), __uint_as_float(y[4 * i + 1]),
-                                   __uint_as_float(y[4 * i + 2]), __uint_as_float(y[4 * i + 3]));
+            for (int i = 0; i < 8; ++i) {
+              float4 z = make_float4(__uint_as_float(y[4 * i]), __uint_as_float(y[4 * i + 1]),
+                                     __uint_as_float(y[4 * i + 2]), __uint_as_float(y[4 * i + 3]));
+              if constexpr (!B16) z.x *= to_l, z.y *= to_l, z.z *= to_l, z.w *= to_l;
+              dst[i] = z;
+            }
           }
         }
       }

@@ -73,6 +73,47 @@ def codes_cache(fmt, B=2, cap=8000, seed=0, **kw):
     return p, c
 
 
+# log2 of V's scale by key: None is a scale of zero
+SPREADS = {
+    "zeros_then_large": lambda j, n: torch.where(j < n // 2, -math.inf, 50.0),
+    "large_then_zeros": lambda j, n: torch.where(j < n // 2, 50.0, -math.inf),
+    "smallest_to_largest": lambda j, n: -105.0 + 215.0 * j / n,
+    "largest_to_smallest": lambda j, n: 110.0 - 215.0 * j / n,
+    "blocks": lambda j, n: torch.tensor([-60.0, 100.0, -math.inf, 0.0, -100.0])[(j // 64) % 5],
+    "mixed": lambda j, n: torch.tensor([-60.0, 100.0, -math.inf, 0.0, -100.0])[(j * 7) % 5],
+}
+
+
+@pytest.mark.parametrize("fmt", ["e4m3", "int8"])
+@pytest.mark.parametrize("spread", SPREADS)
+@pytest.mark.parametrize("form", FORMS)
+def test_scales_at_the_ends_of_the_range(form, spread, fmt):
+    """V's scales from 2^-105 to 2^110 and zeros, in tiles of one segment and in different
+    segments: a key counts in the sum of the exponentials whatever its V row's size.  The sum of
+    the exponentials is checked by LSE, to the bound that holds for scales alike."""
+    T, lens = FORMS[form], [2990, 700]
+    p, c = codes_cache(fmt)
+    n = max(lens) + T
+    j = torch.arange(n)
+    c.v_scale[:, :, :n] *= torch.exp2(SPREADS[spread](j, n).double()).float().cuda()
+    for equal in (True, False):
+        if equal:
+            keep = c.k_scale.clone()
+            c.k_scale.zero_()  # equal logits
+        q = randn(p.B, T, p.H, p.d_head, seed=3)
+        o, lse = focus.decode_tree(p, q.cuda(), c, torch.tensor(lens, **I32))
+        want, want_lse, m, z = dense(p, c, q, lens)
+        if equal:
+            c.k_scale.copy_(keep)
+        # the logits' own error: d 2^-22 of a product of magnitudes below 100
+        ds = 0.0 if equal else p.d_head * 2.0 ** -22 * 100
+        assert float((lse.double() - want_lse).abs().max()) <= 2 * ds + 2.0 ** -18 * float(want_lse.abs().max())
+        # as for scales alike; an output below fp32's normal numbers may be zero
+        bound = (u(torch.float16) + 4 * ds + 2.0 ** -18) * m + u(torch.bfloat16) * want.abs() + 2.0 ** -28 * z + 2.0 ** -126
+        err = (o.double() - want).abs()
+        assert bool((err <= bound).all()), float((err / bound).max())
+
+
 @pytest.mark.parametrize("fmt", ["e4m3", "int8"])
 @pytest.mark.parametrize("form", FORMS)
 def test_weights_of_8_bit_rows_are_rounded_once(form, fmt):
