@@ -395,8 +395,9 @@ int focus_rope_apply(const focus_rope* rope, int32_t dtype, int32_t B, int32_t N
  *   k_scale, v_scale  [B, H_kv, cap] fp32, the 8-bit formats only (NULL for BF16)
  *   mask_cache        [B, R, cap] uint32 group bitmasks (e.g. from focus_route)
  * 8-bit formats: a row (one token, one head, d_head values) is held as codes c_i with
- * one scale: x_i ~ c_i * scale, scale = max|x| / M, c_i = round(x_i * (M / max|x|)),
- * M = 448 (E4M3: 4 exponent and 3 mantissa bits, ties to even) or 127 (INT8).  A row
+ * one scale: x_i ~ c_i * scale, scale = max|x| / M, c_i = round(x_i * (M / max|x|)) with
+ * ties to even, M = 448 (E4M3: 4 exponent and 3 mantissa bits) or 127 (INT8); the quotient
+ * is an fp32 number, and so is the product for E4M3 (for INT8 it is exact).  A row
  * with max|x| < 2^-100 is held as zeros with scale 0; a row with a NaN or an infinity
  * as zeros with a NaN scale (it reads back as NaN).
  */

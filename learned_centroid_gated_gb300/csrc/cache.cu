@@ -217,8 +217,7 @@ __global__ void __launch_bounds__(256, MODE == kHalfAny ? 3 : 4) cache_write(con
 #pragma unroll
       for (int o = 1; o < LPR; o <<= 1) mx = abs_max3(mx, __shfl_xor_sync(0xffffffffu, mx, o), 0.0f);
       const bool finite = mx < INFINITY, some = finite && mx >= kTinyRow;
-      // (the fast quotient, two units in the last place, holds up to 2^126)
-      const float inv = some ? (mx < 8e37f ? __fdividef(M, mx) : M / mx) : 0.0f;
+      const float inv = some ? M / mx : 0.0f;
       if (on) {
         const uint2 zero = make_uint2(0u, 0u);
         *reinterpret_cast<uint2*>(y + 8 * ca) = some ? encode<FMT>(fa, inv) : zero;

@@ -10,6 +10,8 @@ import math
 import pytest
 import torch
 
+import serving_ref as ref
+
 focus = pytest.importorskip("learned_centroid_gated_gb300")
 
 pytestmark = pytest.mark.gpu
@@ -141,3 +143,35 @@ def test_weights_of_8_bit_rows_are_rounded_once(form, fmt):
     err = (o.double() - want).abs() - ulp / 2
     assert bool((err <= off).all()), float((err / want.abs()).max() * 2 ** 11)
     assert float((lse.double() - want_lse).abs().max()) <= 2.0 ** -18 * 8
+
+
+@pytest.mark.parametrize("fmt", ["e4m3", "int8"])
+@pytest.mark.parametrize("H_kv", [1, 16])
+def test_codes_at_ties(fmt, H_kv):
+    """Codes are round(x (M / max|x|)), ties to even, equal to the last code: rows whose largest
+    value divides M exactly and others, filled with values half-way between codes.  The quotient is
+    an fp32 number; its product with x is one too for e4m3, and exact for int8, where the code is
+    rounded from a fused multiply-add (8 by 24 bits: exact in 64-bit arithmetic here)."""
+    M = ref.MAX_CODE[fmt]
+    tops = [2.0 ** e * (7 if fmt == "e4m3" else 127) / 64 for e in range(-20, 20)] + [float(x) for x in range(1, 256)]
+    g = torch.Generator().manual_seed(2)
+    rows = []
+    for i, top in enumerate(tops):
+        code = torch.randint(0, 127, (4, 128), generator=g).float() + 0.5 if fmt == "int8" else \
+            torch.exp2(torch.randint(-5, 8, (4, 128), generator=g).float()) * (2 * torch.randint(8, 16, (4, 128), generator=g) + 1) / 16
+        x = (code * (top / M)).clamp(max=top) * (1 - 2 * torch.randint(0, 2, (4, 128), generator=g))
+        x[:, 5] = top
+        rows.append(x)
+    x = torch.cat(rows).to(torch.bfloat16)
+    T = len(x) // H_kv
+    x = x[:T * H_kv].view(1, T, H_kv, 128)
+    p = focus.CacheParams(B=1, cap=T, H=H_kv, H_kv=H_kv, d_head=128, R=1, K=1, top_k=1, w=1, format=fmt)
+    c = focus.KVCache.empty(p)
+    focus.cache_write(p, c, x.cuda(), x.cuda(), None, torch.zeros(1, **I32))
+    f = x.float()
+    top = f.abs().amax(-1, keepdim=True)
+    y = (f.double() if fmt == "int8" else f) * (torch.tensor(M) / top)
+    want = y.round().to(torch.int8) if fmt == "int8" else y.clamp(-M, M).to(torch.float8_e4m3fn)
+    for got in (c.k, c.v):
+        bad = got.cpu().view(torch.uint8) != want.view(torch.uint8)
+        assert int(bad.sum()) == 0, (int(bad.sum()), bad.numel())
