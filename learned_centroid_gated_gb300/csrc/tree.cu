@@ -548,63 +548,18 @@ __device__ __forceinline__ float cache_value(const void* x, int64_t at) {
   }
 }
 
-// One row again, key by key, without the keys that it does not see: a NaN or an infinity in
-// the V row of such a key, which other rows of the MMA do see, has met a zero weight there
-// and spoilt the sum.  Only rows that came out not finite get here.
-template <int D, int FMT, int NT>
-__device__ __noinline__ float row_by_hand(const TreeArgs& a, int b, int t, int h, int len, float lse2,
-                                          float* weight /* shared, NT */, unsigned* bits /* shared, NT / 32 */) {
-  const int kvh = h / a.gq, rho = kvh / (a.H_kv / a.R);
-  const uint32_t* M = a.mask + ((int64_t)b * a.R + rho) * a.cap;
-  const uint64_t word = tree_word(a, b, t);
-  const int near = len + __popcll(word) - a.w;
-  const uint32_t mrow = M[len + t];
-  const bf16* q = a.q + (((int64_t)b * a.T + t) * a.H + h) * D;
-  const int64_t sc = ((int64_t)b * a.H_kv + kvh) * a.cap;
-  float out = 0.0f;
-  for (int j0 = 0; j0 < len + a.T; j0 += NT) {
-    const int j = j0 + threadIdx.x;
-    bool see = j < len + a.T;
-    if (see) {
-      int p = j;
-      if (j >= len) {
-        see = (word >> (j - len) & 1ull) != 0ull;
-        p = len + __popcll(tree_word(a, b, j - len)) - 1;
-      }
-      see = see && (p >= near || (M[j] & mrow) != 0u);
-    }
-    float x = 0.0f;
-    if (see) {
-      const int64_t at = (((int64_t)b * a.cap + j) * a.H_kv + kvh) * D;
-      for (int c = 0; c < D; ++c) x += __bfloat162float(q[c]) * cache_value<FMT>(a.kc, at + c);
-      if constexpr (FMT != FOCUS_CACHE_BF16) x *= a.ks[sc + j];
-      x = ex2(x * a.sl2 - lse2);
-      if constexpr (FMT != FOCUS_CACHE_BF16) x *= a.vs[sc + j];
-    }
-    __syncthreads();
-    weight[threadIdx.x] = x;
-    const unsigned seen = __ballot_sync(0xffffffffu, see);
-    if ((threadIdx.x & 31) == 0) bits[threadIdx.x >> 5] = seen;
-    __syncthreads();
-    if (threadIdx.x < D)
-      for (int i = 0; i < NT; ++i)
-        if (bits[i >> 5] >> (i & 31) & 1u)
-          out += weight[i] *
-                 cache_value<FMT>(a.vc, (((int64_t)b * a.cap + j0 + i) * a.H_kv + kvh) * D + threadIdx.x);
-  }
-  return out;
-}
-
 // Where the partials of row (t, h) of sequence b are.
 struct RowParts {
   int64_t ln, from, whole, part;
   Stretch s;
   int b, len, row, ns, first, last, n;  // slices first .. last may hold a part; n: partials to look at
 
-  __device__ __forceinline__ bool find(const TreeArgs& a, int c, int64_t& slot) const {
+  // Partial c of those to look at: its place, and its keys as [keys.x, keys.y).
+  __device__ __forceinline__ bool find(const TreeArgs& a, int c, int64_t& slot, int2& keys) const {
     const int sl = first + c;
     const int64_t lo = slice_at(whole, ns, part, sl), hi = slice_at(whole, ns, part, sl + 1);
-    if (units_before(a, s, lo - from) >= units_before(a, s, hi - from)) return false;  // no such partial
+    keys = make_int2(units_before(a, s, lo - from) * kTreeUnit, units_before(a, s, hi - from) * kTreeUnit);
+    if (keys.x >= keys.y) return false;  // no such partial
     slot = (sl + ln * a.B + b) * a.grp + row % a.grp;
     return true;
   }
@@ -638,6 +593,144 @@ __device__ __forceinline__ RowParts row_parts(const TreeArgs& a, int b, int t, i
   return r;
 }
 
+// Shared memory of rows that are worked out again.
+template <int NT>
+struct Again {
+  float weight[NT], x[NT];  // of partial results, of keys
+  int key[NT];
+  int64_t place[NT];
+  int2 range[NT];
+  unsigned bits[NT / 32], bad[NT / 32];
+};
+
+// Keys [js, je) of one row again, without the keys that it does not see: a thread per key
+// lists NT keys, a warp per listed key takes its weight, NT / D groups of D threads sum the
+// values, a key each at a time.  Returns the thread's share of column threadIdx.x % D.
+template <int D, int FMT, int NT>
+__device__ float keys_by_hand(const TreeArgs& a, const RowParts& rp, int t, int h, float lse2, int js, int je, Again<NT>& sh) {
+  constexpr int V = D / 32, NW = NT / 32, NG = NT / D, U = 4;
+  const int b = rp.b, len = rp.len, kvh = h / a.gq, rho = kvh / (a.H_kv / a.R);
+  const int lane = threadIdx.x & 31, wp = threadIdx.x >> 5, g = threadIdx.x / D, d = threadIdx.x % D;
+  const uint32_t* M = a.mask + ((int64_t)b * a.R + rho) * a.cap;
+  const uint64_t word = tree_word(a, b, t);
+  const int near = len + __popcll(word) - a.w;
+  const uint32_t mrow = M[len + t];
+  const bf16* q = a.q + (((int64_t)b * a.T + t) * a.H + h) * D + V * lane;
+  float qf[V];
+#pragma unroll
+  for (int v = 0; v < V; ++v) qf[v] = __bfloat162float(q[v]);
+  const int64_t sc = ((int64_t)b * a.H_kv + kvh) * a.cap, row0 = ((int64_t)b * a.cap * a.H_kv + kvh) * D;
+  const int64_t kvrow = (int64_t)a.H_kv * D;
+  float out = 0.0f;
+  for (int j0 = js; j0 < je; j0 += NT) {
+    const int j = j0 + threadIdx.x;
+    bool see = j < je;
+    if (see) {
+      int p = j;
+      if (j >= len) {
+        see = (word >> (j - len) & 1ull) != 0ull;
+        p = len + __popcll(tree_word(a, b, j - len)) - 1;
+      }
+      see = see && (p >= near || (M[j] & mrow) != 0u);
+    }
+    const unsigned seen = __ballot_sync(0xffffffffu, see);
+    if (lane == 0) sh.bits[wp] = seen;
+    __syncthreads();
+    int n = 0, at = 0;
+    for (int i = 0; i < NW; ++i) {
+      at += i < wp ? __popc(sh.bits[i]) : 0;
+      n += __popc(sh.bits[i]);
+    }
+    if (see) sh.key[at + __popc(seen & lanemask_lt())] = j;
+    __syncthreads();
+    for (int i0 = wp; i0 < n; i0 += U * NW) {
+      float x[U];
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        x[u] = 0.0f;
+        if (i0 + u * NW < n) {
+          const int64_t from = row0 + sh.key[i0 + u * NW] * kvrow + V * lane;
+#pragma unroll
+          for (int v = 0; v < V; ++v) x[u] += qf[v] * cache_value<FMT>(a.kc, from + v);
+        }
+      }
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+#pragma unroll
+        for (int o = 16; o; o >>= 1) x[u] += __shfl_xor_sync(0xffffffffu, x[u], o);
+        if (lane == 0 && i0 + u * NW < n) {
+          const int k = sh.key[i0 + u * NW];
+          if constexpr (FMT != FOCUS_CACHE_BF16) x[u] *= a.ks[sc + k];
+          x[u] = ex2(x[u] * a.sl2 - lse2);
+          if constexpr (FMT != FOCUS_CACHE_BF16) x[u] *= a.vs[sc + k];
+          sh.x[i0 + u * NW] = x[u];
+        }
+      }
+    }
+    __syncthreads();
+    float part = 0.0f;  // (a sum of its own per NT keys: no chain over a long sequence)
+#pragma unroll 8
+    for (int i = g; i < n; i += NG) part += sh.x[i] * cache_value<FMT>(a.vc, row0 + sh.key[i] * kvrow + d);
+    out += part;
+    __syncthreads();
+  }
+  return out;
+}
+
+// A row whose output came out not finite, again, by all of a block's threads: a NaN or an
+// infinity in the V row of a key that it does not see, which other rows of the MMA do see, has
+// met a zero weight there and spoilt the sum, or weights and values that fp32 holds had a
+// product that it does not.  The partial results are merged again with weights that sum up to
+// one, and those that are not finite are worked out again key by key: their part of the
+// sequence, not all of it.  Returns column threadIdx.x of the output (threads below D).
+// Measured, one such key that half of the tokens see behind 100000 keys: one token 0.07 -> 0.13
+// ms, 16 drafts int8 0.15 -> 0.96 (bf16 0.12 -> 0.88), 64 drafts 0.22 -> 2.8 (0.18 -> 2.5); three
+// in different slices, 16 drafts: 2.5.
+template <int D, int FMT, int NT>
+__device__ __noinline__ float row_again(const TreeArgs& a, const RowParts& rp, int t, int h, float lse2, Again<NT>& sh) {
+  constexpr int NG = NT / D, NW = NT / 32;
+  const int tid = threadIdx.x, g = tid / D, d = tid % D;
+  float acc = 0.0f;
+  for (int base = 0; base < rp.n; base += NT) {
+    const int c = base + tid;
+    int64_t slot = 0;
+    int2 range = make_int2(0, 0);
+    float w = 0.0f;
+    if (c < rp.n && rp.find(a, c, slot, range)) {
+      const float2 x = a.part_ml[slot];
+      if (x.y != 0.0f) w = ex2(x.x - lse2);
+    }
+    sh.weight[tid] = w;
+    sh.place[tid] = slot * D;
+    sh.range[tid] = range;
+    if (tid < NW) sh.bad[tid] = 0u;
+    __syncthreads();
+    const int end = min(NT, rp.n - base);
+    for (int i = g; i < end; i += NG) {
+      if (sh.weight[i] == 0.0f) continue;
+      const float p = a.part_acc[sh.place[i] + d];
+      if (fabsf(p) < INFINITY) acc += sh.weight[i] * p;
+      else atomicOr(&sh.bad[i >> 5], 1u << (i & 31));
+    }
+    __syncthreads();
+    for (int i = 0; i < end; ++i) {
+      if (!(sh.bad[i >> 5] >> (i & 31) & 1u)) continue;
+      const bool mine = !(fabsf(a.part_acc[sh.place[i] + d]) < INFINITY);
+      const int2 keys = sh.range[i];
+      const float x = keys_by_hand<D, FMT, NT>(a, rp, t, h, lse2, keys.x, min(keys.y, rp.len + a.T), sh);
+      if (mine) acc += x;
+    }
+    __syncthreads();
+  }
+  // the groups' shares
+  sh.weight[tid] = acc;
+  __syncthreads();
+  if (tid < D)
+    for (int i = 1; i < NG; ++i) acc += sh.weight[i * D + tid];
+  __syncthreads();
+  return acc;
+}
+
 // The call's status, by one warp.
 __device__ __forceinline__ void put_status(const TreeArgs& a, int ns, int64_t total, bool bad, int lane) {
   int code = 0;
@@ -656,11 +749,9 @@ __device__ __forceinline__ void put_status(const TreeArgs& a, int ns, int64_t to
 template <int D, int FMT, int NT>
 __global__ void __launch_bounds__(NT) tree_combine(const __grid_constant__ TreeArgs a) {
   constexpr int NG = NT / D, NW = NT / 32, U = 8;
-  __shared__ float weight[NT];
-  __shared__ int64_t place[NT];
+  __shared__ Again<NT> sh;
   __shared__ float sums[NG][D];
   __shared__ float red[2][NW];
-  __shared__ unsigned bits[NW];
   const int tid = threadIdx.x, wp = tid >> 5, lane = tid & 31, g = tid / D, d = tid % D;
   const int b = blockIdx.y, t = blockIdx.x / a.H, h = blockIdx.x % a.H;
   int64_t total;
@@ -673,7 +764,8 @@ __global__ void __launch_bounds__(NT) tree_combine(const __grid_constant__ TreeA
     const int c = base + tid;
     float2 x = make_float2(-INFINITY, 0.0f);
     int64_t slot = 0;
-    if (c < rp.n && rp.find(a, c, slot)) x = a.part_ml[slot];
+    int2 keys;
+    if (c < rp.n && rp.find(a, c, slot, keys)) x = a.part_ml[slot];
     const bool some = x.y != 0.0f;  // a key of the slice is seen
     float top = some ? x.x : -INFINITY;
 #pragma unroll
@@ -689,8 +781,8 @@ __global__ void __launch_bounds__(NT) tree_combine(const __grid_constant__ TreeA
     l = l * f + (some ? x.y * w : 0.0f);
     acc *= f;
     m = mn;
-    weight[tid] = w;
-    place[tid] = slot * D;
+    sh.weight[tid] = w;
+    sh.place[tid] = slot * D;
     __syncthreads();
     const int end = min(NT, rp.n - base);
     if constexpr (NT == 128) {  // a thread has many to sum: U loads in flight
@@ -699,8 +791,8 @@ __global__ void __launch_bounds__(NT) tree_combine(const __grid_constant__ TreeA
 #pragma unroll
         for (int i = 0; i < U; ++i) {
           const int at = i0 + i * NG;
-          y[i] = at < end ? weight[at] : 0.0f;
-          p[i] = y[i] != 0.0f ? a.part_acc[place[at] + d] : 0.0f;
+          y[i] = at < end ? sh.weight[at] : 0.0f;
+          p[i] = y[i] != 0.0f ? a.part_acc[sh.place[at] + d] : 0.0f;
         }
 #pragma unroll
         for (int i = 0; i < U; ++i) acc += y[i] * p[i];
@@ -708,8 +800,8 @@ __global__ void __launch_bounds__(NT) tree_combine(const __grid_constant__ TreeA
     } else {
 #pragma unroll 4
       for (int i = g; i < end; i += NG) {
-        const float y = weight[i];
-        if (y != 0.0f) acc += y * a.part_acc[place[i] + d];
+        const float y = sh.weight[i];
+        if (y != 0.0f) acc += y * a.part_acc[sh.place[i] + d];
       }
     }
     __syncthreads();
@@ -726,10 +818,27 @@ __global__ void __launch_bounds__(NT) tree_combine(const __grid_constant__ TreeA
   const bool empty = sum == 0.0f;
   const float lse2 = m + log2f(sum);
   out = empty ? 0.0f : out / sum;
-  if (__syncthreads_or(tid < D && !(fabsf(out) < INFINITY)))
-    out = row_by_hand<D, FMT, NT>(a, b, t, h, rp.len, lse2, weight, bits);
+  // (a sum that is not finite either has NaN of the row's own: the row is NaN)
+  if (__syncthreads_or(tid < D && !(fabsf(out) < INFINITY)) && fabsf(lse2) < INFINITY)
+    out = row_again<D, FMT, NT>(a, rp, t, h, lse2, sh);
   if (tid < D) a.o[(((int64_t)b * a.T + t) * a.H + h) * D + d] = __float2bfloat16_rn(out);
   if (tid == 0 && a.lse) a.lse[((int64_t)b * a.H + h) * a.T + t] = empty ? -INFINITY : lse2 * kLn2;
+}
+
+// The rows of a block of tree_combine_rows that came out not finite, one after another.  Out of
+// line, so that the merge itself keeps its registers.
+template <int D, int FMT, int NT>
+__device__ __noinline__ void rows_again(const TreeArgs& a, const int* again, const float* lse_of, Again<NT>& sh) {
+  const int b = blockIdx.y, lane = threadIdx.x & 31;
+  for (int i = 0; i < NT / 32; ++i) {
+    if (!again[i]) continue;
+    const int y = blockIdx.x * (NT / 32) + i, t = y / a.H, h = y % a.H;
+    int64_t total;
+    bool bad;
+    const RowParts rp = row_parts(a, b, t, h, lane, total, bad);
+    const float out = row_again<D, FMT, NT>(a, rp, t, h, lse_of[i], sh);
+    if (threadIdx.x < D) a.o[(((int64_t)b * a.T + t) * a.H + h) * D + threadIdx.x] = __float2bfloat16_rn(out);
+  }
 }
 
 // The same with a warp per row, for calls of many rows: grid (T * H / 8 rounded up, B).
@@ -737,8 +846,7 @@ template <int D, int FMT>
 __global__ void __launch_bounds__(256) tree_combine_rows(const __grid_constant__ TreeArgs a) {
   constexpr int NT = 256, U = 8, V = D / 32;  // V: columns of a lane
   using vec = std::conditional_t<V == 4, float4, float2>;
-  __shared__ float weight[NT];
-  __shared__ unsigned bits[NT / 32];
+  __shared__ Again<NT> sh;
   __shared__ float lse_of[NT / 32];
   const int wp = threadIdx.x >> 5, lane = threadIdx.x & 31, b = blockIdx.y;
   const int x = blockIdx.x * 8 + wp, t = min(x, a.T * a.H - 1) / a.H, h = x % a.H;
@@ -754,7 +862,8 @@ __global__ void __launch_bounds__(256) tree_combine_rows(const __grid_constant__
   for (int base = 0; mine && base < rp.n; base += 32) {
     float2 ml = make_float2(-INFINITY, 0.0f);
     int64_t slot = 0;
-    if (base + lane < rp.n && rp.find(a, base + lane, slot)) ml = a.part_ml[slot];
+    int2 keys;
+    if (base + lane < rp.n && rp.find(a, base + lane, slot, keys)) ml = a.part_ml[slot];
     const bool some = ml.y != 0.0f;  // a key of the slice is seen
     float top = some ? ml.x : -INFINITY;
 #pragma unroll
@@ -802,19 +911,13 @@ __global__ void __launch_bounds__(256) tree_combine_rows(const __grid_constant__
       *reinterpret_cast<uint32_t*>(o) = pack_bf16(acc[0], acc[1]);
     if (lane == 0 && a.lse) a.lse[((int64_t)b * a.H + h) * a.T + t] = empty ? -INFINITY : lse2 * kLn2;
   }
-  odd = __any_sync(0xffffffffu, odd && mine);
+  odd = __any_sync(0xffffffffu, odd && mine && fabsf(lse2) < INFINITY);  // (as above)
   if (!__syncthreads_or(odd)) return;
   // rows that are not finite, one after another, by all warps
   __shared__ int again[NT / 32];
   if (lane == 0) again[wp] = odd, lse_of[wp] = lse2;
   __syncthreads();
-  for (int i = 0; i < NT / 32; ++i) {
-    if (!again[i]) continue;
-    const int y = blockIdx.x * 8 + i, ty = y / a.H, hy = y % a.H;
-    const float out = row_by_hand<D, FMT, NT>(a, b, ty, hy, rp.len, lse_of[i], weight, bits);
-    if (threadIdx.x < D) a.o[(((int64_t)b * a.T + ty) * a.H + hy) * D + threadIdx.x] = __float2bfloat16_rn(out);
-    __syncthreads();
-  }
+  rows_again<D, FMT, NT>(a, again, lse_of, sh);
 }
 
 // ------------------------------------------------------------------------- launch --

@@ -175,3 +175,65 @@ def test_codes_at_ties(fmt, H_kv):
     for got in (c.k, c.v):
         bad = got.cpu().view(torch.uint8) != want.view(torch.uint8)
         assert int(bad.sum()) == 0, (int(bad.sum()), bad.numel())
+
+
+def _time(call, n=3):
+    call()
+    best = math.inf
+    for _ in range(n):
+        a, b = (torch.cuda.Event(enable_timing=True) for _ in range(2))
+        torch.cuda.synchronize()
+        a.record()
+        call()
+        b.record()
+        b.synchronize()
+        best = min(best, a.elapsed_time(b))
+    return best
+
+
+@pytest.mark.parametrize("fmt", ["bf16", "int8"])
+@pytest.mark.parametrize("T,H_kv,places", [(1, 8, 1), (1, 1, 2), (16, 8, 1), (16, 8, 3), (64, 8, 1)])
+def test_keys_that_are_not_finite_in_a_long_sequence(fmt, T, H_kv, places):
+    """V rows of NaN among 100000 keys that half of the tokens see: the rows that see them are
+    NaN, the others keep their values, and the call stays of the order of a call without them
+    (what is worked out again is their parts of the sequence)."""
+    n, at = 100000, [61234, 100, 99990][:places]
+    p = focus.CacheParams(B=1, cap=n + 64, H=32, H_kv=H_kv, d_head=128, R=1, K=2, top_k=1, w=4, format=fmt)
+    g = torch.Generator(device="cuda").manual_seed(1)
+    c = focus.KVCache.empty(p)
+    if fmt == "bf16":
+        c.k.copy_(torch.randn(c.k.shape, generator=g, device="cuda") * 0.3), c.v.copy_(torch.randn(c.v.shape, generator=g, device="cuda"))
+    else:
+        for t in (c.k, c.v):
+            t.copy_(torch.randint(-127, 128, t.shape, generator=g, device="cuda"))
+        c.k_scale.fill_(0.004), c.v_scale.fill_(0.02)
+    c.mask.copy_(torch.randint(1, 3, c.mask.shape, generator=g, device="cuda"))
+    c.mask[:, :, n:] = 1
+    if T > 1:
+        c.mask[:, :, n + T // 2:] = 2
+    c.mask[0, 0, at] = 1
+    q = randn(1, T, p.H, p.d_head, seed=2).cuda()
+    lens = torch.tensor([n], **I32)
+    ws = torch.empty(focus.decode_tree_workspace_size(p, T), dtype=torch.uint8, device="cuda")
+    call = lambda: focus.decode_tree(p, q, c, lens, ws=ws)
+    clean, clean_lse = call()
+    plain = _time(call)
+    if fmt == "bf16":
+        c.v[0, at, :, ::2] = math.nan
+    else:
+        c.v_scale[0, :, at] = math.nan
+    got, lse = call()
+    hit = _time(call)
+    sees = slice(0, max(1, T // 2))
+    cols = slice(0, None, 2 if fmt == "bf16" else 1)
+    assert bool(got[0, sees, :, cols].isnan().all())
+    if fmt == "bf16":  # a column without a NaN keeps its value: 100000 terms in fp32
+        err = (got[0, sees, :, 1::2].float() - clean[0, sees, :, 1::2].float()).abs()
+        assert bool((err <= 2.0 ** -7 * clean[0, sees, :, 1::2].float().abs() + 2.0 ** -12).all()), float(err.max())
+    if T > 1:
+        rest = slice(T // 2, None)
+        err = (got[0, rest].float() - clean[0, rest].float()).abs()
+        assert bool((err <= 2.0 ** -7 * clean[0, rest].float().abs() + 2.0 ** -12).all()), float(err.max())
+        assert bool(lse[0, :, rest].isfinite().all())
+    print("a clean call %.3f ms, with the key %.3f ms" % (plain, hit))
+    assert hit <= 20 * plain + 1.0
