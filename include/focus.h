@@ -462,7 +462,8 @@ int focus_cache_read(const focus_cache_params* p, const void* k_cache, const voi
  * A NaN or an infinity in a row's own keys and values shows in that row's result, in
  * keys it does not see in no result.  A sequence with lens[b] outside [0, cap - T]
  * raises FOCUS_ERR_BOUNDS in the workspace's status word (focus_get_status); its rows
- * get zeros and -inf, and nothing of it is read.
+ * get zeros and -inf, and nothing of it is read.  A wait inside a kernel that runs out
+ * raises FOCUS_ERR_TIMEOUT there, and the rows it spoilt are NaN.
  *   ws    focus_decode_tree_workspace_size(p) bytes, 256-byte aligned; of one call at a
  *         time (calls that may overlap, on two streams, have one each).  o does not
  *         overlap q.
@@ -483,6 +484,14 @@ int focus_decode_tree(const focus_cache_params* p, const uint16_t* q, const void
  *   ws  device buffer of at least 1 MiB, 256-byte aligned (contents overwritten)
  */
 int focus_selftest_timeout(void* ws, size_t ws_bytes, void* stream);
+
+/*
+ * The same for focus_decode_tree's tensor-core kernel, in four forms (bf16 and INT8, up to
+ * 128 rows per KV head and more): a loader warp keeps back one arrival.  Returns
+ * FOCUS_ERR_TIMEOUT when every form raised it and left NaN in every row of o and lse.
+ *   ws  device buffer of at least 16 MiB, 256-byte aligned (contents overwritten)
+ */
+int focus_selftest_timeout_decode(void* ws, size_t ws_bytes, void* stream);
 
 /* Static, human-readable text for a status code. */
 const char* focus_strerror(int code);

@@ -143,6 +143,8 @@ _lib.focus_decode.argtypes = [_PP, _P, _P, _P, _P, _P, _P, _P, ctypes.c_size_t, 
 _lib.focus_decode.restype = ctypes.c_int
 _lib.focus_selftest_timeout.argtypes = [_P, ctypes.c_size_t, _P]
 _lib.focus_selftest_timeout.restype = ctypes.c_int
+_lib.focus_selftest_timeout_decode.argtypes = [_P, ctypes.c_size_t, _P]
+_lib.focus_selftest_timeout_decode.restype = ctypes.c_int
 _lib.focus_get_status.argtypes = [_P, _P]
 _lib.focus_get_status.restype = ctypes.c_int
 _lib.focus_strerror.argtypes = [ctypes.c_int]
@@ -785,6 +787,13 @@ def selftest_timeout(device="cuda", stream=None) -> int:
     """Run the device failure-path diagnostic; returns the status (-5 = FOCUS_ERR_TIMEOUT)."""
     ws = torch.empty(1 << 20, dtype=torch.uint8, device=device)
     return _lib.focus_selftest_timeout(_ptr(ws), ws.numel(), _stream(stream))
+
+
+def selftest_timeout_decode(device="cuda", stream=None) -> int:
+    """The same for decode_tree's tensor-core kernel in its four forms (bf16 and 8 bits, up to 128
+    and more rows per KV head): -5 where each raised FOCUS_ERR_TIMEOUT and left NaN in every row."""
+    ws = torch.empty(16 << 20, dtype=torch.uint8, device=device)
+    return _lib.focus_selftest_timeout_decode(_ptr(ws), ws.numel(), _stream(stream))
 
 
 def get_status(ws: torch.Tensor, stream=None) -> int:

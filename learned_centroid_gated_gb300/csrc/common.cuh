@@ -173,6 +173,8 @@ cudaError_t launch_decode_tree(const focus_cache_params& p, const bf16* q, const
                                const float* ks, const float* vs, const uint32_t* mask,
                                const int32_t* lens, const uint64_t* tree, bf16* o, float* lse, char* ws,
                                float scale, cudaStream_t s);
+size_t tree_selftest_bytes();
+cudaError_t launch_tree_timeout_selftest(char* ws, int format, int T, size_t* o_at, size_t* lse_at, cudaStream_t s);
 // attn_tc.cu (tcgen05 engine)
 int tc_block_rows();
 cudaError_t launch_timeout_selftest(char* ws, size_t ws_bytes, cudaStream_t s);

@@ -804,6 +804,33 @@ int focus_selftest_timeout(void* ws, size_t ws_bytes, void* stream) {
   return focus_get_status(ws, stream);
 }
 
+int focus_selftest_timeout_decode(void* ws, size_t ws_bytes, void* stream) {
+  if (!ws) return FOCUS_ERR_INVALID_ARG;
+  if (!aligned(ws, 256)) return FOCUS_ERR_ALIGNMENT;
+  if (ws_bytes < tree_selftest_bytes()) return FOCUS_ERR_WORKSPACE;
+  cudaStream_t s = (cudaStream_t)stream;
+  char* w = (char*)ws;
+  for (int format : {FOCUS_CACHE_BF16, FOCUS_CACHE_INT8})
+    for (int T : {17, FOCUS_MAX_DRAFT}) {
+      size_t o_at, lse_at;
+      int rc = cuda_rc(launch_tree_timeout_selftest(w, format, T, &o_at, &lse_at, s));
+      if (rc) return rc;
+      if ((rc = focus_get_status(ws, stream)) != FOCUS_ERR_TIMEOUT) return rc;
+      uint16_t o[FOCUS_MAX_DRAFT * 4 * 128];
+      float lse[FOCUS_MAX_DRAFT * 4];
+      const size_t n = (size_t)T * 4;
+      if (cudaMemcpyAsync(o, w + o_at, n * 128 * 2, cudaMemcpyDeviceToHost, s) != cudaSuccess ||
+          cudaMemcpyAsync(lse, w + lse_at, n * 4, cudaMemcpyDeviceToHost, s) != cudaSuccess ||
+          cudaStreamSynchronize(s) != cudaSuccess)
+        return FOCUS_ERR_CUDA;
+      for (size_t i = 0; i < n * 128; ++i)
+        if ((o[i] & 0x7fffu) <= 0x7f80u) return FOCUS_OK;  // a number in place of a NaN
+      for (size_t i = 0; i < n; ++i)
+        if (lse[i] == lse[i]) return FOCUS_OK;
+    }
+  return FOCUS_ERR_TIMEOUT;
+}
+
 int focus_get_status(const void* ws, void* stream) {
   if (!ws) return FOCUS_ERR_INVALID_ARG;
   cudaStream_t s = (cudaStream_t)stream;

@@ -563,6 +563,12 @@ struct RowParts {
     slot = (sl + ln * a.B + b) * a.grp + row % a.grp;
     return true;
   }
+  // (max, sum) of that partial; NaN where its slice gave up, so that nothing stale passes for a result.
+  __device__ __forceinline__ float2 sums(const TreeArgs& a, int c, int64_t slot) const {
+    const float2 x = a.part_ml[slot];
+    if (a.flags && a.flags[first + c] != 0) return make_float2(__uint_as_float(0x7fc00000u), __uint_as_float(0x7fc00000u));
+    return x;
+  }
 };
 
 // All of a warp's lanes; total: all sequences' weight, bad: some length is out of range.
@@ -765,7 +771,7 @@ __global__ void __launch_bounds__(NT) tree_combine(const __grid_constant__ TreeA
     float2 x = make_float2(-INFINITY, 0.0f);
     int64_t slot = 0;
     int2 keys;
-    if (c < rp.n && rp.find(a, c, slot, keys)) x = a.part_ml[slot];
+    if (c < rp.n && rp.find(a, c, slot, keys)) x = rp.sums(a, c, slot);
     const bool some = x.y != 0.0f;  // a key of the slice is seen
     float top = some ? x.x : -INFINITY;
 #pragma unroll
@@ -863,7 +869,7 @@ __global__ void __launch_bounds__(256) tree_combine_rows(const __grid_constant__
     float2 ml = make_float2(-INFINITY, 0.0f);
     int64_t slot = 0;
     int2 keys;
-    if (base + lane < rp.n && rp.find(a, base + lane, slot, keys)) ml = a.part_ml[slot];
+    if (base + lane < rp.n && rp.find(a, base + lane, slot, keys)) ml = rp.sums(a, base + lane, slot);
     const bool some = ml.y != 0.0f;  // a key of the slice is seen
     float top = some ? ml.x : -INFINITY;
 #pragma unroll
@@ -939,7 +945,7 @@ struct TreePlan {
   size_t flags, ml, acc, total;  // offsets and size of the workspace
 };
 
-TreePlan tree_plan(const focus_cache_params& p) {
+TreePlan tree_plan(const focus_cache_params& p, bool force_tc = false) {
   TreePlan t;
   t.gq = p.H / p.H_kv;
   t.rows = p.T * t.gq;
@@ -951,7 +957,7 @@ TreePlan tree_plan(const focus_cache_params& p) {
   // against 43.  The lengths are not known here: the capacity stands for them.
   const double units = (double)p.B * p.H_kv * ((p.cap + kTreeUnit - 1) / kTreeUnit);
   const int r16 = (t.rows + 15) / 16, r128 = (t.rows + 127) / 128;
-  t.tc = t.rows > 16 && 20e3 + units * (r128 == 1 ? 3.0 : 5.5 * ((r128 + 1) / 2)) < 8e3 + units * 2.5 * r16;
+  t.tc = force_tc || t.rows > 16 && 20e3 + units * (r128 == 1 ? 3.0 : 5.5 * ((r128 + 1) / 2)) < 8e3 + units * 2.5 * r16;
   t.grp = t.tc ? (t.rows > kTreeTcRows ? 2 * kTreeTcRows : kTreeTcRows) : t.rows > 8 ? 16 : 8;
   t.nrg = (t.rows + t.grp - 1) / t.grp;
   t.G = kTreeSms * (t.tc ? 1 : split_warps(p.d_head, p.format, t.grp));
@@ -997,11 +1003,7 @@ cudaError_t launch_combine(const TreeArgs& a, K* kernel, int rows, int threads, 
 }
 
 template <int D, int FMT>
-cudaError_t launch_tree(const TreeArgs& a, bool tc, cudaStream_t s) {
-  const cudaError_t e = tc             ? launch_tree_tc(a, D, FMT, s)
-                        : a.grp == 8 ? launch_split<D, FMT, 8>(a, s)
-                                     : launch_split<D, FMT, 16>(a, s);
-  if (e != cudaSuccess) return e;
+cudaError_t launch_merge(const TreeArgs& a, cudaStream_t s) {
   // The merge, by its rows and by the partials of one, were all sequences alike.  Few rows with
   // many partials: many threads for a row (32 rows of 210: 10 us with 1024 threads, 33 with a
   // warp).  Many rows with few: 2048 of 19 take 8 us by warps, 12 by 128 threads, 41 by 512;
@@ -1015,15 +1017,23 @@ cudaError_t launch_tree(const TreeArgs& a, bool tc, cudaStream_t s) {
                      : launch_combine(a, tree_combine<D, FMT, 128>, 1, 128, s);
 }
 
+template <int D, int FMT>
+cudaError_t launch_tree(const TreeArgs& a, bool tc, cudaStream_t s) {
+  const cudaError_t e = tc             ? launch_tree_tc(a, D, FMT, s)
+                        : a.grp == 8 ? launch_split<D, FMT, 8>(a, s)
+                                     : launch_split<D, FMT, 16>(a, s);
+  return e != cudaSuccess ? e : launch_merge<D, FMT>(a, s);
+}
+
 }  // namespace
 
 size_t tree_workspace_bytes(const focus_cache_params& p) { return tree_plan(p).total; }
 
-cudaError_t launch_decode_tree(const focus_cache_params& p, const bf16* q, const void* kc, const void* vc,
-                               const float* ks, const float* vs, const uint32_t* mask,
-                               const int32_t* lens, const uint64_t* tree, bf16* o, float* lse, char* ws,
-                               float scale, cudaStream_t s) {
-  const TreePlan t = tree_plan(p);
+namespace {
+
+TreeArgs args_of(const focus_cache_params& p, const TreePlan& t, const bf16* q, const void* kc, const void* vc,
+                 const float* ks, const float* vs, const uint32_t* mask, const int32_t* lens, const uint64_t* tree,
+                 bf16* o, float* lse, char* ws, float scale) {
   TreeArgs a;
   a.q = q, a.kc = kc, a.vc = vc, a.ks = ks, a.vs = vs, a.mask = mask, a.lens = lens, a.tree = tree;
   a.part_ml = reinterpret_cast<float2*>(ws + t.ml);
@@ -1034,6 +1044,17 @@ cudaError_t launch_decode_tree(const focus_cache_params& p, const bf16* q, const
   a.gq = t.gq, a.rows = t.rows, a.grp = t.grp, a.nrg = t.nrg;
   a.G = t.G, a.wfar = t.wfar, a.tma = 0;
   a.sl2 = scale * kLog2e;
+  return a;
+}
+
+}  // namespace
+
+cudaError_t launch_decode_tree(const focus_cache_params& p, const bf16* q, const void* kc, const void* vc,
+                               const float* ks, const float* vs, const uint32_t* mask,
+                               const int32_t* lens, const uint64_t* tree, bf16* o, float* lse, char* ws,
+                               float scale, cudaStream_t s) {
+  const TreePlan t = tree_plan(p);
+  const TreeArgs a = args_of(p, t, q, kc, vc, ks, vs, mask, lens, tree, o, lse, ws, scale);
   if (p.d_head == 64)
     return p.format == FOCUS_CACHE_BF16   ? launch_tree<64, FOCUS_CACHE_BF16>(a, t.tc, s)
            : p.format == FOCUS_CACHE_E4M3 ? launch_tree<64, FOCUS_CACHE_E4M3>(a, t.tc, s)
@@ -1041,6 +1062,41 @@ cudaError_t launch_decode_tree(const focus_cache_params& p, const bf16* q, const
   return p.format == FOCUS_CACHE_BF16   ? launch_tree<128, FOCUS_CACHE_BF16>(a, t.tc, s)
          : p.format == FOCUS_CACHE_E4M3 ? launch_tree<128, FOCUS_CACHE_E4M3>(a, t.tc, s)
                                         : launch_tree<128, FOCUS_CACHE_INT8>(a, t.tc, s);
+}
+
+// Diagnostic launch of the tensor-core kernel on a small problem, one CTA: one loader warp keeps
+// back its word that Q is there, the waits end after ~10 ms.  The MMA warp's wait runs out while the
+// other roles stand at theirs, the loaders with all stages full: the CTA gives up, waits for its
+// copies, frees its tensor memory and exits, and the merge makes every row NaN.
+// o [T, 4, 128] bf16 and lse [4, T] are left at the returned offsets of ws.
+size_t tree_selftest_bytes() { return 16u << 20; }
+cudaError_t launch_tree_timeout_selftest(char* ws, int format, int T, size_t* o_at, size_t* lse_at, cudaStream_t s) {
+  focus_cache_params p{};
+  p.B = 1, p.cap = 2048, p.T = T, p.H = 4, p.H_kv = 1, p.d_head = 128;
+  p.R = 1, p.K = 1, p.top_k = 1, p.w = 1 << 20, p.format = format;
+  const TreePlan t = tree_plan(p, true);
+  size_t at = t.total;
+  auto take = [&](size_t bytes) {
+    const size_t x = at;
+    at += align_up(bytes, 256);
+    return x;
+  };
+  const size_t kv = (size_t)p.cap * p.d_head * 2, rows = (size_t)T * p.H;
+  const size_t q = take(rows * p.d_head * 2), k = take(kv), v = take(kv), ks = take(p.cap * 4), vs = take(p.cap * 4);
+  const size_t mask = take(p.cap * 4), lens = take(4);
+  *o_at = take(rows * p.d_head * 2), *lse_at = take(rows * 4);
+  if (at > tree_selftest_bytes()) return cudaErrorInvalidValue;
+  cudaError_t e = cudaMemsetAsync(ws, 0, at, s);
+  if (e != cudaSuccess) return e;
+  if ((e = cudaMemsetAsync(ws + lens + 1, 4, 1, s)) != cudaSuccess) return e;  // 1024 cached tokens
+  const bool scales = format != FOCUS_CACHE_BF16;
+  TreeArgs a = args_of(p, t, reinterpret_cast<bf16*>(ws + q), ws + k, ws + v, scales ? reinterpret_cast<float*>(ws + ks) : nullptr,
+                       scales ? reinterpret_cast<float*>(ws + vs) : nullptr, reinterpret_cast<uint32_t*>(ws + mask),
+                       reinterpret_cast<int32_t*>(ws + lens), nullptr, reinterpret_cast<bf16*>(ws + *o_at),
+                       reinterpret_cast<float*>(ws + *lse_at), ws, 0.1f);
+  a.G = 1;
+  if ((e = launch_tree_tc_held(a, format, s)) != cudaSuccess) return e;
+  return format == FOCUS_CACHE_BF16 ? launch_merge<128, FOCUS_CACHE_BF16>(a, s) : launch_merge<128, FOCUS_CACHE_INT8>(a, s);
 }
 
 }  // namespace focus

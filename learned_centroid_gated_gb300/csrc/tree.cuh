@@ -212,5 +212,6 @@ __device__ __forceinline__ void row_unit(float largest, float& up, float& down) 
 
 // tree_tc.cu
 cudaError_t launch_tree_tc(const TreeArgs& a, int d_head, int format, cudaStream_t s);
+cudaError_t launch_tree_tc_held(const TreeArgs& a, int format, cudaStream_t s);  // self-test; d_head 128, bf16 or int8
 
 }  // namespace focus

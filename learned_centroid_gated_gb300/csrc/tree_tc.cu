@@ -159,7 +159,9 @@ __device__ __forceinline__ void sts128(uint32_t addr, uint32_t x, uint32_t y, ui
   asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(addr), "r"(x), "r"(y), "r"(z), "r"(w) : "memory");
 }
 
-template <int D, int FMT, int NT>
+// HOLD: the self-test's form, in which a loader warp keeps back its word that Q is there and the
+// waits end after about 10 ms.  (A limit read at run time cost the others 1%.)
+template <int D, int FMT, int NT, bool HOLD>
 __global__ void __launch_bounds__(kThreads, 1)
 tree_tc(const __grid_constant__ TreeArgs a, const __grid_constant__ CUtensorMap map_k,
         const __grid_constant__ CUtensorMap map_v) {
@@ -168,6 +170,7 @@ tree_tc(const __grid_constant__ TreeArgs a, const __grid_constant__ CUtensorMap 
   constexpr bool B16 = L::B16;
   constexpr int S = L::STAGES, ES = B16 ? 2 : 1;
   constexpr int LW = L::LW;
+  constexpr long long kLimit = HOLD ? 20000000LL : kTimeoutCycles;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* sm = smem_raw + (-smem_u32(smem_raw) & 1023u);  // (stays a shared-memory pointer to the compiler)
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -232,7 +235,7 @@ tree_tc(const __grid_constant__ TreeArgs a, const __grid_constant__ CUtensorMap 
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
-  auto wait = [&](uint32_t b, int phase) { return mbar_wait(b, phase & 1, abort_flag, status); };
+  auto wait = [&](uint32_t b, int phase) { return mbar_wait(b, phase & 1, abort_flag, status, kLimit); };
   auto wait_all = [&](uint32_t b, int phase) { return __all_sync(0xffffffffu, wait(b, phase)) != 0; };
   auto o_read = [&](int seg) {  // the softmax warps have read the O of segment seg
     const uint32_t b = b_epi + 8 * (seg & 1);
@@ -300,7 +303,7 @@ tree_tc(const __grid_constant__ TreeArgs a, const __grid_constant__ CUtensorMap 
       }
       fence_proxy_async_smem();
       __syncwarp();
-      if (lane == 0) mbar_arrive(b_q);
+      if (lane == 0 && !(HOLD && lw == 0)) mbar_arrive(b_q);
       // ---- what the tokens see, taken together
       uint32_t many = 0u, wlo = 0u, whi = 0u;
       int nearest = INT_MAX;
@@ -507,7 +510,9 @@ tree_tc(const __grid_constant__ TreeArgs a, const __grid_constant__ CUtensorMap 
       if (ok) meet();  // the list starts anew
     });
     cp_async_wait<0>();
-    if (lt == 0 && *abort_flag)  // giving up: copies in flight land before the CTA exits
+    // No CTA exits with a copy in flight, whoever gives up and when: the last TMA of each slot lands
+    // first (codes' copies have been waited for, unless this warp gave up).
+    if (lt == 0 && (B16 || *abort_flag))
       for (int i = 0; i < L::SLOTS; ++i) {
         if (!(tma_any >> i & 1u)) continue;
         if constexpr (B16) mbar_drain(b_full + 8 * i, (uint32_t)((t - 1 - i) / S & 1));
@@ -551,7 +556,7 @@ tree_tc(const __grid_constant__ TreeArgs a, const __grid_constant__ CUtensorMap 
               t0 = clock64();
             } else if (*abort_flag) {
               ok = false;
-            } else if (clock64() - t0 > kTimeoutCycles) {
+            } else if (clock64() - t0 > kLimit) {
               *abort_flag = 1;
               raise_status(status, FOCUS_ERR_TIMEOUT);
               ok = false;
@@ -590,7 +595,7 @@ tree_tc(const __grid_constant__ TreeArgs a, const __grid_constant__ CUtensorMap 
               s_product(tmem + rt * 2 * kTile, rt, (nb & ~1) % S);
               umma_commit(b_s + 8 * rt);
             };
-            look(true);
+            if (ok) look(true);
             if (ready) {
               make_s(0);
               make_s(1);
@@ -1081,25 +1086,25 @@ bool make_map(CUtensorMap* m, const void* base, const TreeArgs& a, int D, bool b
             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-template <int D, int FMT, int NT>
+template <int D, int FMT, int NT, bool HOLD>
 cudaError_t launch(TreeArgs a, cudaStream_t s) {
   using L = Tc<D, FMT, NT>;
   static std::atomic<uint64_t> done{0};
   const cudaError_t e = once_per_device(done, [] {
-    return cudaFuncSetAttribute(tree_tc<D, FMT, NT>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+    return cudaFuncSetAttribute(tree_tc<D, FMT, NT, HOLD>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                 Tc<D, FMT, NT>::BYTES);
   });
   if (e != cudaSuccess) return e;
   CUtensorMap mk{}, mv{};
   // a TMA coordinate is 32 bits; beyond that (or without the encoder) rows come one by one
   a.tma = (int64_t)a.B * a.cap < INT32_MAX && make_map(&mk, a.kc, a, D, L::B16) && make_map(&mv, a.vc, a, D, L::B16);
-  tree_tc<D, FMT, NT><<<(unsigned)a.G, kThreads, L::BYTES, s>>>(a, mk, mv);
+  tree_tc<D, FMT, NT, HOLD><<<(unsigned)a.G, kThreads, L::BYTES, s>>>(a, mk, mv);
   return cudaGetLastError();
 }
 
 template <int D, int FMT>
 cudaError_t launch_nt(const TreeArgs& a, cudaStream_t s) {
-  return a.grp == kRows ? launch<D, FMT, 1>(a, s) : launch<D, FMT, 2>(a, s);
+  return a.grp == kRows ? launch<D, FMT, 1, false>(a, s) : launch<D, FMT, 2, false>(a, s);
 }
 
 }  // namespace
@@ -1112,6 +1117,12 @@ cudaError_t launch_tree_tc(const TreeArgs& a, int d_head, int format, cudaStream
   return format == FOCUS_CACHE_BF16   ? launch_nt<128, FOCUS_CACHE_BF16>(a, s)
          : format == FOCUS_CACHE_E4M3 ? launch_nt<128, FOCUS_CACHE_E4M3>(a, s)
                                       : launch_nt<128, FOCUS_CACHE_INT8>(a, s);
+}
+
+cudaError_t launch_tree_tc_held(const TreeArgs& a, int format, cudaStream_t s) {
+  constexpr int B = FOCUS_CACHE_BF16, I = FOCUS_CACHE_INT8;
+  if (format == B) return a.grp == kRows ? launch<128, B, 1, true>(a, s) : launch<128, B, 2, true>(a, s);
+  return a.grp == kRows ? launch<128, I, 1, true>(a, s) : launch<128, I, 2, true>(a, s);
 }
 
 }  // namespace focus

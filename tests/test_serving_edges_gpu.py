@@ -75,6 +75,16 @@ def codes_cache(fmt, B=2, cap=8000, seed=0, **kw):
     return p, c
 
 
+def plain_cache():
+    p = focus.CacheParams(B=2, cap=8000, H=16, H_kv=4, d_head=128, R=1, K=1, top_k=1, w=1 << 30)
+    c = focus.KVCache.empty(p)
+    g = torch.Generator(device="cuda").manual_seed(4)
+    for t in (c.k, c.v):
+        t.copy_(torch.randn(t.shape, generator=g, device="cuda"))
+    c.mask.fill_(1)
+    return p, c
+
+
 # log2 of V's scale by key: None is a scale of zero
 SPREADS = {
     "zeros_then_large": lambda j, n: torch.where(j < n // 2, -math.inf, 50.0),
@@ -237,3 +247,24 @@ def test_keys_that_are_not_finite_in_a_long_sequence(fmt, T, H_kv, places):
         assert bool(lse[0, :, rest].isfinite().all())
     print("a clean call %.3f ms, with the key %.3f ms" % (plain, hit))
     assert hit <= 20 * plain + 1.0
+
+
+def test_a_decode_that_times_out_leaves_nan_and_a_usable_context():
+    """The tensor-core kernel with one arrival kept back: its waits run out, every role gives up,
+    and the rows are NaN rather than what stood in the workspace.  The next call is right."""
+    for _ in range(2):
+        assert focus.ERRORS[focus.selftest_timeout_decode()] == "FOCUS_ERR_TIMEOUT"
+    for fmt in ("bf16", "int8"):
+        for T in (16, 64):
+            p, c = (codes_cache(fmt) if fmt != "bf16" else plain_cache())
+            lens = [700, 31]
+            q = randn(p.B, T, p.H, p.d_head, seed=5)
+            ws = torch.empty(focus.decode_tree_workspace_size(p, T), dtype=torch.uint8, device="cuda")
+            o, lse = focus.decode_tree(p, q.cuda(), c, torch.tensor(lens, **I32), ws=ws)
+            assert focus.get_status(ws) == 0
+            want, want_lse, m, _ = dense(p, c, q, lens)
+            # one rounding of P, one of the result; logits of magnitudes below 100 off by d 2^-22 of them
+            ds = p.d_head * 2.0 ** -22 * 100
+            bound = (u(torch.bfloat16) + 4 * ds + 2.0 ** -18) * m + u(torch.bfloat16) * want.abs()
+            assert bool(((o.double() - want).abs() <= bound).all())
+            assert float((lse.double() - want_lse).abs().max()) <= 2 * ds + 2.0 ** -18 * 16
