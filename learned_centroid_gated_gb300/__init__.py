@@ -752,14 +752,16 @@ def decode_tree_workspace_size(p: CacheParams, T: int) -> int:
 
 
 def decode_tree(p: CacheParams, q: torch.Tensor, cache: KVCache, lens: torch.Tensor, tree=None, *, out=None,
-                lse=None, want_lse: bool = True, ws=None, stream=None):
+                lse=None, want_lse: bool = True, ws=None, status=None, stream=None):
     """Decode step for T <= MAX_DRAFT drafted tokens per sequence: q [B, T, H, d] bf16, lens [B]
     int32 tokens in the cache before them; the drafted tokens' own keys, values and masks stand
     in slots lens[b] + u.  tree [B, T] int64: bit u of word t set when drafted token u is an
     ancestor of t or t itself (None: a chain; a word of 0 marks a row that is no token).
     T = 1 is the plain next token of sequences of different lengths.  ws: a workspace of
     decode_tree_workspace_size(p, T) bytes, of one call at a time; get_status(ws) reads the
-    call's status (FOCUS_ERR_BOUNDS where a length does not fit).
+    call's status (FOCUS_ERR_BOUNDS where a length does not fit: zeros and -inf; FOCUS_ERR_TIMEOUT:
+    NaN).  status: an int32 device word, as in cache_write, that keeps the lowest code of all
+    calls that it was given to; without ws and status a call's code is lost.
     Returns (o [B, T, H, d] bf16, lse [B, H, T] fp32)."""
     what = "focus_decode_tree"
     dev, kc, vc, ksc, vsc, mc = cache._args(p, what)
@@ -776,10 +778,13 @@ def decode_tree(p: CacheParams, q: torch.Tensor, cache: KVCache, lens: torch.Ten
             lse = torch.empty((p.B, p.H, T), dtype=torch.float32, device=q.device)
         ws = torch.empty(c.tree_ws, dtype=torch.uint8, device=q.device) if ws is None else ws
         _require(ws.get_device() == dev and ws.is_contiguous(), what)
+        _vector(status, (1,), dev, what)
         _check(_lib.focus_decode_tree(
             c.addr, qp, kc, vc, ksc, vsc, mc, _vector(lens, (p.B,), dev, what),
             _vector(tree, (p.B, T), dev, what, torch.int64), _vector(out, shape, dev, what, torch.bfloat16),
             _vector(lse, (p.B, p.H, T), dev, what, torch.float32), ws.data_ptr(), ws.nbytes, s), what)
+        if status is not None:
+            torch.minimum(status, ws.view(-1).view(torch.uint8)[:4].view(torch.int32), out=status)
     return out, lse
 
 

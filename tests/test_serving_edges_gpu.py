@@ -268,3 +268,37 @@ def test_a_decode_that_times_out_leaves_nan_and_a_usable_context():
             bound = (u(torch.bfloat16) + 4 * ds + 2.0 ** -18) * m + u(torch.bfloat16) * want.abs()
             assert bool(((o.double() - want).abs() <= bound).all())
             assert float((lse.double() - want_lse).abs().max()) <= 2 * ds + 2.0 ** -18 * 16
+
+
+def test_a_status_word_outlives_the_workspace():
+    """A decode without a workspace of the caller's: its code, and that of a captured one, is in
+    the status word, which keeps it; a call that fits leaves it alone."""
+    p, c = plain_cache()
+    q = randn(p.B, 2, p.H, p.d_head, seed=5).cuda()
+    good, bad = torch.tensor([5, 7], **I32), torch.tensor([5, p.cap - 1], **I32)
+    status = torch.zeros(1, **I32)
+    want = focus.decode_tree(p, q, c, good)[0]
+    assert torch.equal(focus.decode_tree(p, q, c, good, status=status)[0], want) and focus.get_status(status) == 0
+    focus.decode_tree(p, q, c, bad, status=status)
+    focus.decode_tree(p, q, c, good, status=status)
+    assert focus.ERRORS[focus.get_status(status)] == "FOCUS_ERR_BOUNDS"
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    status.zero_()
+    side.wait_stream(torch.cuda.current_stream())
+    focus.decode_tree(p, q, c, bad, status=status, stream=side)
+    assert focus.ERRORS[focus.get_status(status, side)] == "FOCUS_ERR_BOUNDS"
+    torch.cuda.current_stream().wait_stream(side)
+    status.zero_()
+    lens = good.clone()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        focus.decode_tree(p, q, c, lens, status=status)
+    graph.replay()
+    assert focus.get_status(status) == 0
+    lens.copy_(bad)
+    graph.replay()
+    assert focus.ERRORS[focus.get_status(status)] == "FOCUS_ERR_BOUNDS"
+    for wrong in (torch.zeros(2, **I32), torch.zeros(1, device="cuda"), torch.zeros(1, dtype=torch.int32)):
+        with pytest.raises(focus.FocusError):
+            focus.decode_tree(p, q, c, good, status=wrong)
