@@ -379,7 +379,8 @@ typedef struct focus_strides {
  *       respect to the rotated tensors, and the outputs are those with respect to the
  *       inputs (the rotation by -pos f_i, times attn_factor)
  *   q_out, k_out  outputs; each may be its own input (same pointer, same strides) and
- *       overlaps nothing else (an output with a stride of 0 is refused)
+ *       overlaps nothing else (refused: a stride of 0, an overlap of tensors whose strides are
+ *       alike or that have no gaps; other overlaps are the caller's to avoid)
  * Pointers are aligned to the element size; 16-byte aligned pointers and strides that
  * are multiples of 16 bytes take the vector path.  Computed in fp32, rounded once.
  */
@@ -417,7 +418,8 @@ typedef struct focus_cache_params {
  * Append tokens: token t < count[b] of sequence b goes to slot start[b] + t, its key
  * rotated on the way when a rope is given.
  *   k, v       [B, T, H_kv, d_head] bf16 with strides ks, vs (16-byte aligned rows); no
- *              part of the cache lies between their first and last element
+ *              part of the cache lies between their first and last element, and none of its
+ *              arrays overlaps another or an input (refused)
  *   mask       [B, R, T] uint32 or NULL (then mask_cache is not written)
  *   start      [B] int32;  count [B] int32 or NULL (all T tokens)
  *   rope       NULL or a plan with dim <= d_head; positions [B, T] int32 or NULL: the
@@ -438,7 +440,7 @@ int focus_cache_write(const focus_cache_params* p, const uint16_t* k, const focu
  * k, v [B, T, H_kv, d_head] out, token t from slot start[b] + t (start NULL: 0); tokens
  * from count[b] on (count NULL: none) are zeros, and so are tokens outside the cache,
  * which set `status` as in focus_cache_write.  k and v overlap neither each other nor the
- * cache.
+ * cache nor start and count (refused).
  */
 int focus_cache_read(const focus_cache_params* p, const void* k_cache, const void* v_cache,
                      const float* k_scale, const float* v_scale, const int32_t* start,
@@ -465,8 +467,8 @@ int focus_cache_read(const focus_cache_params* p, const void* k_cache, const voi
  * get zeros and -inf, and nothing of it is read.  A wait inside a kernel that runs out
  * raises FOCUS_ERR_TIMEOUT there, and the rows it spoilt are NaN.
  *   ws    focus_decode_tree_workspace_size(p) bytes, 256-byte aligned; of one call at a
- *         time (calls that may overlap, on two streams, have one each).  o does not
- *         overlap q.
+ *         time (calls that may overlap, on two streams, have one each).  o, lse and ws
+ *         overlap neither each other nor an input (refused).
  */
 size_t focus_decode_tree_workspace_size(const focus_cache_params* p);
 int focus_decode_tree(const focus_cache_params* p, const uint16_t* q, const void* k_cache,

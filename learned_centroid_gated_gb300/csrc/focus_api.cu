@@ -5,6 +5,8 @@
 
 #include <nvtx3/nvToolsExt.h>
 
+#include <initializer_list>
+
 #include "common.cuh"
 
 namespace focus {
@@ -635,9 +637,66 @@ focus_strides dense(int N, int H, int d) {
 int64_t span(int B, int N, int H, int d, const focus_strides& s, int size) {
   return ((B - 1) * s.b + (N - 1) * s.n + (H - 1) * s.h + d) * size;
 }
-bool overlap(const void* a, int64_t na, const void* b, int64_t nb) {
-  const uintptr_t x = (uintptr_t)a, y = (uintptr_t)b;
-  return x < y + (uintptr_t)nb && y < x + (uintptr_t)na;
+// A call's dense arrays: what it writes, and what it reads (absent ones: NULL).
+struct Bytes {
+  const void* p;
+  int64_t n;
+};
+bool overlap(const Bytes& a, const Bytes& b) {
+  const uintptr_t x = (uintptr_t)a.p, y = (uintptr_t)b.p;
+  return x && y && x < y + (uintptr_t)b.n && y < x + (uintptr_t)a.n;
+}
+bool any_overlap(std::initializer_list<Bytes> out, std::initializer_list<Bytes> in) {
+  for (const Bytes* x = out.begin(); x != out.end(); ++x) {
+    for (const Bytes* y = out.begin(); y != x; ++y)
+      if (overlap(*x, *y)) return true;
+    for (const Bytes& y : in)
+      if (overlap(*x, y)) return true;
+  }
+  return false;
+}
+
+// Whether two strided tensors of B x N tokens (of their own numbers of heads) share bytes.
+// Answered exactly where the axes' strides are alike (views of one packed tensor) or neither
+// tensor has gaps; other pairs count as apart.
+struct View {
+  const void* p;
+  int H;
+  focus_strides s;
+};
+bool nested(int B, int N, int d, const View& x) {
+  const int64_t row = d, token = (x.H - 1) * x.s.h + row, seq = (N - 1) * x.s.n + token;
+  return (x.H == 1 || x.s.h >= row) && (N == 1 || x.s.n >= token) && (B == 1 || x.s.b >= seq);
+}
+bool meet(int B, int N, int d, int size, const View& x, const View& y) {
+  if (!x.p || !y.p || !nested(B, N, d, x) || !nested(B, N, d, y)) return false;
+  const bool alike = (B == 1 || x.s.b == y.s.b) && (N == 1 || x.s.n == y.s.n) && (x.H == 1 || y.H == 1 || x.s.h == y.s.h);
+  if (!alike) {
+    const int64_t nx = span(B, N, x.H, d, x.s, size), ny = span(B, N, y.H, d, y.s, size), one = (int64_t)B * N * d * size;
+    return nx == one * x.H && ny == one * y.H && overlap(Bytes{x.p, nx}, Bytes{y.p, ny});
+  }
+  // Rows i of x and j of y are `from` + (their steps along the axes) bytes apart.  All that the
+  // inner axes and a row reach is at most one step of an outer axis, so only its two steps
+  // next to -from can bring the rows within d elements of another.
+  struct Axis {
+    int64_t step, lo, hi;
+  };
+  const int64_t sh = x.H > 1 ? x.s.h : y.H > 1 ? y.s.h : d;
+  const Axis axes[3] = {{B > 1 ? x.s.b * size : 1, 1 - B, B - 1}, {N > 1 ? x.s.n * size : 1, 1 - N, N - 1}, {sh * size, 1 - x.H, y.H - 1}};
+  const int64_t from = (int64_t)((uintptr_t)y.p - (uintptr_t)x.p);
+  for (int pick = 0; pick < 8; ++pick) {
+    int64_t at = from;
+    for (int k = 0; k < 3; ++k) {
+      const Axis& a = axes[k];
+      int64_t n = -at / a.step;                   // towards zero
+      if (n * a.step > -at) --n;                  // floor
+      n += pick >> k & 1;
+      n = n < a.lo ? a.lo : n > a.hi ? a.hi : n;  // (a step out of range is no nearer)
+      at += n * a.step;
+    }
+    if (at > -(int64_t)d * size && at < (int64_t)d * size) return true;
+  }
+  return false;
 }
 // An output whose rows share elements (an expanded view) would be written twice.
 bool broadcast(int B, int N, int H, const focus_strides& s) {
@@ -714,6 +773,21 @@ int focus_rope_apply(const focus_rope* rope, int32_t dtype, int32_t B, int32_t N
   const focus_strides dq = dense(N, H, d_head), dk = dense(N, hk, d_head);
   if (broadcast(B, N, H, qos ? *qos : dq) || (k && broadcast(B, N, hk, kos ? *kos : dk)))
     return FOCUS_ERR_INVALID_ARG;
+  // an output may be its own input, and shares nothing with anything else
+  const View x[2] = {{q, H, qs ? *qs : dq}, {k, hk, ks ? *ks : dk}};
+  const View y[2] = {{q_out, H, qos ? *qos : dq}, {k ? k_out : nullptr, hk, kos ? *kos : dk}};
+  auto same = [&](const View& a, const View& b) {
+    return a.p == b.p && (B == 1 || a.s.b == b.s.b) && (N == 1 || a.s.n == b.s.n) && (a.H == 1 || a.s.h == b.s.h);
+  };
+  for (int i = 0; i < 2; ++i)
+    for (int j = 0; j < 2; ++j)
+      if (y[i].p && !(i == j && same(x[i], y[i])) && meet(B, N, d_head, (int)size, x[j], y[i])) return FOCUS_ERR_INVALID_ARG;
+  if (meet(B, N, d_head, (int)size, y[0], y[1])) return FOCUS_ERR_INVALID_ARG;
+  for (const View& o : y) {
+    const int64_t n = o.p ? span(B, N, o.H, d_head, o.s, (int)size) : 0;
+    if (n == (int64_t)B * N * o.H * d_head * (int64_t)size && overlap(Bytes{o.p, n}, Bytes{positions, (int64_t)B * N * 4}))
+      return FOCUS_ERR_INVALID_ARG;
+  }
   return cuda_rc(launch_rope(*rope, dtype, B, N, H, hk, d_head, q, qs ? *qs : dq, k, ks ? *ks : dk,
                              positions, offset, inverse != 0, q_out, qos ? *qos : dq, k_out,
                              kos ? *kos : dk, (cudaStream_t)stream));
@@ -736,11 +810,13 @@ int focus_cache_write(const focus_cache_params* p, const uint16_t* k, const focu
       !aligned(positions, 4) || !aligned(status, 4))
     return FOCUS_ERR_ALIGNMENT;
   // rows leave for other slots while others are still read
-  const int64_t cache = cache_bytes(p), nk = span(p->B, p->T, p->H_kv, p->d_head, sk, 2),
-                nv = span(p->B, p->T, p->H_kv, p->d_head, sv, 2);
-  if (overlap(k_cache, cache, v_cache, cache) || overlap(k, nk, k_cache, cache) || overlap(k, nk, v_cache, cache) ||
-      overlap(v, nv, k_cache, cache) || overlap(v, nv, v_cache, cache))
-    return FOCUS_ERR_INVALID_ARG;
+  const int64_t cache = cache_bytes(p), words = (int64_t)p->B * p->T * 4;
+  const int64_t scales = (int64_t)p->B * p->H_kv * p->cap * 4;
+  const std::initializer_list<Bytes> out = {{k_cache, cache}, {v_cache, cache}, {k_scale, scales}, {v_scale, scales},
+                       {mask ? mask_cache : nullptr, (int64_t)p->B * p->R * p->cap * 4}};
+  const std::initializer_list<Bytes> in = {{k, span(p->B, p->T, p->H_kv, p->d_head, sk, 2)}, {v, span(p->B, p->T, p->H_kv, p->d_head, sv, 2)},
+                      {mask, words * p->R}, {start, (int64_t)p->B * 4}, {count, (int64_t)p->B * 4}, {positions, words}};
+  if (any_overlap(out, in)) return FOCUS_ERR_INVALID_ARG;
   return cuda_rc(launch_cache_write(*p, k, sk, v, sv, mask, start, count, rope, positions, k_cache,
                                     v_cache, k_scale, v_scale, mask_cache, status,
                                     (cudaStream_t)stream));
@@ -757,9 +833,11 @@ int focus_cache_read(const focus_cache_params* p, const void* k_cache, const voi
       !aligned(status, 4))
     return FOCUS_ERR_ALIGNMENT;
   const int64_t cache = cache_bytes(p), n = (int64_t)p->B * p->T * p->H_kv * p->d_head * 2;
-  if (overlap(k, n, v, n) || overlap(k, n, k_cache, cache) || overlap(k, n, v_cache, cache) ||
-      overlap(v, n, k_cache, cache) || overlap(v, n, v_cache, cache))
-    return FOCUS_ERR_INVALID_ARG;
+  const int64_t scales = (int64_t)p->B * p->H_kv * p->cap * 4;
+  const std::initializer_list<Bytes> out = {{k, n}, {v, n}};
+  const std::initializer_list<Bytes> in = {{k_cache, cache}, {v_cache, cache}, {k_scale, scales}, {v_scale, scales},
+                      {start, (int64_t)p->B * 4}, {count, (int64_t)p->B * 4}};
+  if (any_overlap(out, in)) return FOCUS_ERR_INVALID_ARG;
   return cuda_rc(launch_cache_read(*p, k_cache, v_cache, k_scale, v_scale, start, count, k, v, status,
                                    (cudaStream_t)stream));
 }
@@ -783,9 +861,12 @@ int focus_decode_tree(const focus_cache_params* p, const uint16_t* q, const void
   if (!ws) return FOCUS_ERR_INVALID_ARG;
   if (!aligned(ws, 256)) return FOCUS_ERR_ALIGNMENT;
   if (ws_bytes < tree_workspace_bytes(*p)) return FOCUS_ERR_WORKSPACE;
-  // (q is read again, for rows that come out not finite, while other rows of o are written)
-  const int64_t n = (int64_t)p->B * p->T * p->H * p->d_head * 2;
-  if (overlap(q, n, o, n)) return FOCUS_ERR_INVALID_ARG;
+  // (for rows that come out not finite the inputs are read while other rows of o are written)
+  const int64_t rows = (int64_t)p->B * p->T * p->H, cache = cache_bytes(p), scales = (int64_t)p->B * p->H_kv * p->cap * 4;
+  const std::initializer_list<Bytes> out = {{o, rows * p->d_head * 2}, {lse, rows * 4}, {ws, (int64_t)tree_workspace_bytes(*p)}};
+  const std::initializer_list<Bytes> in = {{q, rows * p->d_head * 2}, {k_cache, cache}, {v_cache, cache}, {k_scale, scales}, {v_scale, scales},
+                      {mask_cache, (int64_t)p->B * p->R * p->cap * 4}, {lens, (int64_t)p->B * 4}, {tree, (int64_t)p->B * p->T * 8}};
+  if (any_overlap(out, in)) return FOCUS_ERR_INVALID_ARG;
   const float scale = p->softmax_scale > 0.0f ? p->softmax_scale : 1.0f / sqrtf((float)p->d_head);
   return cuda_rc(launch_decode_tree(*p, reinterpret_cast<const bf16*>(q), k_cache, v_cache, k_scale,
                                     v_scale, mask_cache, lens, tree, reinterpret_cast<bf16*>(o), lse,
@@ -856,7 +937,7 @@ const char* focus_strerror(int code) {
   }
 }
 
-int focus_version(void) { return (1 << 16) | 1; }
+int focus_version(void) { return (1 << 16) | 2; }
 
 const char* focus_cuda_error_string(void) {
   return g_last_cuda_error == cudaSuccess ? "no CUDA error" : cudaGetErrorString(g_last_cuda_error);

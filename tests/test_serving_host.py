@@ -1,12 +1,15 @@
-"""Host side of the serving calls (no GPU needed): plans that are copied, pickled and shared."""
+"""Host side of the serving calls (no GPU needed): plans that are copied, pickled and shared,
+tensors that overlap."""
 import copy
 import ctypes
 import gc
 import multiprocessing
 import pickle
+import random
 import threading
 
 import pytest
+import torch
 
 import learned_centroid_gated_gb300 as focus
 
@@ -89,3 +92,94 @@ def test_cache_params_shared_by_threads():
     [t.start() for t in threads]
     [t.join() for t in threads]
     assert not bad
+
+
+# ------------------------------------------------------------------------- overlaps --
+host_only = pytest.mark.skipif(torch.cuda.is_available(), reason="passes made-up device addresses; host-only check")
+BAD, CUDA = -1, -4  # refused; gone on to the launch, which a machine without a GPU fails
+AT = 1 << 20
+
+
+def rope_call(B, N, d, size, views, positions=None):
+    """focus_rope_apply on made-up addresses: views of q, k, q_out, k_out as (address, heads, strides)."""
+    plan = focus.Rope(dim=64)
+    arg = []
+    for v in views:
+        arg += [None, None] if v is None else [ctypes.c_void_p(v[0]), ctypes.byref(focus._Strides(*v[2]))]
+    return focus._lib.focus_rope_apply(plan._addr, 2 if size == 4 else 0, B, N, views[0][1], views[1][1] if views[1] else 0,
+                                       d, *arg[:4], positions, 0, 0, *arg[4:], None)
+
+
+def elements(B, N, d, size, v):
+    return {v[0] + size * (b * v[2][0] + n * v[2][1] + h * v[2][2]) + i
+            for b in range(B) for n in range(N) for h in range(v[1]) for i in range(0, d * size, size)}
+
+
+@host_only
+def test_rotation_refuses_outputs_that_overlap():
+    """Packed views, shifted views, dense tensors side by side: refused exactly where elements are
+    shared, by the elements themselves."""
+    rng = random.Random(1)
+    d, size, refused, taken = 64, 4, 0, 0
+    for _ in range(3000):
+        B, N, H, H_kv = rng.choice([1, 2, 3]), rng.choice([1, 2, 5]), rng.choice([1, 2, 4]), rng.choice([1, 2])
+        sh = rng.choice([d, d, d + 4, 2 * d])
+        heads = rng.choice([H + H_kv, H + H_kv + 3])
+        sn = heads * sh + rng.choice([0, 0, 8])
+        sb = N * sn + rng.choice([0, 0, sn, 12])
+        at = lambda: AT + size * rng.choice([0, 4, sh * rng.randrange(-2, heads + 1), sn * rng.randrange(-1, N + 2) + sh * rng.randrange(0, 3),
+                                             sb * rng.randrange(-1, B + 1), rng.randrange(-2 * sn, 2 * sb)])
+        q, k = (AT, H, (sb, sn, sh)), (AT + size * H * sh, H_kv, (sb, sn, sh))
+        qo = q if rng.random() < 0.3 else (at(), H, (sb, sn, sh))
+        ko = k if rng.random() < 0.3 else (at(), H_kv, (sb, sn, sh))
+        sets = [elements(B, N, d, size, v) for v in (q, k, qo, ko)]
+        meet = lambda i, j: bool(sets[i] & sets[j])
+        want = meet(2, 3) or meet(1, 2) or meet(0, 3) or (qo != q and meet(0, 2)) or (ko != k and meet(1, 3))
+        got = rope_call(B, N, d, size, (q, k, qo, ko))
+        assert got == (BAD if want else CUDA), (B, N, q, k, qo, ko, got, want)
+        refused, taken = refused + want, taken + (not want)
+    assert refused > 300 and taken > 300
+    # dense tensors of different head counts; the positions
+    dense = lambda p, H: (p, H, (4 * H * d, H * d, d))
+    q, k = dense(AT, 4), dense(AT + (1 << 16), 1)
+    assert rope_call(2, 4, d, 4, (q, k, q, k)) == CUDA
+    assert rope_call(2, 4, d, 4, (q, k, dense(AT + (1 << 16) - 256, 4), k)) == BAD
+    assert rope_call(2, 4, d, 4, (q, k, q, dense(AT + 256 * 31, 1))) == BAD
+    assert rope_call(2, 4, d, 4, (q, None, q, None), ctypes.c_void_p(AT + 64)) == BAD
+    assert rope_call(2, 4, d, 4, (q, None, q, None), ctypes.c_void_p(AT + 2 * 4 * 4 * d * 4)) == CUDA
+
+
+@host_only
+def test_cache_and_decode_refuse_arrays_that_overlap():
+    """Every array that a call writes against every other one, at their first and last bytes."""
+    p = focus.CacheParams(B=2, cap=64, H=8, H_kv=2, d_head=128, R=2, K=4, top_k=2, w=16, format="int8").c(3)
+    kv, sc, ws = 2 * 64 * 2 * 128, 2 * 2 * 64 * 4, p.tree_ws
+    sizes = dict(q=2 * 3 * 8 * 128 * 2, k=2 * 3 * 2 * 128 * 2, v=2 * 3 * 2 * 128 * 2, kc=kv, vc=kv, ks=sc, vs=sc, mc=2 * 2 * 64 * 4,
+                 mask=2 * 2 * 3 * 4, n=8, count=8, pos=24, lens=8, tree=48, o=2 * 3 * 8 * 128 * 2, lse=2 * 3 * 8 * 4, ws=ws)
+    free = {name: AT + (i << 24) for i, name in enumerate(sizes)}
+    P = ctypes.c_void_p
+
+    def write(a):
+        return focus._lib.focus_cache_write(p.addr, P(a["k"]), None, P(a["v"]), None, P(a["mask"]), P(a["n"]), P(a["count"]),
+                                            None, P(a["pos"]), P(a["kc"]), P(a["vc"]), P(a["ks"]), P(a["vs"]), P(a["mc"]), None, None)
+
+    def read(a):
+        return focus._lib.focus_cache_read(p.addr, P(a["kc"]), P(a["vc"]), P(a["ks"]), P(a["vs"]), P(a["n"]), P(a["count"]),
+                                           P(a["k"]), P(a["v"]), None, None)
+
+    def decode(a):
+        return focus._lib.focus_decode_tree(p.addr, P(a["q"]), P(a["kc"]), P(a["vc"]), P(a["ks"]), P(a["vs"]), P(a["mc"]),
+                                            P(a["lens"]), P(a["tree"]), P(a["o"]), P(a["lse"]), P(a["ws"]), ws, None)
+    calls = ((write, ("kc", "vc", "ks", "vs", "mc"), ("k", "v", "mask", "n", "count", "pos")),
+             (read, ("k", "v"), ("kc", "vc", "ks", "vs", "n", "count")),
+             (decode, ("o", "lse", "ws"), ("q", "kc", "vc", "ks", "vs", "mc", "lens", "tree")))
+    for call, out, inp in calls:
+        assert call(free) == CUDA
+        for x in out:
+            for y in out + inp:
+                if x == y:
+                    continue
+                last = free[y] + (sizes[y] - 1) // 256 * 256
+                assert call({**free, x: free[y]}) == call({**free, x: last}) == BAD, (call.__name__, x, y)
+                end = free[y] + (sizes[y] + 255) // 256 * 256
+                assert call({**free, x: end}) == CUDA, (call.__name__, x, y)
