@@ -537,6 +537,7 @@ class _Launch:
     that what is allocated meanwhile belongs to that stream; gives the raw stream."""
 
     def __init__(self, index: int, stream):
+        _require(stream is None or stream.device_index == index, "stream of another device than the tensors'")
         self.index = index
         self.device = None if _current_device() == index else torch.cuda.device(index)
         self.stream = None if stream is None else torch.cuda.stream(stream)

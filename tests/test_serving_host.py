@@ -7,6 +7,7 @@ import multiprocessing
 import pickle
 import random
 import threading
+import types
 
 import pytest
 import torch
@@ -92,6 +93,13 @@ def test_cache_params_shared_by_threads():
     [t.start() for t in threads]
     [t.join() for t in threads]
     assert not bad
+
+
+def test_a_stream_of_another_device_is_refused():
+    """Before anything is launched: the tensors' device would not be the current one."""
+    other = types.SimpleNamespace(device=torch.device("cuda", 1), device_index=1, cuda_stream=0)
+    with pytest.raises(focus.FocusError):
+        focus._Launch(0, other)
 
 
 # ------------------------------------------------------------------------- overlaps --
