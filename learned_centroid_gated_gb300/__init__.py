@@ -562,6 +562,7 @@ def _strides_of(t: torch.Tensor):
 
 
 def _rope_call(what, rope_plan, q, k, positions, offset, out, out_k, inverse, stream):
+    _require(positions is None or offset == 0, what + ": positions and offset given together")
     dev, dtype = q.get_device(), q.dtype
     code = _ROPE_DTYPES.get(dtype)
     _require(dev >= 0 and code is not None and q.dim() == 4 and q.stride(3) == 1, what)
@@ -603,7 +604,7 @@ def rope(plan: Rope, q: torch.Tensor, k: torch.Tensor | None = None, *, position
          out=None, out_k=None, stream=None):
     """Rotary positions of q [B, N, H, d] and, in the same launch, k [B, N, H_kv, d] (bf16,
     fp16 or fp32; strided views with consecutive columns are fine).  Token n stands at
-    offset + n, or at positions[b, n] (int32).  out / out_k may be q / k themselves.
+    offset + n, or at positions[b, n] (int32; not both).  out / out_k may be q / k themselves.
     An input may be a broadcast view, an output not.  Returns the rotated q, or (q, k)."""
     return _rope_call("focus_rope_apply", plan, q, k, positions, offset, out, out_k, 0, stream)
 

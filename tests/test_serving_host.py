@@ -102,6 +102,14 @@ def test_a_stream_of_another_device_is_refused():
         focus._Launch(0, other)
 
 
+@pytest.mark.parametrize("call", [focus.rope, focus.rope_bwd])
+def test_positions_and_an_offset_together_are_refused(call):
+    """One of them would be ignored without a word."""
+    x, pos = torch.zeros(1, 2, 1, 64), torch.zeros(1, 2, dtype=torch.int32)
+    with pytest.raises(focus.FocusError, match="positions and offset"):
+        call(focus.Rope(dim=64), x, positions=pos, offset=3)
+
+
 # ------------------------------------------------------------------------- overlaps --
 host_only = pytest.mark.skipif(torch.cuda.is_available(), reason="passes made-up device addresses; host-only check")
 BAD, CUDA = -1, -4  # refused; gone on to the launch, which a machine without a GPU fails
