@@ -329,8 +329,10 @@ int focus_attn_bwd_ev(const focus_params* p, const uint16_t* q, const uint16_t* 
  *   BY_PARTS  f_i (1 - keep) / factor + f_i keep with keep = clamp((orig_len f_i / 2 pi -
  *             beta_slow) / (beta_fast - beta_slow), 0, 1): pairs that turn often inside
  *             the original context stay, slow ones are stretched
- * The angle is exact for every 32-bit position: the plan holds f_i as a 64-bit
- * fraction of a turn, and pos * f_i modulo one turn is a 64-bit integer product.
+ * The plan holds f_i as the nearest 64-bit fraction of a turn, and pos * f_i modulo one
+ * turn is a 64-bit integer product, of which the upper 32 bits go to the cosine and sine:
+ * the angle is right to |pos| 2^-65 + 2^-32 turns (2^-31 at any 32-bit position; 2^-25 at
+ * an offset of 2^40) before its rounding to fp32.
  */
 enum focus_rope_layout { FOCUS_ROPE_HALF = 0, FOCUS_ROPE_INTERLEAVED = 1 };
 enum focus_rope_scaling {

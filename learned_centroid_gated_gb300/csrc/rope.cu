@@ -280,6 +280,44 @@ cudaError_t launch_rope(const focus_rope& rope, int dtype, int B, int N, int H, 
   return launch_d<bf16>(a, d, chunks, s);
 }
 
+namespace {
+
+// Sums of two doubles, about 106 bits: the plan's frequencies are needed to 2^-64 of a turn.
+struct Twice {
+  double h, l;
+};
+Twice sum(double a, double b) {  // exact
+  const double s = a + b, t = s - a;
+  return {s, (a - (s - t)) + (b - t)};
+}
+Twice operator+(Twice a, Twice b) {
+  const Twice s = sum(a.h, b.h);
+  return sum(s.h, s.l + (a.l + b.l));
+}
+Twice operator-(Twice a, Twice b) { return a + Twice{-b.h, -b.l}; }
+Twice operator*(Twice a, Twice b) {
+  const double p = a.h * b.h;
+  return sum(p, fma(a.h, b.h, -p) + (a.h * b.l + a.l * b.h));
+}
+Twice operator/(Twice a, Twice b) {  // a quotient, and that of what it leaves
+  const Twice q{a.h / b.h, 0.0}, r = a - b * q;
+  const Twice q2{r.h / b.h, 0.0}, r2 = r - b * q2;
+  return q + q2 + Twice{r2.h / b.h, 0.0};
+}
+// x^(-1/k), x >= 1: Newton's step for y^-k = x, which doubles the digits, from the library's value.
+Twice root(Twice x, int k) {
+  Twice y{pow(x.h, -1.0 / k), 0.0};
+  for (int step = 0; step < 2; ++step) {
+    Twice power{1.0, 0.0}, square = y;
+    for (int n = k; n; n >>= 1, square = square * square)
+      if (n & 1) power = power * square;
+    y = y + y * (Twice{1.0, 0.0} - x * power) / Twice{(double)k, 0.0};
+  }
+  return y;
+}
+
+}  // namespace
+
 int rope_plan(const focus_rope_params& p, focus_rope* out) {
   if (p.dim < 2 || p.dim % 2 || p.dim > 128) return FOCUS_ERR_INVALID_ARG;
   if (p.layout != FOCUS_ROPE_HALF && p.layout != FOCUS_ROPE_INTERLEAVED) return FOCUS_ERR_INVALID_ARG;
@@ -292,29 +330,35 @@ int rope_plan(const focus_rope_params& p, focus_rope* out) {
   if (parts && (p.orig_len < 1 || !(p.beta_slow >= 0.0) || !(p.beta_fast > p.beta_slow) ||
                 !isfinite(p.beta_fast)))
     return FOCUS_ERR_INVALID_ARG;
-  const double two_pi = 6.283185307179586476925;
-  double base = p.base;
-  if (p.scaling == FOCUS_ROPE_SCALING_NTK)
-    base *= pow(p.factor, (double)p.dim / (p.dim > 2 ? p.dim - 2 : 1));
+  const Twice two_pi{6.283185307179586, 2.4492935982947064e-16}, one{1.0, 0.0};
+  const Twice factor{p.factor, 0.0};
+  Twice base{p.base, 0.0};
+  // factor^(dim / (dim - 2)); dim = 2 has pair 0 alone, which no base stretches
+  if (p.scaling == FOCUS_ROPE_SCALING_NTK && p.dim > 2) base = base * factor / root(factor, (p.dim - 2) / 2);
+  const Twice ratio = root(base, p.dim / 2);  // f_i = ratio^i
   out->dim = p.dim;
   out->layout = p.layout;
   out->reserved = 0;
   out->attn_factor =
       (float)(p.attn_factor > 0.0 ? p.attn_factor : parts ? 0.1 * log(p.factor) + 1.0 : 1.0);
+  Twice power = one;
   for (int i = 0; i < 64; ++i) {
-    if (i >= p.dim / 2) {
-      out->turn[i] = 0;
-      continue;
-    }
-    double f = pow(base, -2.0 * i / p.dim);
-    if (p.scaling == FOCUS_ROPE_SCALING_LINEAR) f /= p.factor;
+    out->turn[i] = 0;
+    if (i >= p.dim / 2) continue;
+    Twice f = power;
+    power = power * ratio;
+    if (p.scaling == FOCUS_ROPE_SCALING_LINEAR) f = f / factor;
     if (parts) {
-      const double turns = p.orig_len * f / two_pi;
-      double keep = (turns - p.beta_slow) / (p.beta_fast - p.beta_slow);
-      keep = keep < 0.0 ? 0.0 : keep > 1.0 ? 1.0 : keep;
-      f = f * (1.0 - keep) / p.factor + f * keep;
+      const Twice turns = Twice{(double)p.orig_len, 0.0} * f / two_pi;
+      Twice keep = (turns - Twice{p.beta_slow, 0.0}) / sum(p.beta_fast, -p.beta_slow);
+      if (keep.h < 0.0) keep = Twice{0.0, 0.0};
+      if (keep.h >= 1.0) keep = one;
+      f = f * (one - keep) / factor + f * keep;
     }
-    out->turn[i] = (uint64_t)(f / two_pi * 18446744073709551616.0);  // f <= 1: below 2^62
+    // f <= 1: a turn below 2^62; its whole part, and the rest rounded
+    const Twice t = f / two_pi;
+    const double high = t.h * 18446744073709551616.0, whole = floor(high);
+    out->turn[i] = (uint64_t)whole + (uint64_t)llrint((high - whole) + t.l * 18446744073709551616.0);
   }
   return FOCUS_OK;
 }

@@ -2,6 +2,7 @@
 tensors that overlap."""
 import copy
 import ctypes
+import decimal
 import gc
 import multiprocessing
 import pickle
@@ -108,6 +109,54 @@ def test_positions_and_an_offset_together_are_refused(call):
     x, pos = torch.zeros(1, 2, 1, 64), torch.zeros(1, 2, dtype=torch.int32)
     with pytest.raises(focus.FocusError, match="positions and offset"):
         call(focus.Rope(dim=64), x, positions=pos, offset=3)
+
+
+# ------------------------------------------------------------------------- frequencies --
+D = decimal.Decimal
+
+
+def two_pi():
+    """By Machin's formula, to the context's digits."""
+    def atan_of_one_over(n):
+        x, total, k = D(1) / n, D(0), 0
+        while abs(x) > D(10) ** -(decimal.getcontext().prec + 2):
+            total += x / (2 * k + 1) if k % 2 == 0 else -x / (2 * k + 1)
+            x, k = x / (n * n), k + 1
+        return total
+    return 8 * (4 * atan_of_one_over(5) - atan_of_one_over(239))
+
+
+def turns(dim, base=10000.0, scaling="none", factor=1.0, orig_len=4096, beta_fast=32.0, beta_slow=1.0):
+    """f_i / 2 pi to 60 digits, from the definition."""
+    pi2, base, factor = two_pi(), D(base), D(factor)
+    if scaling == "ntk":
+        base *= factor ** (D(dim) / max(dim - 2, 1))
+    for i in range(dim // 2):
+        f = base ** (D(-2 * i) / dim)
+        if scaling == "linear":
+            f /= factor
+        if scaling == "by_parts":
+            keep = min(D(1), max(D(0), (orig_len * f / pi2 - D(beta_slow)) / (D(beta_fast) - D(beta_slow))))
+            f = f * (1 - keep) / factor + f * keep
+        yield f / pi2
+
+
+@pytest.mark.parametrize("kw", [dict(dim=128), dict(dim=2), dict(dim=64, base=5e5), dict(dim=126, base=1.0), dict(dim=6, base=1e15),
+                                dict(dim=100, scaling="linear", factor=3.0), dict(dim=128, scaling="ntk", factor=8.7),
+                                dict(dim=2, scaling="ntk", factor=8.0), dict(dim=4, scaling="ntk", factor=1.1),
+                                dict(dim=128, scaling="by_parts", factor=32.0, orig_len=8192),
+                                dict(dim=96, scaling="by_parts", factor=3.3, orig_len=777, beta_fast=20.1, beta_slow=0.3)])
+def test_frequencies_are_the_nearest_64_bit_fractions(kw):
+    """Each f_i / 2 pi in units of 2^-64, so the angle of position p is off by |p| 2^-65 turns at
+    most: 2^-34 at the ends of 32 bits.  (Half a unit, and 2^-96 relative of the way there.)"""
+    with decimal.localcontext() as ctx:
+        ctx.prec = 60
+        plan = focus.Rope(**kw)._plan
+        want = [t * 2 ** 64 for t in turns(**kw)]
+        assert len(want) == kw["dim"] // 2
+        for got, exact in zip(plan.turn, want):
+            assert abs(got - exact) <= D("0.5") + D("0.0001"), (got, exact)
+        assert not any(plan.turn[len(want):])
 
 
 # ------------------------------------------------------------------------- overlaps --
