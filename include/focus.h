@@ -438,7 +438,9 @@ int focus_cache_write(const focus_cache_params* p, const uint16_t* k, const focu
                       float* v_scale, uint32_t* mask_cache, int32_t* status, void* stream);
 
 /*
- * Read tokens back as bf16 (e.g. the prefix of a further prompt for focus_attn_fwd):
+ * Read tokens back as bf16.  (focus_attn_fwd takes N queries for N keys: a further prompt
+ * on a prefix read back goes through it with queries for the prefix too, whose rows are
+ * worked out and left; focus_decode_tree takes up to 64 new tokens on the cache itself.)
  * k, v [B, T, H_kv, d_head] out, token t from slot start[b] + t (start NULL: 0); tokens
  * from count[b] on (count NULL: none) are zeros, and so are tokens outside the cache,
  * which set `status` as in focus_cache_write.  k and v overlap neither each other nor the
@@ -450,7 +452,8 @@ int focus_cache_read(const focus_cache_params* p, const void* k_cache, const voi
 
 /*
  * Decode step for T <= FOCUS_MAX_DRAFT drafted tokens per sequence over a cache in any
- * format (T = 1: the next token of sequences of different lengths).  Sequence b holds
+ * format (T = 1: the next token of sequences of different lengths; focus_decode is the step
+ * of bf16 sequences of one length N, without a cache's capacity or drafted tokens).  Sequence b holds
  * lens[b] tokens in slots 0 .. lens[b] - 1; its drafted tokens' keys, values and masks
  * stand in slots lens[b] + u (focus_cache_write puts them there, with
  * positions lens[b] + depth when they form a tree).

@@ -562,7 +562,7 @@ def _strides_of(t: torch.Tensor):
 
 
 def _rope_call(what, rope_plan, q, k, positions, offset, out, out_k, inverse, stream):
-    _require(positions is None or offset == 0, what + ": positions and offset given together")
+    _require(positions is None or offset == 0, "positions and offset given together")
     dev, dtype = q.get_device(), q.dtype
     code = _ROPE_DTYPES.get(dtype)
     _require(dev >= 0 and code is not None and q.dim() == 4 and q.stride(3) == 1, what)
@@ -730,7 +730,8 @@ def cache_write(p: CacheParams, cache: KVCache, k: torch.Tensor, v: torch.Tensor
 def cache_read(p: CacheParams, cache: KVCache, T: int, start=None, count=None, *, out=None, status=None,
                stream=None):
     """k, v [B, T, H_kv, d] bf16 of the tokens in slots start[b] + t (start None: 0), zeros
-    for t >= count[b]; e.g. the prefix of a further prompt for attn_fwd.  out: (k, v) to fill."""
+    for t >= count[b].  out: (k, v) to fill.  (attn_fwd takes as many queries as keys: a further
+    prompt on a prefix read back needs queries for the prefix too, whose rows are left.)"""
     what = "focus_cache_read"
     dev, kc, vc, ksc, vsc, _ = cache._args(p, what)
     shape = (p.B, T, p.H_kv, p.d_head)
@@ -759,7 +760,8 @@ def decode_tree(p: CacheParams, q: torch.Tensor, cache: KVCache, lens: torch.Ten
     int32 tokens in the cache before them; the drafted tokens' own keys, values and masks stand
     in slots lens[b] + u.  tree [B, T] int64: bit u of word t set when drafted token u is an
     ancestor of t or t itself (None: a chain; a word of 0 marks a row that is no token).
-    T = 1 is the plain next token of sequences of different lengths.  ws: a workspace of
+    T = 1 is the plain next token of sequences of different lengths (decode: of bf16 sequences of
+    one length).  ws: a workspace of
     decode_tree_workspace_size(p, T) bytes, of one call at a time; get_status(ws) reads the
     call's status (FOCUS_ERR_BOUNDS where a length does not fit: zeros and -inf; FOCUS_ERR_TIMEOUT:
     NaN).  status: an int32 device word, as in cache_write, that keeps the lowest code of all

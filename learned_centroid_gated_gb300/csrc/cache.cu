@@ -6,10 +6,10 @@
 // (int8).  Memory-bound: each bf16 row is read once, its codes written once.  A warp takes
 // one token: a key's cosines and sines are computed once and serve all KV heads, the row
 // maximum is a shuffle over the row's D / 16 lanes, and the codes leave from registers.
-// Measured, e4m3, d = 128: 32K tokens of 32 KV heads written with rotation, 136 us (6.0 TB/s;
-// after the memory come the instructions, 0.59 of the issue slots); 128K tokens of 8 KV heads
-// read back, 116 us (7.0 TB/s); one token of each of 32 sequences, 4.2 us, which is the launch
-// and three dependent reads.
+// Measured, e4m3, d = 128: 32K tokens of 32 KV heads written with rotation, 134 us (6.1 TB/s;
+// after the memory come the instructions, 0.59 of the issue slots), in bf16 158 us (6.8 TB/s); 128K
+// tokens of 8 KV heads read back, 116 us (7.0 TB/s); one token of each of 32 sequences, 4.2 us,
+// which is the launch and three dependent reads.
 #include <cuda_fp8.h>
 #include <math.h>
 
@@ -247,8 +247,8 @@ __global__ void __launch_bounds__(256, MODE == kHalfAny ? 3 : 4) cache_write(con
   }
   // Rows h0 .. h1 - 1 of the keys or of the values.  Every lane takes part in every pass (the
   // row maximum is a shuffle); rows past the end are not loaded or stored.  The loads of two
-  // passes are in flight together, and four blocks on an SM (136 us for the prompt above; one
-  // pass 152, four 149, three blocks 149).
+  // passes are in flight together, and four blocks on an SM (the prompt above, then
+  // 136 us: one pass 152, four 149, three blocks 149).
   auto rows = [&](auto is_key, const uint16_t* src, const focus_strides& st, void* cache, float* scale, int h0, int h1) {
     constexpr int U = 2;
     const bf16* x = reinterpret_cast<const bf16*>(src) + b * st.b + t * st.n + (h0 + sub) * st.h;

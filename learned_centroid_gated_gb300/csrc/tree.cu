@@ -13,10 +13,13 @@
 //                 softmax per row; both products are m16n8k16 register-fragment MMAs.
 //   tree_combine  merges a row's slices by their maxima: O, LSE.
 // Measured, one token per sequence, 32 / 8 heads of 128: 32 sequences of up to 32K bf16 keys
-// 175 us (6.1 TB/s), e4m3 108 us (5.1 TB/s); 128K int8 keys and 4 tokens (16 rows) 90 us; 4
-// sequences of up to 1000 keys (12 heads of 64) 8.6 us and 4.1 for the merge, of which the memory
-// needs 0.8: the kernels' starts, the listing and dependent reads.  In bf16 the memory bounds it; in 8 bits the instructions per key
-// (conversion, scales, exponentials: 8 rows, 16 twice the accumulators) do.
+// 175 us (6.1 TB/s), e4m3 110 us (5.0 TB/s), int8 121; 4 tokens (16 rows) over 128K keys, bf16 90 us,
+// e4m3 85, int8 93; 4 sequences of up to 1000 keys (12 heads of 64) 8.7 us and 4.1 for the merge, of
+// which the memory needs 0.8: the kernels' starts, the listing and dependent reads.  In bf16 the
+// memory bounds it.  In 8 bits neither the memory (0.64 of its rate with 8 rows, 0.36 with 16) nor
+// the issue slots (0.47, 0.41) are full: a warp's chain of conversion, scales and exponentials per
+// tile, with 2.75 and 2 warps a scheduler to overlap, at 168 registers (D = 128: 152 bytes of
+// them spilled) and 255.
 #include <math.h>
 
 #include <algorithm>
@@ -377,8 +380,10 @@ tree_split(const __grid_constant__ TreeArgs a) {
           }
         }
       }
-      float corr[RL];           // of acc
-      uint32_t pa[RL][2 * KH];  // P rounded for the tensor core; l sums it unrounded
+      // P is rounded for the tensor core (bf16, as in the forward pass; in 8 bits times V's scale,
+      // once, to fp16); l sums it unrounded.
+      float corr[RL];  // of acc
+      uint32_t pa[RL][2 * KH];
 #pragma unroll
       for (int r = 0; r < RL; ++r) {
         float mt = -INFINITY, mv = -INFINITY;  // largest logit; 8-bit formats: with V's scale

@@ -23,12 +23,15 @@
 //               warpgroup, and eight loader warps, since the codes' conversion, not the
 //               softmax, is the longer chain (64 rows over 128K int8 keys: 158 us with two
 //               softmax warpgroups by turns and four loader warps, 141 so; bf16 114 and 117).
-// Measured: 64 drafts of 32 / 8 heads over a million bf16 keys 1.19 ms, 3.4 TB/s and 0.88
+// Measured: 64 drafts of 32 / 8 heads over a million bf16 keys 1.20 ms, 3.4 TB/s and 0.88
 // PFLOP/s (the products alone would take 0.53 ms at the peak rate); 16 drafts over 128K keys
-// 117 us bf16 (4.6 TB/s), 141 us int8 (2.0 TB/s).  What bounds it: with 256 rows the thread
-// that issues the MMAs; with fewer rows the softmax warps' instructions (1800 cycles a tile of
-// int8, 1200 of bf16, against 740 and 1400 that its bytes take); 8-bit codes cost the
-// conversion and the scales on top, so that they save less time than bytes.
+// 117 us bf16 (4.6 TB/s), 144 us int8 (1.9 TB/s); 64 drafts over 128K 179 and 236 us.  What bounds
+// it: with 256 rows nothing is full (of 2700 cycles a tile the issuer is busy 1200, the tensor
+// pipe a third, DRAM 0.38): a half's S, softmax and P V follow one another, since P lies over S and
+// its next S waits for its last P V.  With fewer rows and int8 the softmax warps' instructions
+// (1800 cycles of a tile's 2500, its bytes 740); with bf16 the bytes' 1400 and the softmax's 1200
+// of 2000, partly in turn.  8-bit codes cost the conversion and the scales on top, so that they
+// save less time than bytes.
 // The roles' loops share the instruction cache: the code is kept short rather than unrolled
 // (the conversion's loop unrolled by 4: 157 -> 172 us, by 2 the least).
 // The scales of 8-bit rows: K's multiplies the logits; V's multiplies P, and the reference of
@@ -50,7 +53,6 @@ namespace {
 
 using namespace ptx;
 using wmma16::cp_async16;
-using wmma16::cp_async4;
 using wmma16::cp_async_commit;
 using wmma16::cp_async_wait;
 using wmma16::lds128;

@@ -48,7 +48,8 @@ def dense(p, c, q, lens):
             for h in range(g * gq, (g + 1) * gq):
                 s = (q[b, :, h].cuda().double() @ k.T) * p.scale
                 s = s.masked_fill(~see, -math.inf)
-                lse[b, h] = torch.logsumexp(s, 1)
+                top = s.amax(1)
+                lse[b, h] = top + (s - top[:, None]).exp().sum(1).log()
                 w = (s - lse[b, h][:, None]).exp()
                 o[b, :, h], m[b, :, h] = w @ v, w @ v.abs()
                 if vs is not None:
