@@ -630,6 +630,18 @@ __device__ float keys_by_hand(const TreeArgs& a, const RowParts& rp, int t, int 
   float qf[V];
 #pragma unroll
   for (int v = 0; v < V; ++v) qf[v] = __bfloat162float(q[v]);
+  float fac = a.sl2;
+  if constexpr (FMT != FOCUS_CACHE_BF16) {  // (scaled as in the kernels: a large query times codes may pass fp32)
+    float mx = 0.0f, up, down;
+#pragma unroll
+    for (int v = 0; v < V; ++v) mx = fmaxf(mx, fabsf(qf[v]));
+#pragma unroll
+    for (int o = 16; o; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
+    row_unit(mx, up, down);
+    fac *= down;
+#pragma unroll
+    for (int v = 0; v < V; ++v) qf[v] *= up;
+  }
   const int64_t sc = ((int64_t)b * a.H_kv + kvh) * a.cap, row0 = ((int64_t)b * a.cap * a.H_kv + kvh) * D;
   const int64_t kvrow = (int64_t)a.H_kv * D;
   float out = 0.0f;
@@ -671,8 +683,9 @@ __device__ float keys_by_hand(const TreeArgs& a, const RowParts& rp, int t, int 
         for (int o = 16; o; o >>= 1) x[u] += __shfl_xor_sync(0xffffffffu, x[u], o);
         if (lane == 0 && i0 + u * NW < n) {
           const int k = sh.key[i0 + u * NW];
-          if constexpr (FMT != FOCUS_CACHE_BF16) x[u] *= a.ks[sc + k];
-          x[u] = ex2(x[u] * a.sl2 - lse2);
+          if constexpr (FMT != FOCUS_CACHE_BF16) x[u] *= a.ks[sc + k] * fac;
+          else x[u] *= fac;
+          x[u] = ex2(x[u] - lse2);
           if constexpr (FMT != FOCUS_CACHE_BF16) x[u] *= a.vs[sc + k];
           sh.x[i0 + u * NW] = x[u];
         }

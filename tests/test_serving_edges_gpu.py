@@ -303,3 +303,34 @@ def test_a_status_word_outlives_the_workspace():
     for wrong in (torch.zeros(2, **I32), torch.zeros(1, device="cuda"), torch.zeros(1, dtype=torch.int32)):
         with pytest.raises(focus.FocusError):
             focus.decode_tree(p, q, c, good, status=wrong)
+
+
+@pytest.mark.parametrize("fmt", ["e4m3", "int8"])
+@pytest.mark.parametrize("form", FORMS)
+def test_large_queries_beside_a_key_that_is_not_finite(form, fmt):
+    """Queries near the largest bf16 number, against key scales that bring the logits back, and a
+    key of NaN that half of the tokens (of a single one's: none) see: the others keep their values."""
+    T, lens = FORMS[form], [600, 77]
+    for e in (126, -127):
+        half = 2.0 ** (-60 if e > 0 else 60)
+        p, c = codes_cache(fmt, K=2, w=4, softmax_scale=2.0 ** -e / half / math.sqrt(128))
+        c.k_scale.mul_(half)
+        q = (randn(p.B, T, p.H, p.d_head, seed=3).double().clamp(-3.9, 3.9) * 2.0 ** e).to(torch.bfloat16).cuda()
+        rest = slice(T // 2, None)
+        for b, n in enumerate(lens):
+            c.mask[b, :, n:n + T] = 1
+            c.mask[b, :, n + T // 2:n + T] = 2
+            c.mask[b, :, :n] = 3
+            c.mask[b, :, 20] = 1
+        n = torch.tensor(lens, **I32)
+        clean, clean_lse = focus.decode_tree(p, q, c, n)
+        c.v_scale[:, :, 20] = math.nan
+        got, lse = focus.decode_tree(p, q, c, n)
+        # both within their bound of the truth: m is at most the largest value, logits below 100
+        ds = p.d_head * 2.0 ** -22 * 100
+        top = float((c.v.float().abs().amax() * c.v_scale.nan_to_num().amax()))
+        bound = 2 * (u(torch.float16) + 4 * ds + 2.0 ** -18) * top + 2 * u(torch.bfloat16) * clean[:, rest].float().abs()
+        assert bool(((got[:, rest].float() - clean[:, rest].float()).abs() <= bound).all())
+        assert float((lse[..., rest] - clean_lse[..., rest]).abs().max()) <= 4 * ds
+        if T > 1:
+            assert bool(got[:, :T // 2].isnan().all())
