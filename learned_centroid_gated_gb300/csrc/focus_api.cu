@@ -670,11 +670,10 @@ bool nested(int B, int N, int d, const View& x) {
 }
 bool meet(int B, int N, int d, int size, const View& x, const View& y) {
   if (!x.p || !y.p || !nested(B, N, d, x) || !nested(B, N, d, y)) return false;
+  const int64_t nx = span(B, N, x.H, d, x.s, size), ny = span(B, N, y.H, d, y.s, size), one = (int64_t)B * N * d * size;
+  if (!overlap(Bytes{x.p, nx}, Bytes{y.p, ny})) return false;
   const bool alike = (B == 1 || x.s.b == y.s.b) && (N == 1 || x.s.n == y.s.n) && (x.H == 1 || y.H == 1 || x.s.h == y.s.h);
-  if (!alike) {
-    const int64_t nx = span(B, N, x.H, d, x.s, size), ny = span(B, N, y.H, d, y.s, size), one = (int64_t)B * N * d * size;
-    return nx == one * x.H && ny == one * y.H && overlap(Bytes{x.p, nx}, Bytes{y.p, ny});
-  }
+  if (!alike) return nx == one * x.H && ny == one * y.H;
   // Rows i of x and j of y are `from` + (their steps along the axes) bytes apart.  All that the
   // inner axes and a row reach is at most one step of an outer axis, so only its two steps
   // next to -from can bring the rows within d elements of another.
