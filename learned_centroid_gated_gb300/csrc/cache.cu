@@ -116,7 +116,7 @@ __device__ __forceinline__ void decode8(const uint2& x, float scale, float (&f)[
 // FEW: fewer KV heads than a warp's 32 / (D / 16) rows.  A warp then takes several tokens,
 // a.lanes_of of those row places each (a power of two, at least H_kv); keys and values are in
 // flight together.  4 sequences of up to 175K int8 tokens, one head of 64: 446 us with a warp per token,
-// 63 so; 200K e4m3 tokens of two heads of 128: 216 and 108; 32 tokens: 5.7 both.
+// 60 so; 200K e4m3 tokens of two heads of 128: 216 and 103; 32 tokens: 5.7 both.
 template <int D, int FMT, int MODE, bool FEW>
 __global__ void __launch_bounds__(256, MODE == kHalfAny ? 3 : 4) cache_write(const __grid_constant__ CacheArgs a) {
   using C = RowChunk<bf16>;

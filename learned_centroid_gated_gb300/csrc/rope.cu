@@ -49,7 +49,7 @@ __device__ __forceinline__ void row_of(const RopeArgs& a, int64_t b, int64_t n, 
 //   INTERLEAVED: chunks c and c + D / (2 V), V / 2 pairs each.
 // FEW: fewer heads than a warp's RPW rows.  A warp then takes U times RPW / a.lanes_of tokens, a
 // lane's group one row of each.  400K bf16 tokens of 1 + 1 heads of 64: 197 us with a warp per
-// token, 65 so; of 128: 264 and 131; 3000 tokens, where latency counts: 3.9 and 4.4.
+// token, 60 so; of 128: 264 and 124; 3000 tokens, where latency counts: 3.9 and 4.4.
 template <typename T, int D, bool HALF, bool FEW>
 __global__ void __launch_bounds__(256) rope_rows(const __grid_constant__ RopeArgs a) {
   using C = RowChunk<T>;

@@ -334,3 +334,31 @@ def test_large_queries_beside_a_key_that_is_not_finite(form, fmt):
         assert float((lse[..., rest] - clean_lse[..., rest]).abs().max()) <= 4 * ds
         if T > 1:
             assert bool(got[:, :T // 2].isnan().all())
+
+
+@pytest.mark.parametrize("layout", ["half", "interleaved"])
+def test_cosines_and_sines_to_fp32(layout):
+    """Unit vectors in fp32 turn into the cosines and sines themselves.  They are within 2
+    steps of their angle's; the angle, taken from the nearest quarter of a turn, is rounded once (2^-24 of
+    its at most an eighth of a turn) and cut off at 2^-32 of a turn.  References by the plan's own
+    64-bit fractions, which are exact here."""
+    plan = focus.Rope(dim=128, layout=layout, base=5e5)
+    N, H = 4096, 3
+    g = torch.Generator().manual_seed(6)
+    pos = torch.cat([torch.arange(N // 4), torch.randint(-(1 << 31), (1 << 31) - 1, (3 * N // 4,), generator=g)])[None]
+    x = torch.zeros(1, N, H, 128)
+    ia = torch.arange(64) if layout == "half" else 2 * torch.arange(64)
+    ib = ia + (64 if layout == "half" else 1)
+    x[..., ia] = 1.0
+    turn = torch.tensor([int(t) for t in plan._plan.turn])
+    phase = (pos[0].long()[:, None] * turn).double() * 2.0 ** -64  # wraps at 2^64: a turn
+    want = torch.cos(2 * math.pi * phase), torch.sin(2 * math.pi * phase)
+    off = (4 * phase - (4 * phase).round()).abs() * math.pi / 2  # to the nearest quarter
+    for heads in (H, 1):  # a warp per token, and several tokens per warp
+        many = 1 if heads == H else 3
+        y = focus.rope(plan, x[:, :, :heads].repeat(1, many, 1, 1).contiguous().cuda(), positions=pos.repeat(1, many).to(torch.int32).cuda())
+        for at, value, other in ((ia, want[0], want[1]), (ib, want[1], want[0])):
+            step = torch.exp2(torch.floor(torch.log2(value.abs().clamp(min=2.0 ** -100)))) * 2.0 ** -23
+            bound = 2 * step + other.abs() * (off * 2.0 ** -24 + 2 * math.pi * 2.0 ** -32) + 2.0 ** -50
+            err = (y[0, :N, :, :][..., at].double().cpu() - value[:, None]).abs()
+            assert bool((err <= bound[:, None]).all()), float((err / bound[:, None]).max())
