@@ -765,7 +765,7 @@ def decode_tree(p: CacheParams, q: torch.Tensor, cache: KVCache, lens: torch.Ten
     decode_tree_workspace_size(p, T) bytes, of one call at a time; get_status(ws) reads the
     call's status (FOCUS_ERR_BOUNDS where a length does not fit: zeros and -inf; FOCUS_ERR_TIMEOUT:
     NaN).  status: an int32 device word, as in cache_write, that keeps the lowest code of all
-    calls that it was given to; without ws and status a call's code is lost.
+    calls of one stream that it was given to; without ws and status a call's code is lost.
     Returns (o [B, T, H, d] bf16, lse [B, H, T] fp32)."""
     what = "focus_decode_tree"
     dev, kc, vc, ksc, vsc, mc = cache._args(p, what)

@@ -6,6 +6,7 @@ window and the drafted tokens form a chain, attention is causal attention: `dens
 u(t) = eps(t) / 2 is the largest relative error of one rounding to type t.
 """
 import math
+import threading
 
 import pytest
 import torch
@@ -362,3 +363,39 @@ def test_cosines_and_sines_to_fp32(layout):
             bound = 2 * step + other.abs() * (off * 2.0 ** -24 + 2 * math.pi * 2.0 ** -32) + 2.0 ** -50
             err = (y[0, :N, :, :][..., at].double().cpu() - value[:, None]).abs()
             assert bool((err <= bound[:, None]).all()), float((err / bound[:, None]).max())
+
+
+def test_calls_at_once_on_two_streams():
+    """Decodes of all forms and writes to two caches, side by side on two streams from two host
+    threads: the same bits as one after another."""
+    jobs = []
+    for i, (fmt, T) in enumerate([("int8", 1), ("e4m3", 16), ("int8", 64), ("e4m3", 4)]):
+        p, c = codes_cache(fmt, seed=i)
+        jobs.append((p, c, randn(p.B, T, p.H, p.d_head, seed=i).cuda(), torch.tensor([2000 + 300 * i, 77], **I32),
+                     randn(p.B, T, p.H_kv, p.d_head, seed=i + 9).cuda()))
+    plan = focus.Rope(dim=128)
+
+    def run(job, stream=None):
+        p, c, q, n, k = job
+        focus.cache_write(p, c, k, k, None, n, rope=plan, stream=stream)
+        return focus.decode_tree(p, focus.rope(plan, q, offset=7, stream=stream), c, n, stream=stream)
+
+    want = [run(job) for job in jobs]
+    torch.cuda.synchronize()
+    got, failed = [None] * len(jobs), []
+
+    def work(mine):
+        try:
+            stream = torch.cuda.Stream()
+            for _ in range(25):
+                for i in mine:
+                    got[i] = run(jobs[i], stream)
+            stream.synchronize()
+        except Exception as e:  # seen by the test below
+            failed.append(e)
+    threads = [threading.Thread(target=work, args=(m,)) for m in ((0, 1), (2, 3))]
+    [t.start() for t in threads]
+    [t.join() for t in threads]
+    assert not failed
+    for (o, lse), (o2, lse2) in zip(want, got):
+        assert torch.equal(o, o2) and torch.equal(lse, lse2)
