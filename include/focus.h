@@ -524,10 +524,11 @@ int focus_decode_shared(const focus_cache_params* p, const uint16_t* q, int32_t 
  *   token   [rows] int32 out;  logprob [rows] fp32 out or NULL: natural logarithm of the
  *           token's share of the weights that are left
  *   status  NULL or a device int32 that the caller zeroed (focus_get_status reads it)
- * Weights are 64-bit integers, right to about 2^-30, and sums are exact: the choice does not
- * depend on the order of sums.  A weight below 2^-44 counts as zero, a temperature below 1e-30
- * or above 1e28 as that.  A logit of -inf is never taken.  A row with a NaN or +inf, or of -inf alone, gets token -1 and a NaN, and
- * FOCUS_ERR_NONFINITE in `status`; a row whose temperature is negative or not finite, whose
+ * Weights are 64-bit integers, within 2^-29 of themselves but for what is below 2^-44 of the largest
+ * (a weight below that counts as zero), and sums are exact: the choice does not depend on the order
+ * of sums.  A temperature below 1e-30 or above 1e28 counts as that.  A logit of -inf is never taken.
+ * A row with a NaN or +inf, or of -inf alone, gets token -1 and a NaN, and FOCUS_ERR_NONFINITE in
+ * `status`; a row whose temperature is negative or not finite, whose
  * top_p is negative or NaN, whose min_p is outside [0, 1] or whose u is outside [0, 1) gets
  * the same and FOCUS_ERR_INVALID_ARG (the lowest code stays).  No workspace.  token and
  * logprob overlap neither each other nor an input (refused).

@@ -8,8 +8,8 @@
 // token is the first index i with sum_{j <= i, left} w_j > u W, W the sum of all that are left.
 //
 // Such a choice is exact or wrong, and a vocabulary has 10^5 borders that u W may fall next to.  So
-// weights are 64-bit integers, 2^44 for the largest, right to about 2^-30 of their size: the
-// exponent as a sum of two floats, 2^-x from a table of 64 entries and a polynomial.  Integer sums have
+// weights are 64-bit integers, 2^44 for the largest, right to 2^-29 of their size: the exponent to
+// 2^-31 (Weigh), 2^-x from a table of 64 entries and a polynomial.  Integer sums have
 // no order, and the thresholds found by digits (radix selection over counts, or over weights for
 // top_p) agree with the sums of the draw.
 //
@@ -106,6 +106,7 @@ struct SampleShared {
   uint32_t warp_b[kSampleWarps];
   uint32_t powers[64];
   float m, ch, cl, rh, rl;  // the largest logit; the others as in the arguments, of this row
+  float a, xh, xl;          // (see Weigh)
   // the bin that a selection has found, and the sum of those before it
   u64 above;
   int digit;
@@ -138,38 +139,51 @@ __device__ __forceinline__ float key_value(uint32_t key) {
 // The largest fp32 number below x (x not -inf).
 __device__ __forceinline__ float below(float x) { return key_value(order_key(x) - 1u); }
 
-// A row's logits against its largest, m, as weights.  WIDE: logits of more than 11 bits, whose
-// distance to m takes two floats; of 16-bit ones it does where |l| < 2^-13 |m| (2^-10 in fp16), and is
-// off by 2^-25 |m| there, which such tokens' share of the sum makes less than 2^-34 of it.
-template <bool WIDE>
+// A row's logits against its largest, m, as weights 2^-x, x = (m - l) (ch + cl).  The difference rounded
+// to fp32 would move x by up to 2^-24 of itself, where |l| and |m| lie 2^13 and more apart, and a row may be
+// of such tokens alone.  So x = (a - l) (ch + cl) + xh + xl, with products that stay whole inside an fma:
+//   a = 0 up to |m| ch = 2^11: xh + xl = m (ch + cl), xh a multiple of 2^-11, from which k / 64 can be taken
+//         without a rounding;
+//   a = m beyond, xh = xl = 0: m - l is exact for the tokens with weights, which are nearer to m than |m| / 44.
+// Weights are within 2^-29 of themselves (of which the table has 2^-30) but for the bits below 2^-44.
 struct Weigh {
-  float m, ch, cl;  // ch + cl = log2(e) / temperature
-  float far;        // a distance to m from which on a weight is zero
+  float a, ch, cl, xh, xl;  // ch + cl = log2(e) / temperature
   const uint32_t* powers;
 
-  __device__ __forceinline__ explicit Weigh(const SampleShared& sh) : m(sh.m), ch(sh.ch), cl(sh.cl), far(45.9f / sh.ch), powers(sh.powers) {}
+  __device__ __forceinline__ explicit Weigh(const SampleShared& sh) : a(sh.a), ch(sh.ch), cl(sh.cl), xh(sh.xh), xl(sh.xl), powers(sh.powers) {}
 
-  // sum + the weight of l: 22 instructions and those of the sum, no branch (the sum of one row's 131072
-  // weights is what takes longest).
+  static constexpr float kFar = 45.9f;  // octaves from which on a weight is zero
+  static constexpr float kGrid = 6144.0f, kNear = 2048.0f;  // numbers of [2^12, 2^13) are multiples of 2^-11
+  // x = k / 64 + r: a sum with this has k in its low bits, and 18 in the next six for weight()'s shift
+  static constexpr float kRound = 12582912.0f + 18.0f * 64.0f;
+  // 2^-r - 1 = r (C1 + r (C2 + r C3)) = -r ln 2 + (r ln 2)^2 / 2 - (r ln 2)^3 / 6, in units of 2^-32
+  static constexpr double kLn2 = 0.6931471805599453, kUnit = 4294967296.0;
+  static constexpr float kC1 = (float)(-kUnit * kLn2), kC2 = (float)(kUnit * kLn2 * kLn2 / 2), kC3 = (float)(-kUnit * kLn2 * kLn2 * kLn2 / 6);
+  // The row's a, xh and xl.
+  __device__ __forceinline__ static void prepare(SampleShared& sh, float m) {
+    const float x = m * sh.ch;
+    const bool near = fabsf(x) < kNear;
+    const float h = __fadd_rn(__fadd_rn(x, kGrid), -kGrid);
+    sh.a = near ? 0.0f : m;
+    sh.xh = near ? h : 0.0f;
+    sh.xl = near ? fmaf(m, sh.cl, fmaf(m, sh.ch, -h)) : 0.0f;
+  }
+  // x but for 2^-12 + 2^-14, as bins and k take it.
+  __device__ __forceinline__ float octaves(float l) const { return fminf(fmaf(a - l, ch, xh), kFar); }
+
+  // sum + the weight of l: no branch (the sum of one row's 131072 weights is what takes longest).  (A logit
+  // that is far away, or -inf, makes r infinite or NaN: its weight's digits all go in the shift.)
   __device__ __forceinline__ u64 add(u64 sum, float l) const {
-    // x = (m - l) (ch + cl) = xh + xl
-    const float d = fminf(m - l, far), xh = d * ch;
-    float xl = fmaf(d, cl, fmaf(d, ch, -xh));
-    if constexpr (WIDE) {  // (l = -inf: a NaN, which x = 45.9 makes zero)
-      const float b = (m - l) - m;
-      xl = fmaf((m - ((m - l) - b)) - (l + b), ch, xl);
-    }
-    // x = k / 64 + r; k comes in the low bits, and 18 in the next six for the shift below
-    constexpr float kRound = 12582912.0f + 18.0f * 64.0f;
-    const float t = fmaf(xh, 64.0f, kRound);
+    const float d = a - l;
+    const float t = fmaf(octaves(l), 64.0f, kRound);
     const uint32_t k = __float_as_uint(t);
-    const float r = fmaf(t - kRound, -0.015625f, xh) + xl;
-    // 2^-r - 1 = r (-a + r (a^2 / 2 - r a^3 / 6)), a = ln 2, in units of 2^-32
-    constexpr double a = 0.6931471805599453, s = 4294967296.0;
-    const float p = r * fmaf(r, fmaf(r, (float)(-s * a * a * a / 6), (float)(s * a * a / 2)), (float)(-s * a));
-    // 2^-(k % 64 / 64) 2^-r to 30 bits, 2^-(k / 64) by a shift, in units of 2^-44
-    const uint32_t w = powers[k & 63u], v = w + (uint32_t)__mulhi((int)w, __float2int_rn(p));
-    return sum + ((u64)v << 32 >> (k >> 6 & 63u));
+    const float r = fmaf(d, ch, fmaf(t - kRound, -0.015625f, xh)) + fmaf(d, cl, xl);
+    const float p = r * fmaf(r, fmaf(r, kC3, kC2), kC1);
+    return sum + weight(powers[k & 63u], __float2int_rn(p), k);
+  }
+  // 2^-(k % 64 / 64) 2^-r, r's part (p) in units of 2^-32, and 2^-(k / 64) by a shift, in units of 2^-44
+  __device__ __forceinline__ static u64 weight(uint32_t power, int p, uint32_t k) {
+    return (((u64)power << 32) + (u64)((long long)(int)power * p)) >> (k >> 6 & 63u);
   }
   // The same of two, their products and sums two at a time; x0, x1: their octaves, as bin takes them.
   __device__ __forceinline__ void pair(float l0, float l1, u64& w0, u64& w1) const {
@@ -178,39 +192,25 @@ struct Weigh {
   }
   __device__ __forceinline__ void pair(float l0, float l1, u64& w0, u64& w1, float& x0, float& x1) const {
     float d0, d1, y0, y1, t0, t1, r0, r1, p0, p1;
-    ptx::fadd2(d0, d1, m, m, -l0, -l1);
-    [[maybe_unused]] const float e0 = d0, e1 = d1;
-    d0 = fminf(d0, far), d1 = fminf(d1, far);
-    ptx::fmul2(x0, x1, d0, d1, ch, ch);
-    ptx::ffma2(y0, y1, d0, d1, ch, ch, -x0, -x1);
-    ptx::ffma2(y0, y1, d0, d1, cl, cl, y0, y1);
-    if constexpr (WIDE) {
-      float b0, b1, c0, c1;
-      ptx::fadd2(b0, b1, e0, e1, -m, -m);
-      ptx::fadd2(c0, c1, e0, e1, -b0, -b1);
-      ptx::fadd2(c0, c1, m, m, -c0, -c1);
-      ptx::fadd2(b0, b1, l0, l1, b0, b1);
-      ptx::fadd2(c0, c1, c0, c1, -b0, -b1);
-      ptx::ffma2(y0, y1, c0, c1, ch, ch, y0, y1);
-    }
-    constexpr float kRound = 12582912.0f + 18.0f * 64.0f;
+    ptx::fadd2(d0, d1, a, a, -l0, -l1);
+    ptx::ffma2(x0, x1, d0, d1, ch, ch, xh, xh);
+    x0 = fminf(x0, kFar), x1 = fminf(x1, kFar);
+    ptx::ffma2(y0, y1, d0, d1, cl, cl, xl, xl);
     ptx::ffma2(t0, t1, x0, x1, 64.0f, 64.0f, kRound, kRound);
     ptx::fadd2(r0, r1, t0, t1, -kRound, -kRound);
-    ptx::ffma2(r0, r1, r0, r1, -0.015625f, -0.015625f, x0, x1);
+    ptx::ffma2(r0, r1, r0, r1, -0.015625f, -0.015625f, xh, xh);
+    ptx::ffma2(r0, r1, d0, d1, ch, ch, r0, r1);
     ptx::fadd2(r0, r1, r0, r1, y0, y1);
-    constexpr double a = 0.6931471805599453, s = 4294967296.0;
-    constexpr float c3 = (float)(-s * a * a * a / 6), c2 = (float)(s * a * a / 2), c1 = (float)(-s * a);
-    ptx::ffma2(p0, p1, r0, r1, c3, c3, c2, c2);
-    ptx::ffma2(p0, p1, r0, r1, p0, p1, c1, c1);
+    ptx::ffma2(p0, p1, r0, r1, kC3, kC3, kC2, kC2);
+    ptx::ffma2(p0, p1, r0, r1, p0, p1, kC1, kC1);
     ptx::fmul2(p0, p1, r0, r1, p0, p1);
     const uint32_t k0 = __float_as_uint(t0), k1 = __float_as_uint(t1);
-    const uint32_t v0 = powers[k0 & 63u], v1 = powers[k1 & 63u];
-    w0 = (u64)(v0 + (uint32_t)__mulhi((int)v0, __float2int_rn(p0))) << 32 >> (k0 >> 6 & 63u);
-    w1 = (u64)(v1 + (uint32_t)__mulhi((int)v1, __float2int_rn(p1))) << 32 >> (k1 >> 6 & 63u);
+    w0 = weight(powers[k0 & 63u], __float2int_rn(p0), k0);
+    w1 = weight(powers[k1 & 63u], __float2int_rn(p1), k1);
   }
   // Bins of equal distances from m, 0 to kBins - 2, by which a first selection goes.
   static constexpr float kBinsPerOctave = 11.1f;
-  __device__ __forceinline__ int bin(float l) const { return (int)(fminf(m - l, far) * ch * kBinsPerOctave); }
+  __device__ __forceinline__ int bin(float l) const { return (int)(octaves(l) * kBinsPerOctave); }
 };
 
 // The row's 16-byte pieces: piece c has elements VEC c - lead ..; warps have runs of pieces.
@@ -338,10 +338,7 @@ __device__ __forceinline__ uint32_t warp_upto(uint32_t x, int lane) {
   }
   return x;
 }
-template <bool WIDE>
-__device__ __noinline__ u64 weight(const SampleShared& sh, float l) {
-  return Weigh<WIDE>(sh).add(0, l);
-}
+__device__ __noinline__ u64 weight(const SampleShared& sh, float l) { return Weigh(sh).add(0, l); }
 
 // The least q with q x >= n, of a quotient below 2^20 (a vocabulary's tokens), n and x positive.
 __device__ __noinline__ uint32_t times(u64 n, u64 x) {
@@ -456,7 +453,6 @@ __device__ __noinline__ void put(const SampleArgs& a, int r, const SampleShared&
 template <typename T>
 struct Sampler {
   static constexpr int VEC = Row<T>::VEC;
-  static constexpr bool WIDE = sizeof(T) == 4;
   SampleShared& sh;
   int C, rank, lane, wp;
   Row<T> row;
@@ -466,7 +462,7 @@ struct Sampler {
   int only;
   int listed;  // those of the warp's run, in its list; -1: too many for it, or none made
 
-  __device__ __forceinline__ u64 weight(float l) const { return focus::weight<WIDE>(sh, l); }
+  __device__ __forceinline__ u64 weight(float l) const { return focus::weight(sh, l); }
 
   // The warp's tokens between two bounds into its list, in order (those of other bins than `bin` among them
   // too: there are few).  Given up where it will hardly hold them all.
@@ -504,7 +500,7 @@ struct Sampler {
   __device__ __forceinline__ void visit(F&& f) const {
     const int n = listed;
     const int only = this->only;
-    const Weigh<WIDE> weigh(sh);
+    const Weigh weigh(sh);
     if (n >= 0) {
 #pragma unroll 1
       for (int i = lane; i < n; i += 32) {
@@ -614,7 +610,7 @@ struct Sampler {
       u64* h = bins();
       {
         const Row<T> row = this->row;
-        const Weigh<WIDE> weigh(sh);
+        const Weigh weigh(sh);
         row.template for_pieces<1>(row.first, row.end, lane, [&](int, const float(&l)[VEC]) {
           u64 w[VEC];
           float x[VEC];
@@ -628,13 +624,13 @@ struct Sampler {
       }
       const int bin = find(sh, C, rank, target, share, above);
       if (bin < 0) return Cut{-INFINITY, 0u};
-      // (the bin's values are inside these, whatever the roundings)
-      const Weigh<WIDE> weigh(sh);
-      const float width = 1.0f / (weigh.kBinsPerOctave * weigh.ch), slack = 1.0f + 1e-5f;
-      high = fminf(high, weigh.m - ((float)bin * width) / slack + 2.5e-7f * fabsf(weigh.m));
-      const float lowest = weigh.m - ((float)(bin + 1) * width) * slack - 2.5e-7f * fabsf(weigh.m);
-      // (a bound that all finite numbers are above, for a last bin without one)
-      least = bin < kBins - 3 ? fmaxf(least, lowest) : fmaxf(least, -3.4028234663852886e38f);
+      // (the bin's values are inside these, whatever the roundings: octaves are off by less than 2^-11)
+      const float m = sh.m, width = 1.0f / (Weigh::kBinsPerOctave * sh.ch), slack = 1.0f + 1e-5f;
+      const float off = 2.5e-7f * fabsf(m) + 0x1p-11f / sh.ch;
+      high = fminf(high, m - ((float)bin * width) / slack + off);
+      const float lowest = m - ((float)(bin + 1) * width) * slack - off;
+      // (no lower than a bound that all finite numbers are above; the last bin has no other)
+      least = fmaxf(least, fmaxf(bin < kBins - 3 ? lowest : -INFINITY, -3.4028234663852886e38f));
       list(least, high, bin);
     }
     uint32_t top = order_key(high) >> KS;  // the highest key of the bins
@@ -676,7 +672,7 @@ struct Sampler {
       n = __reduce_add_sync(0xffffffffu, n);
     } else {
       const Row<T> row = this->row;
-      const Weigh<WIDE> weigh(sh);
+      const Weigh weigh(sh);
       u64 all = 0;
       uint32_t count = 0;
 #pragma unroll 1
@@ -806,7 +802,7 @@ __global__ void __launch_bounds__(kSampleThreads, 2) sample_rows(const __grid_co
     }
     return;
   }
-  if (tid == 0) sh.m = m;
+  if (tid == 0) sh.m = m, Weigh::prepare(sh, m);
 
   // ---- one is left: the first of the largest
   if (greedy || top_k == 1 || a.V == 1) {
