@@ -551,7 +551,8 @@ int focus_sample(const focus_sample_params* p, const void* logits, const float* 
  * focus_decode_tree; token 0 is the root, a token of the sequence already (the one chosen
  * last).  From the root on, a token's first child (the lowest index) whose token is the one
  * chosen there is accepted, until there is none; with choices by focus_sample from the
- * drafted tokens' logits the sequence is distributed as without a draft.
+ * drafted tokens' logits the sequence is distributed as without a draft.  A negative token is
+ * none (focus_sample's -1 for a row without one, an empty place of a draft): it is not accepted.
  *   draft   [B, T] int32: the drafted tokens;  chosen [B, T] int32: the token chosen after each
  *   tree    [B, T] uint64 as in focus_decode_tree, or NULL: a chain.  A token's parent is the
  *           highest bit of its word below its own; a token whose word is not its parent's with
@@ -561,8 +562,8 @@ int focus_sample(const focus_sample_params* p, const void* logits, const float* 
  *   lens    [B] int32;  lens_out [B] int32 out: lens[b] + the accepted; may be lens itself
  *   count   [B] int32 out: accepted tokens, the root among them
  *   path    [B, T] int32 out: their indices, then -1
- *   next    [B] int32 out: the token chosen after the last accepted one (the next step's root),
- *           -1 where none is accepted
+ *   next    [B] int32 out: the token chosen after the last accepted one (the next step's root;
+ *           negative where that row had none), -1 where none is accepted
  *   status  NULL or a device int32 that the caller zeroed: FOCUS_ERR_BOUNDS for a lens[b] outside
  *           [0, cap - T]; such a sequence accepts nothing
  * Outputs overlap neither each other nor an input, but for lens_out (refused).  No workspace.

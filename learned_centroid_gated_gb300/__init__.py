@@ -855,7 +855,7 @@ def tree_accept(p: CacheParams, cache: KVCache, lens: torch.Tensor, draft: torch
     """The path of drafted tokens that the model's choices follow, taken into the cache: draft [B, T]
     int32 (token 0 the root, which the sequence has already), chosen [B, T] int32 the token chosen
     after each (e.g. by sample), tree as in decode_tree.  From the root on, the first child whose
-    token is the one chosen is accepted.  The accepted tokens' rows move to slots lens[b] + i.
+    token is the one chosen is accepted (a negative token is none and never is).  The accepted tokens' rows move to slots lens[b] + i.
     out_lens: where the new lengths go (lens itself is fine).  status: an int32 device word, as in
     cache_write.  Returns int32 (count [B] of accepted tokens with the root, path [B, T] of their
     indices and then -1, next [B], the token chosen after the last, or -1, and the new lens [B])."""

@@ -2,7 +2,7 @@
 // rows moved together in the cache.
 //
 // A drafted token u is right when it is the first child of its parent whose token is the one
-// chosen there, and accepted when it and all its ancestors but the root are right: no walk, one
+// chosen there (and not negative), and accepted when it and all its ancestors but the root are right: no walk, one
 // test of 64-bit words per token (a thread each), so that a tree of depth 64 takes no longer than
 // one of depth 2.  The accepted tokens are a chain 0 = u_0 < u_1 < .., and row u_i moves from slot
 // len + u_i to slot len + i: never upwards, so one thread that takes a 16-byte column of all rows
@@ -76,8 +76,9 @@ __global__ void __launch_bounds__(kAcceptThreads) accept_path(const __grid_const
     const uint64_t above = word & ((1ull << tid) - 1);
     const int parent = above ? 63 - __clzll(above) : -1;
     parents[tid] = parent;
-    // (a word that is not its parent's and its own bit is of no token of the tree)
-    const bool right = token && (parent >= 0 ? word == (words[parent] | 1ull << tid) && draft == chosen[parent]
+    // (a word that is not its parent's and its own bit is of no token of the tree; a negative token is none:
+    // the choice of a row without one, a place that the draft left empty)
+    const bool right = token && (parent >= 0 ? word == (words[parent] | 1ull << tid) && draft >= 0 && draft == chosen[parent]
                                              : tid == 0 && word == 1ull);
     const unsigned w = __ballot_sync(0xffffffffu, right);
     if (lane == 0) bits[0][wp] = w;

@@ -109,6 +109,32 @@ def test_words_that_are_no_tree_and_twins():
     assert [x for x, _ in got] == [[0, 1], [], [0, 2], [], [0, 1, 3], [0, 1]]
 
 
+def test_negative_tokens_are_none():
+    """A choice of -1 (of a row of logits without a token) and an empty place of a draft are not a
+    match, as the root's choice, along a chain, and beside a twin that has a token."""
+    p = params(B=4, cap=40)
+    c = filled(p, 6)
+    words = [[1, 3, 7, 15], [1, 3, 5, 11], [1, 3, 7, 15], [1, 3, 5, 9]]
+    draft = torch.tensor([[5, -1, -1, -1], [5, -1, 7, 8], [5, 6, -1, 9], [5, -7, -7, 2]], **I32)
+    chosen = torch.tensor([[-1, -1, -1, -1], [7, 8, -1, 4], [6, -1, 9, 9], [-7, 1, 1, 1]], **I32)
+    old, n = clone(c), torch.tensor([3, 0, 9, 36], **I32)
+    count, path, following, new = focus.tree_accept(p, c, n, draft, chosen, torch.tensor(words, dtype=torch.int64, device="cuda"))
+    assert count.tolist() == [1, 2, 2, 1] and following.tolist() == [-1, -1, -1, -7]
+    assert path.tolist() == [[0, -1, -1, -1], [0, 2, -1, -1], [0, 1, -1, -1], [0, -1, -1, -1]]
+    assert new.tolist() == [4, 2, 11, 37]
+    want = expect(old, [3, 0, 9, 36], [[0], [0, 2], [0, 1], [0]])
+    for x, y in zip(tensors(c), tensors(want)):
+        assert torch.equal(raw(x), raw(y))
+    # a chain whose choices are those of logits without a token
+    logits = torch.randn(4, 4, 50, device="cuda")
+    logits[0, 1], logits[2, 0, 7] = float("nan"), float("inf")
+    chosen, _ = focus.sample(logits, torch.full((4, 4), 0.5, device="cuda"))
+    assert chosen[0, 1] == chosen[2, 0] == -1
+    draft = torch.cat([torch.zeros(4, 1, **I32), chosen[:, :-1]], 1).contiguous()
+    count, _, following, _ = focus.tree_accept(p, c, torch.zeros(4, **I32), draft, chosen)
+    assert count.tolist() == [2, 4, 1, 4] and following.tolist() == [-1, int(chosen[1, 3]), -1, int(chosen[3, 3])]
+
+
 @pytest.mark.parametrize("fmt", ["bf16", "int8"])
 def test_lengths_in_place_and_outside(fmt):
     p = params(B=70, cap=50, format=fmt)
