@@ -163,6 +163,8 @@ CASES = {
     "many": dict(B=1000, T=1, P=700, length=3, d_head=64, top_k=2),
     "sorted_many": dict(B=700, T=3, P=8192, length=4, d_head=64, H=4, H_kv=2, kind="tree"),
     "trees_many_rows_4": dict(B=37, T=5, P=600, length=40, H=32, H_kv=8, kind="tree", w=30, K=8, top_k=2),
+    # sorted, with rows enough for a merge of four heads at a time
+    "sorted_trees_rows_4": dict(B=20, T=8, P=6200, length=60, H=32, H_kv=8, kind="tree", w=300, K=3),
     "none_meet": dict(B=8, T=1, P=500, length=10, K=32, top_k=1, w=3),
 }
 
@@ -184,7 +186,7 @@ def test_matches_the_definition(name, fmt):
 
 
 @pytest.mark.parametrize("fmt", ["bf16", "int8"])
-@pytest.mark.parametrize("name", ["sorted_small", "sorted_runs", "sorted_trees"])
+@pytest.mark.parametrize("name", ["sorted_small", "sorted_runs", "sorted_trees", "sorted_trees_rows_4"])
 def test_masks_of_other_numbers_of_groups(name, fmt):
     """top_k is what the work is planned by: masks of none, of several or of all groups are what is seen."""
     kw = CASES[name]
@@ -230,7 +232,8 @@ def test_agrees_with_decode_tree_behind_a_copied_prefix():
 
 
 @pytest.mark.parametrize("fmt", ["bf16", "e4m3"])
-@pytest.mark.parametrize("name", ["rows_16", "rows_64", "one_run", "trees_many_rows", "trees_many_rows_4", "sorted_runs", "sorted_trees"])
+@pytest.mark.parametrize("name", ["rows_16", "rows_64", "one_run", "trees_many_rows", "trees_many_rows_4", "sorted_runs", "sorted_trees",
+                                  "sorted_trees_rows_4"])
 def test_what_a_row_must_not_see_shows_in_no_result(name, fmt):
     """NaN and infinities in slots behind the prefix, in slots behind the drafted tokens, and in
     prefix keys that only some tokens see."""
@@ -279,6 +282,36 @@ def test_what_a_row_must_not_see_shows_in_no_result(name, fmt):
     assert err <= 2.0 ** -7 * clean.float().abs().max().item()
     live = ~heads & (clean_lse > -math.inf)
     assert (lse[live] - clean_lse[live]).abs().max().item() <= 1e-4
+
+
+@pytest.mark.parametrize("fmt", ["bf16", "e4m3"])
+@pytest.mark.parametrize("name", ["sorted_runs", "sorted_trees", "sorted_trees_rows_4"])
+def test_spoilt_keys_in_the_windows_of_some_of_a_run(name, fmt):
+    """Keys of no group near the prefix's end: of the tokens of one group, which share their tiles, those with
+    short sequences see them in their windows, and the others' rows are worked out again without them."""
+    kw = dict(CASES[name], w=30)
+    p, q, prefix, _, c, lens, words = make(fmt, **kw)
+    P, T = kw["P"], kw["T"]
+    bad = [(P - 29, math.inf), (P - 25, math.nan)]       # what sees the first sees the second
+    for j, _ in bad:
+        prefix.mask[:, :, j] = 0
+    clean, clean_lse = call(p, q, prefix, P, c, lens, words)
+    for j, value in bad:
+        if fmt == "bf16":
+            prefix.k[0, j], prefix.v[0, j] = value, value
+        else:
+            prefix.k_scale[0, :, j], prefix.v_scale[0, :, j] = value, value
+    o, lse = call(p, q, prefix, P, c, lens, words)
+    hit = torch.tensor([[x != 0 and any(P + n + bin(x & (1 << T) - 1).count("1") - 1 - j < p.w for j, _ in bad) for x in words[b]]
+                        for b, n in enumerate(lens)], device="cuda")              # [B, T]
+    live = torch.tensor([[x != 0 for x in w] for w in words], device="cuda")
+    group = torch.stack([c.mask[b, 0, n:n + T] for b, n in enumerate(lens)])
+    assert any(bool((hit & (group == g)).any() and (live & ~hit & (group == g)).any()) for g in (1, 2, 4, 8))
+    assert bool(o[hit].isnan().all()) and bool(lse.transpose(1, 2)[hit].isnan().all())
+    assert bool(o[~hit].isfinite().all())
+    assert (o[~hit].float() - clean[~hit].float()).abs().max().item() <= 2.0 ** -7 * clean.float().abs().max().item()
+    rows = (live & ~hit)[:, None].expand_as(lse)
+    assert (lse[rows] - clean_lse[rows]).abs().max().item() <= 1e-4
 
 
 @pytest.mark.parametrize("fmt", ["e4m3", "int8"])
