@@ -592,6 +592,13 @@ int focus_selftest_timeout(void* ws, size_t ws_bytes, void* stream);
  */
 int focus_selftest_timeout_decode(void* ws, size_t ws_bytes, void* stream);
 
+/*
+ * The same for focus_decode_shared, in eight forms: bf16 and INT8, up to 128 rows per KV head and
+ * more, the arrival kept back in the prefix's kernel or in the own part's, while the other works.
+ *   ws  as above
+ */
+int focus_selftest_timeout_shared(void* ws, size_t ws_bytes, void* stream);
+
 /* Static, human-readable text for a status code. */
 const char* focus_strerror(int code);
 

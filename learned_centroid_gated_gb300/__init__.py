@@ -146,6 +146,8 @@ _lib.focus_selftest_timeout.argtypes = [_P, ctypes.c_size_t, _P]
 _lib.focus_selftest_timeout.restype = ctypes.c_int
 _lib.focus_selftest_timeout_decode.argtypes = [_P, ctypes.c_size_t, _P]
 _lib.focus_selftest_timeout_decode.restype = ctypes.c_int
+_lib.focus_selftest_timeout_shared.argtypes = [_P, ctypes.c_size_t, _P]
+_lib.focus_selftest_timeout_shared.restype = ctypes.c_int
 _lib.focus_get_status.argtypes = [_P, _P]
 _lib.focus_get_status.restype = ctypes.c_int
 _lib.focus_strerror.argtypes = [ctypes.c_int]
@@ -938,6 +940,12 @@ def selftest_timeout_decode(device="cuda", stream=None) -> int:
     and more rows per KV head): -5 where each raised FOCUS_ERR_TIMEOUT and left NaN in every row."""
     ws = torch.empty(16 << 20, dtype=torch.uint8, device=device)
     return _lib.focus_selftest_timeout_decode(_ptr(ws), ws.numel(), _stream(stream))
+
+
+def selftest_timeout_shared(device="cuda", stream=None) -> int:
+    """The same for decode_shared, with the arrival kept back in the prefix's kernel or in the own part's."""
+    ws = torch.empty(16 << 20, dtype=torch.uint8, device=device)
+    return _lib.focus_selftest_timeout_shared(_ptr(ws), ws.numel(), _stream(stream))
 
 
 def get_status(ws: torch.Tensor, stream=None) -> int:

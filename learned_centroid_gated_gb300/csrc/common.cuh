@@ -180,6 +180,9 @@ cudaError_t launch_decode_shared(const focus_cache_params& p, const bf16* q, int
                                  const uint64_t* tree, bf16* o, float* lse, char* ws, float scale, cudaStream_t s);
 size_t tree_selftest_bytes();
 cudaError_t launch_tree_timeout_selftest(char* ws, int format, int T, size_t* o_at, size_t* lse_at, cudaStream_t s);
+constexpr int kSelftestSeqs = 2;
+cudaError_t launch_shared_timeout_selftest(char* ws, int format, int T, bool hold_prefix, size_t* o_at, size_t* lse_at,
+                                           cudaStream_t s);
 // accept.cu
 cudaError_t launch_tree_accept(const focus_cache_params& p, const int32_t* draft, const int32_t* chosen,
                                const uint64_t* tree, void* kc, void* vc, float* ks, float* vs, uint32_t* mask,

@@ -973,6 +973,24 @@ int focus_selftest_timeout(void* ws, size_t ws_bytes, void* stream) {
   return focus_get_status(ws, stream);
 }
 
+// The status of a self-test's call, if all its rows (of up to FOCUS_MAX_DRAFT tokens, 4 heads of 128) are NaN.
+static int timed_out_to_nan(const char* w, size_t o_at, size_t lse_at, int tokens, cudaStream_t s) {
+  const int rc = focus_get_status(w, s);
+  if (rc != FOCUS_ERR_TIMEOUT) return rc;
+  uint16_t o[FOCUS_MAX_DRAFT * 4 * 128];
+  float lse[FOCUS_MAX_DRAFT * 4];
+  const size_t n = (size_t)tokens * 4;
+  if (cudaMemcpyAsync(o, w + o_at, n * 128 * 2, cudaMemcpyDeviceToHost, s) != cudaSuccess ||
+      cudaMemcpyAsync(lse, w + lse_at, n * 4, cudaMemcpyDeviceToHost, s) != cudaSuccess ||
+      cudaStreamSynchronize(s) != cudaSuccess)
+    return FOCUS_ERR_CUDA;
+  for (size_t i = 0; i < n * 128; ++i)
+    if ((o[i] & 0x7fffu) <= 0x7f80u) return FOCUS_OK;  // a number in place of a NaN
+  for (size_t i = 0; i < n; ++i)
+    if (lse[i] == lse[i]) return FOCUS_OK;
+  return rc;
+}
+
 int focus_selftest_timeout_decode(void* ws, size_t ws_bytes, void* stream) {
   if (!ws) return FOCUS_ERR_INVALID_ARG;
   if (!aligned(ws, 256)) return FOCUS_ERR_ALIGNMENT;
@@ -984,19 +1002,25 @@ int focus_selftest_timeout_decode(void* ws, size_t ws_bytes, void* stream) {
       size_t o_at, lse_at;
       int rc = cuda_rc(launch_tree_timeout_selftest(w, format, T, &o_at, &lse_at, s));
       if (rc) return rc;
-      if ((rc = focus_get_status(ws, stream)) != FOCUS_ERR_TIMEOUT) return rc;
-      uint16_t o[FOCUS_MAX_DRAFT * 4 * 128];
-      float lse[FOCUS_MAX_DRAFT * 4];
-      const size_t n = (size_t)T * 4;
-      if (cudaMemcpyAsync(o, w + o_at, n * 128 * 2, cudaMemcpyDeviceToHost, s) != cudaSuccess ||
-          cudaMemcpyAsync(lse, w + lse_at, n * 4, cudaMemcpyDeviceToHost, s) != cudaSuccess ||
-          cudaStreamSynchronize(s) != cudaSuccess)
-        return FOCUS_ERR_CUDA;
-      for (size_t i = 0; i < n * 128; ++i)
-        if ((o[i] & 0x7fffu) <= 0x7f80u) return FOCUS_OK;  // a number in place of a NaN
-      for (size_t i = 0; i < n; ++i)
-        if (lse[i] == lse[i]) return FOCUS_OK;
+      if ((rc = timed_out_to_nan(w, o_at, lse_at, T, s)) != FOCUS_ERR_TIMEOUT) return rc;
     }
+  return FOCUS_ERR_TIMEOUT;
+}
+
+int focus_selftest_timeout_shared(void* ws, size_t ws_bytes, void* stream) {
+  if (!ws) return FOCUS_ERR_INVALID_ARG;
+  if (!aligned(ws, 256)) return FOCUS_ERR_ALIGNMENT;
+  if (ws_bytes < tree_selftest_bytes()) return FOCUS_ERR_WORKSPACE;
+  cudaStream_t s = (cudaStream_t)stream;
+  char* w = (char*)ws;
+  for (int format : {FOCUS_CACHE_BF16, FOCUS_CACHE_INT8})
+    for (int T : {9, FOCUS_MAX_DRAFT / kSelftestSeqs})
+      for (bool prefix : {true, false}) {
+        size_t o_at, lse_at;
+        int rc = cuda_rc(launch_shared_timeout_selftest(w, format, T, prefix, &o_at, &lse_at, s));
+        if (rc) return rc;
+        if ((rc = timed_out_to_nan(w, o_at, lse_at, kSelftestSeqs * T, s)) != FOCUS_ERR_TIMEOUT) return rc;
+      }
   return FOCUS_ERR_TIMEOUT;
 }
 

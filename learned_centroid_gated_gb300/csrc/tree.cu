@@ -1422,9 +1422,53 @@ cudaError_t launch_tree_timeout_selftest(char* ws, int format, int T, size_t* o_
                        reinterpret_cast<int32_t*>(ws + lens), nullptr, reinterpret_cast<bf16*>(ws + *o_at),
                        reinterpret_cast<float*>(ws + *lse_at), ws, 0.1f);
   a.G = 1;
-  if ((e = launch_tree_tc_held(a, format, s)) != cudaSuccess) return e;
+  if ((e = launch_tree_tc_held(a, format, false, s)) != cudaSuccess) return e;
   return format == FOCUS_CACHE_BF16 ? launch_merge<128, FOCUS_CACHE_BF16, false>(a, a, s)
                                     : launch_merge<128, FOCUS_CACHE_INT8, false>(a, a, s);
+}
+
+// The same over a prefix of 1024 tokens, kSelftestSeqs sequences with 1024 of their own: the prefix's kernel
+// or the own part's is the held one, the other works as always beside it; the merge reads both kernels' flags.
+cudaError_t launch_shared_timeout_selftest(char* ws, int format, int T, bool hold_prefix, size_t* o_at, size_t* lse_at,
+                                           cudaStream_t s) {
+  focus_cache_params p{};
+  p.B = kSelftestSeqs, p.cap = 2048, p.T = T, p.H = 4, p.H_kv = 1, p.d_head = 128;
+  p.R = 1, p.K = 1, p.top_k = 1, p.w = 1 << 20, p.format = format;
+  constexpr int kPrefix = 1024;
+  focus_cache_params run = p;
+  run.B = 1, run.T = p.B * T, run.cap = kPrefix;
+  const TreePlan own_plan = tree_plan(p, true), plan = tree_plan(run, true);
+  size_t at = align_up(own_plan.total, 256) + align_up(plan.total, 256);
+  auto take = [&](size_t bytes) {
+    const size_t x = at;
+    at += align_up(bytes, 256);
+    return x;
+  };
+  const size_t kv = (size_t)p.cap * p.d_head * 2, rows = (size_t)p.B * T * p.H;
+  const size_t q = take(rows * p.d_head * 2), k = take(p.B * kv), v = take(p.B * kv), ks = take(p.B * p.cap * 4), vs = take(p.B * p.cap * 4);
+  const size_t mask = take(p.B * p.cap * 4), lens = take(p.B * 4);
+  *o_at = take(rows * p.d_head * 2), *lse_at = take(rows * 4);
+  if (run.T > FOCUS_MAX_DRAFT || at > tree_selftest_bytes()) return cudaErrorInvalidValue;
+  cudaError_t e = cudaMemsetAsync(ws, 0, at, s);
+  for (int b = 0; b < p.B && e == cudaSuccess; ++b) e = cudaMemsetAsync(ws + lens + 4 * b + 1, 4, 1, s);
+  if (e != cudaSuccess) return e;
+  auto args = [&](const focus_cache_params& x, const TreePlan& t, size_t from) {  // (the prefix: the first sequence's cache)
+    const bool scales = format != FOCUS_CACHE_BF16;
+    return args_of(x, t, reinterpret_cast<bf16*>(ws + q), ws + k, ws + v, scales ? reinterpret_cast<float*>(ws + ks) : nullptr,
+                   scales ? reinterpret_cast<float*>(ws + vs) : nullptr, reinterpret_cast<uint32_t*>(ws + mask),
+                   reinterpret_cast<int32_t*>(ws + lens), nullptr, reinterpret_cast<bf16*>(ws + *o_at),
+                   reinterpret_cast<float*>(ws + *lse_at), ws + from, 0.1f);
+  };
+  TreeArgs own = args(p, own_plan, 0), pre = args(run, plan, align_up(own_plan.total, 256));
+  pre.status = own.status, pre.per = T;
+  pre.own_mask = own.mask, pre.own_cap = p.cap, pre.plen = kPrefix, pre.tokens = p.B * T;
+  (hold_prefix ? pre : own).G = 1;
+  e = hold_prefix ? launch_tree_tc(own, 128, format, false, s) : launch_tree_tc_held(own, format, false, s);
+  if (e != cudaSuccess) return e;
+  e = hold_prefix ? launch_tree_tc_held(pre, format, true, s) : launch_tree_tc(pre, 128, format, true, s);
+  if (e != cudaSuccess) return e;
+  return format == FOCUS_CACHE_BF16 ? launch_merge<128, FOCUS_CACHE_BF16, true>(pre, own, s)
+                                    : launch_merge<128, FOCUS_CACHE_INT8, true>(pre, own, s);
 }
 
 }  // namespace focus

@@ -1124,7 +1124,7 @@ bool make_map(CUtensorMap* m, const void* base, const TreeArgs& a, int caches, i
             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-template <int D, int FMT, int NT, bool HOLD, bool PRE = false>
+template <int D, int FMT, int NT, bool HOLD, bool PRE>
 cudaError_t launch(TreeArgs a, cudaStream_t s) {
   using L = Tc<D, FMT, NT, PRE>;
   static std::atomic<uint64_t> done{0};
@@ -1174,10 +1174,19 @@ cudaError_t launch_tree_tc(const TreeArgs& a, int d_head, int format, bool prefi
   return prefix ? launch_for<true>(a, d_head, format, s) : launch_for<false>(a, d_head, format, s);
 }
 
-cudaError_t launch_tree_tc_held(const TreeArgs& a, int format, cudaStream_t s) {
+namespace {
+
+template <bool PRE>
+cudaError_t launch_held(const TreeArgs& a, int format, cudaStream_t s) {
   constexpr int B = FOCUS_CACHE_BF16, I = FOCUS_CACHE_INT8;
-  if (format == B) return a.grp == kRows ? launch<128, B, 1, true>(a, s) : launch<128, B, 2, true>(a, s);
-  return a.grp == kRows ? launch<128, I, 1, true>(a, s) : launch<128, I, 2, true>(a, s);
+  if (format == B) return a.grp == kRows ? launch<128, B, 1, true, PRE>(a, s) : launch<128, B, 2, true, PRE>(a, s);
+  return a.grp == kRows ? launch<128, I, 1, true, PRE>(a, s) : launch<128, I, 2, true, PRE>(a, s);
+}
+
+}  // namespace
+
+cudaError_t launch_tree_tc_held(const TreeArgs& a, int format, bool prefix, cudaStream_t s) {
+  return prefix ? launch_held<true>(a, format, s) : launch_held<false>(a, format, s);
 }
 
 }  // namespace focus

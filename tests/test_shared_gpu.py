@@ -373,6 +373,17 @@ def test_graph_with_growing_sequences_and_streams(name):
     assert all(torch.equal(x, want) and torch.equal(y, want_lse) for x, y in got)
 
 
+def test_a_part_that_times_out_leaves_nan_and_a_usable_context():
+    """The prefix's kernel or the own part's with one arrival kept back: its waits run out, and every row
+    has a part in it and is NaN, whatever the other kernel left.  The next call is right."""
+    p, q, prefix, _, c, lens, words = make("bf16", **CASES["rows_64"])
+    want, want_lse = call(p, q, prefix, 7000, c, lens)
+    for _ in range(2):
+        assert focus.ERRORS[focus.selftest_timeout_shared()] == "FOCUS_ERR_TIMEOUT"
+    o, lse = call(p, q, prefix, 7000, c, lens)
+    assert torch.equal(o, want) and torch.equal(lse, want_lse)
+
+
 def test_prefix_behind_four_gigabytes():
     P, H_kv = 2300000, 8
     p = params(B=3, cap=8, H=32, H_kv=H_kv, w=300, K=32, top_k=1)
