@@ -131,7 +131,7 @@ tree_split(const __grid_constant__ TreeArgs a) {
       const int x = rg * NR + (on ? r : 0), t = x / a.gq, h = kvh * a.gq + x % a.gq;
       int64_t token = (int64_t)b * a.T + t;
       if constexpr (PRE) {
-        const Drafted<PRE> tok(a, b, t);
+        const Drafted tok(a, b, t);
         on = on && tok.some;
         token = tok.x;
         word[e] = on ? tok.word : 0ull;
@@ -611,7 +611,7 @@ __device__ __forceinline__ RowParts<PRE> row_parts(const TreeArgs& a, int b, int
   r.whole = total * a.H_kv * a.nrg;
   r.ns = slices_of<PRE>(a, r.whole);
   bool live = r.s.units > 0;
-  if constexpr (PRE) live = live && Drafted<PRE>(a, b, t).word != 0ull;
+  if constexpr (PRE) live = live && Drafted(a, b, t).word != 0ull;
   else live = live && tree_word(a, b, t) != 0ull;
   r.part = quotient(r.whole, r.ns);  // a slice is `part` weights or one more
   r.first = live ? (int)max((int64_t)0, quotient(r.from, r.part + 1) - 1) : 0;
@@ -703,7 +703,7 @@ __device__ float keys_by_hand(const TreeArgs& a, const RowParts<PRE>& rp, int t,
   uint32_t mrow;
   int64_t token = (int64_t)b * a.T + t;
   if constexpr (PRE) {
-    const Drafted<PRE> tok(a, b, t);
+    const Drafted tok(a, b, t);
     word = tok.word, near = tok.near(a), mrow = tok.groups(a, rho), token = tok.x;
   } else {
     word = tree_word(a, b, t);
@@ -1251,7 +1251,7 @@ __global__ void __launch_bounds__(kSortThreads) sort_tokens(const __grid_constan
   int4 entry;  // of the token looked at last
   int known = -1;
   auto group_of = [&](int x) {  // 32: no token
-    const Drafted<true> tok(a, x / a.T, x % a.T);  // (a.order is not set here: as they stand)
+    const Drafted tok(a, x / a.T, x % a.T);  // (a.order is not set here: as they stand)
     known = x;
     if (!tok.word) return 32;
     const uint32_t m = tok.groups(a, 0);

@@ -35,7 +35,7 @@ struct TreeArgs {
   int tma;           // tensor-core kernel: tensor maps are there
   float sl2;         // softmax scale * log2(e)
   int per;           // drafted tokens of a sequence
-  // A batch behind one prefix (kPrefix): kc .. mask, cap are the prefix's, `plen` tokens of it; the
+  // A batch behind one prefix (PRE): kc .. mask, cap are the prefix's, `plen` tokens of it; the
   // `tokens` drafted tokens of all sequences stand in one row, cut into B runs of T that count as
   // sequences, each over the whole prefix.
   const uint32_t* own_mask;
@@ -202,19 +202,15 @@ __device__ __forceinline__ uint64_t tree_word(const TreeArgs& a, int b, int t) {
          all;
 }
 
-// Token i of sequence `run` (or run of a batch behind a prefix): its word, not zero where it is one, its
-// number in the batch's row (0 where there is none), its window and groups.
-template <bool PRE>
+// Token i of a run of a batch behind a prefix: its word, not zero where it is one, its number in the batch's
+// row (0 where there is none), its window and groups.
 struct Drafted {
   uint64_t word;
   int x;
   bool some;  // a token of the batch, whether its sequence's length fits or not
   __device__ __forceinline__ Drafted(const TreeArgs& a, int run, int i) {
-    x = run * a.T + i, some = true;
-    if constexpr (!PRE) {
-      b = run, t = i, len = __ldg(a.lens + run);
-      word = tree_word(a, run, i);
-    } else if (a.order) {
+    x = run * a.T + i;
+    if (a.order) {
       at = __ldg(a.order + x);  // (one load for a row's start in place of four that wait for each other)
       some = at.x >= 0;
       word = some ? 1ull : 0ull;
@@ -233,13 +229,10 @@ struct Drafted {
     }
   }
   __device__ __forceinline__ int near(const TreeArgs& a) const {  // first position inside its window
-    if (PRE && a.order) return at.y;
-    return (PRE ? a.plen : 0) + len + __popcll(word) - a.w;
+    return a.order ? at.y : a.plen + len + __popcll(word) - a.w;
   }
   __device__ __forceinline__ uint32_t groups(const TreeArgs& a, int rho) const {
-    if (PRE && a.order) return (uint32_t)at.z;
-    return PRE ? __ldg(a.own_mask + ((int64_t)b * a.R + rho) * a.own_cap + len + t)
-               : __ldg(a.mask + ((int64_t)b * a.R + rho) * a.cap + len + t);
+    return a.order ? (uint32_t)at.z : __ldg(a.own_mask + ((int64_t)b * a.R + rho) * a.own_cap + len + t);
   }
 
  private:

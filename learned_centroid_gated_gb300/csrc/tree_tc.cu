@@ -280,7 +280,7 @@ tree_tc(const __grid_constant__ TreeArgs a, const __grid_constant__ CUtensorMap 
         const int x = row0 + (on ? y : 0), h = kvh * a.gq + x % a.gq;
         int64_t token = (int64_t)b * a.T + x / a.gq;
         if constexpr (PRE) {
-          const Drafted<PRE> tok(a, b, x / a.gq);
+          const Drafted tok(a, b, x / a.gq);
           on = on && tok.some;
           token = tok.x;
         }
@@ -321,7 +321,7 @@ tree_tc(const __grid_constant__ TreeArgs a, const __grid_constant__ CUtensorMap 
       int nearest = INT_MAX;
       for (int i = lane; i < ntok; i += 32) {
         if constexpr (PRE) {
-          const Drafted<PRE> tok(a, b, tok0 + i);
+          const Drafted tok(a, b, tok0 + i);
           if (tok.word) {
             many |= tok.groups(a, rho);
             nearest = min(nearest, tok.near(a));
@@ -723,7 +723,7 @@ tree_tc(const __grid_constant__ TreeArgs a, const __grid_constant__ CUtensorMap 
         for (int e = 0; e < 2; ++e) {
           const int i = 32 * e + lane;
           if constexpr (PRE) {
-            const Drafted<PRE> tok(a, b, tok0 + (i < ntok ? i : 0));
+            const Drafted tok(a, b, tok0 + (i < ntok ? i : 0));
             word[e] = i < ntok ? tok.word : 0ull;
             grp[e] = word[e] ? tok.groups(a, rho) : 0u;
             near[e] = word[e] ? tok.near(a) : INT_MAX;
@@ -858,7 +858,7 @@ tree_tc(const __grid_constant__ TreeArgs a, const __grid_constant__ CUtensorMap 
       const bool on = x < a.rows;
       const int tt = min(x, a.rows - 1) / a.gq, ti = tt - row0 / a.gq;  // token; its place in the row group
       bool alive = on;
-      if constexpr (PRE) alive = alive && Drafted<PRE>(a, b, tt).word != 0ull;
+      if constexpr (PRE) alive = alive && Drafted(a, b, tt).word != 0ull;
       else alive = alive && tree_word(a, b, tt) != 0ull;
       // a row that is no token sees nothing: its reference need not be looked for
       // 8-bit formats: m is the reference of O, that is of P times V's scale; the sum l has one of
