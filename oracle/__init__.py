@@ -38,7 +38,7 @@ def build(force: bool = False) -> str:
     with _lock:
         if force or not os.path.exists(_LIB_PATH) or os.path.getmtime(_LIB_PATH) < os.path.getmtime(_SRC):
             tmp = _LIB_PATH + f".tmp{os.getpid()}"
-            subprocess.check_call(["gcc", "-O2", "-std=c11", "-ffp-contract=off", "-fPIC", "-shared",
+            subprocess.check_call(["gcc", "-O3", "-std=c11", "-ffp-contract=off", "-fPIC", "-shared",
                                    "-pthread", _SRC, "-o", tmp, "-lm"])
             os.replace(tmp, _LIB_PATH)
     return _LIB_PATH
@@ -76,7 +76,7 @@ def compile_variant(source: str, out_path: str) -> str:
     src_path = out_path[:-3] + ".c" if out_path.endswith(".so") else out_path + ".c"
     with open(src_path, "w") as f:
         f.write(source)
-    subprocess.check_call(["gcc", "-O2", "-std=c11", "-ffp-contract=off", "-fPIC", "-shared",
+    subprocess.check_call(["gcc", "-O3", "-std=c11", "-ffp-contract=off", "-fPIC", "-shared",
                            "-pthread", src_path, "-o", out_path, "-lm"])
     return out_path
 

@@ -215,30 +215,65 @@ static void attn_row(const attn_job* J, int64_t out_row, int64_t bi, int hs, dou
   const uint16_t* qi = J->q + (((int64_t)b * J->N + i) * J->H + h) * d;
   for (int t = 0; t < d; ++t) qv[t] = bf16_to_double(qi[t]);
 
-  /* logits over the attended set */
+  /* the attended set */
   int64_t n = 0;
-  double mx = -INFINITY;
-  for (int64_t j = 0; j <= i; ++j) {
-    if (!allowed(i, j, J->w, m[i], m[j])) continue;
-    const uint16_t* kj = J->k + (((int64_t)b * J->N + j) * J->H_kv + kvh) * d;
-    double s = 0.0;
-    for (int t = 0; t < d; ++t) s += qv[t] * bf16_to_double(kj[t]);
-    s *= J->scale;
-    s_buf[n] = s;
-    j_buf[n] = j;
-    if (s > mx) mx = s;
-    ++n;
-  }
+  for (int64_t j = 0; j <= i; ++j)
+    if (allowed(i, j, J->w, m[i], m[j])) j_buf[n++] = j;
   /* the diagonal is always in the window, so n >= 1 */
+
+  /* logits; the sums of four keys go side by side, each in the order of its terms (one key after
+   * another waits for every addition; the last key stands in for those behind it), the products of
+   * 16 terms before their sums */
+  double mx = -INFINITY;
+  for (int64_t a0 = 0; a0 < n; a0 += 4) {
+    const uint16_t* kj[4];
+    for (int e = 0; e < 4; ++e)
+      kj[e] = J->k + (((int64_t)b * J->N + j_buf[a0 + e < n ? a0 + e : n - 1]) * J->H_kv + kvh) * d;
+    double s0 = 0.0, s1 = 0.0, s2 = 0.0, s3 = 0.0;
+    int t = 0;
+    for (; t + 16 <= d; t += 16) {
+      double x[4][16];
+      for (int e = 0; e < 4; ++e)
+        for (int c = 0; c < 16; ++c) x[e][c] = qv[t + c] * bf16_to_double(kj[e][t + c]);
+      for (int c = 0; c < 16; ++c) s0 += x[0][c], s1 += x[1][c], s2 += x[2][c], s3 += x[3][c];
+    }
+    for (; t < d; ++t) {
+      s0 += qv[t] * bf16_to_double(kj[0][t]);
+      s1 += qv[t] * bf16_to_double(kj[1][t]);
+      s2 += qv[t] * bf16_to_double(kj[2][t]);
+      s3 += qv[t] * bf16_to_double(kj[3][t]);
+    }
+    const double s4[4] = {s0, s1, s2, s3};
+    for (int e = 0; e < 4 && a0 + e < n; ++e) {
+      double s = s4[e];
+      s *= J->scale;
+      s_buf[a0 + e] = s;
+      if (s > mx) mx = s;
+    }
+  }
   double sum = 0.0;
   for (int64_t a = 0; a < n; ++a) sum += exp(s_buf[a] - mx);
   const double lse = mx + log(sum);
   double* o = J->o + (out_row * J->n_heads + hs) * d;
   for (int t = 0; t < d; ++t) o[t] = 0.0;
-  for (int64_t a = 0; a < n; ++a) {
-    const double p = exp(s_buf[a] - lse);
-    const uint16_t* vj = J->v + (((int64_t)b * J->N + j_buf[a]) * J->H_kv + kvh) * d;
-    for (int t = 0; t < d; ++t) o[t] += p * bf16_to_double(vj[t]);
+  /* four keys at a time, added in their order */
+  for (int64_t a0 = 0; a0 < n; a0 += 4) {
+    double p4[4];
+    const uint16_t* v4[4];
+    const int m4 = n - a0 < 4 ? (int)(n - a0) : 4;
+    for (int e = 0; e < m4; ++e) {
+      const int64_t a = a0 + e;
+      const uint16_t* vj = J->v + (((int64_t)b * J->N + j_buf[a]) * J->H_kv + kvh) * d;
+      p4[e] = exp(s_buf[a] - lse);
+      v4[e] = vj;
+    }
+    if (m4 == 4)
+      for (int t = 0; t < d; ++t)
+        o[t] = o[t] + p4[0] * bf16_to_double(v4[0][t]) + p4[1] * bf16_to_double(v4[1][t]) +
+               p4[2] * bf16_to_double(v4[2][t]) + p4[3] * bf16_to_double(v4[3][t]);
+    else
+      for (int e = 0; e < m4; ++e)
+        for (int t = 0; t < d; ++t) o[t] += p4[e] * bf16_to_double(v4[e][t]);
   }
   J->lse[out_row * J->n_heads + hs] = lse;
 }
