@@ -95,7 +95,8 @@ __global__ void __launch_bounds__(kAcceptThreads) accept_path(const __grid_const
   __syncthreads();
   if (tid < FOCUS_MAX_DRAFT) {
     const uint64_t right = (uint64_t)bits[1][1] << 32 | bits[1][0];
-    const unsigned w = __ballot_sync(0xffffffffu, word != 0ull && (word & ~right) == 0ull);
+    // (a word need not have its own token's bit, where it is of no tree)
+    const unsigned w = __ballot_sync(0xffffffffu, (right >> tid & 1ull) != 0ull && (word & ~right) == 0ull);
     if (lane == 0) bits[2][wp] = w;
   }
   __syncthreads();

@@ -109,6 +109,20 @@ def test_words_that_are_no_tree_and_twins():
     assert [x for x, _ in got] == [[0, 1], [], [0, 2], [], [0, 1, 3], [0, 1]]
 
 
+@pytest.mark.parametrize("T", [2, 3, 8, 33, 64])
+def test_words_at_random(T):
+    """Words without their own bit, with later ones', copied from other tokens: none of them is accepted."""
+    r = random.Random(T)
+    B = 200
+    p = params(B=B, cap=T + 9)
+    words = [ref.random_tree(r, T, reach=r.choice([1, 2, 64])) for _ in range(B)]
+    for w in words:
+        for _ in range(r.randrange(4)):
+            w[r.randrange(T)] = r.choice([r.getrandbits(T), w[r.randrange(T)], w[r.randrange(T)] | 1 << r.randrange(T), 0])
+    pick = lambda: torch.tensor([[r.randrange(2) for _ in range(T)] for _ in range(B)], **I32)  # noqa: E731
+    check(p, filled(p, 8), [r.randrange(10) for _ in range(B)], words, pick(), pick())
+
+
 def test_negative_tokens_are_none():
     """A choice of -1 (of a row of logits without a token) and an empty place of a draft are not a
     match, as the root's choice, along a chain, and beside a twin that has a token."""
