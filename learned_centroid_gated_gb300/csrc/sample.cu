@@ -22,7 +22,7 @@
 //
 // Measured: one row of 32000 with top_k and top_p 12.4 us (27 before the few went to one block, most of it
 // fetching instructions that run once); 64 rows of 100003, top_p 62 us; 512 rows of 131072 bf16, no
-// limits, 133 us, of which the memory needs 20: 38 instructions a token, at 55% of the issue slots;
+// limits, 129 us, of which the memory needs 20: 39 instructions a token, at 57% of the issue slots;
 // 143 fp32 rows of 69235, the largest of each, 12.4 us (6 for the memory).  In between it is the
 // steps' dependent latencies, some 2000 cycles each for a meeting of the blocks and a sum.
 #include <cooperative_groups.h>

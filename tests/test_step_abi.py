@@ -82,6 +82,13 @@ def test_shared_argument_errors():
     assert size(ctypes.byref(_cp()), 50) > focus._lib.focus_decode_tree_workspace_size(ctypes.byref(_cp()))
 
 
+@host_only
+def test_selftest_argument_errors():
+    selftest = focus._lib.focus_selftest_timeout_shared
+    for ws, size, want in ((None, 1 << 24, "INVALID_ARG"), (P((1 << 36) + 64), 1 << 24, "ALIGNMENT"), (at(0), (1 << 24) - 1, "WORKSPACE")):
+        assert selftest(ws, size, None) == E["FOCUS_ERR_" + want]
+
+
 def _accept(p, draft=at(0), chosen=at(1), tree=None, kc=at(2), vc=at(3), ks=None, vs=None, mc=at(4), lens=at(5), lens_out=at(6),
             count=at(7), path=at(8), following=at(9), status=None):
     return focus._lib.focus_tree_accept(ctypes.byref(p), draft, chosen, tree, kc, vc, ks, vs, mc, lens, lens_out, count, path,
